@@ -347,6 +347,136 @@ s4dplr_status s4dplr_block_forward(const s4dplr_plan* plan, const float* x, cons
 /* Release a plan (NULL is ignored).  Host-only. */
 void s4dplr_plan_destroy(s4dplr_plan* plan);
 
+/* ------------------------------------------------------------------------
+ * Operators of a token-major sequence block: the gated delta rule (a linear
+ * recurrence over a dk x dv matrix state, next to the recurrent view above)
+ * and the layer norm with its gradients.  Unlike the entry points above they
+ * take three element types, any sizes, and buffers that are aligned to their
+ * own elements only (ERR_ALIGN otherwise); arithmetic and carried values are
+ * fp32, and each output is rounded once.
+ * ---------------------------------------------------------------------- */
+
+typedef enum s4dplr_dtype { S4DPLR_F32 = 0, S4DPLR_BF16 = 1, S4DPLR_F16 = 2 } s4dplr_dtype;
+
+/*
+ * Layer norm over the middle axis of x [outer][D][inner] (contiguous):
+ *   m = mean_d x,  r = 1 / sqrt(mean_d (x - m)^2 + eps),  y = (x - m) r gamma_d + beta_d.
+ * inner = 1 normalizes rows of D contiguous values (tokens); outer = batch,
+ * D = H, inner = L is the normalization of s4dplr_block_forward.
+ *   x, y       : elements of `dtype`; y may be x itself, else must not overlap it.
+ *   gamma, beta: [D] float32, each may be NULL (1 and 0).
+ *   mean, rstd : [outer][inner] float32, the m and r that s4dplr_layer_norm_bwd
+ *                reads; each may be NULL (not written).
+ * outer = 0 is a no-op.  Limits: outer >= 0, 1 <= D <= 32768, inner >= 1,
+ * outer * inner < 2^31, eps >= 0 (ERR_SHAPE).
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS (an output overlaps an
+ * input or another output), ERR_UNSUPPORTED (dtype), ERR_HIP.
+ */
+s4dplr_status s4dplr_layer_norm_fwd(const void* x, const float* gamma, const float* beta, void* y,
+                                    float* mean, float* rstd, long outer, long D, long inner,
+                                    float eps, int dtype, hipStream_t stream);
+
+/* Bytes of workspace of s4dplr_layer_norm_bwd (partial sums of dgamma and
+ * dbeta).  Errors: ERR_NULL, ERR_SHAPE. */
+s4dplr_status s4dplr_layer_norm_workspace_bytes(long outer, long D, long inner, size_t* bytes);
+
+/*
+ * Gradients of s4dplr_layer_norm_fwd from dy = dloss/dy, with xh = (x - mean) rstd
+ * and w = dy gamma:
+ *   dx = rstd (w - mean_d w - xh mean_d (w xh)),
+ *   dgamma_d = sum dy xh,  dbeta_d = sum dy   over outer and inner.
+ * x, dy, dx: elements of `dtype`; gamma may be NULL (1); mean and rstd as the
+ * forward pass wrote them; dgamma, dbeta: [D] float32.  Any output may be NULL
+ * (not computed); outputs are overwritten, not accumulated, and must not overlap
+ * an input, each other or the workspace.  The sums are taken in a fixed order:
+ * equal calls give equal bits.  outer = 0 writes dgamma = dbeta = 0.
+ * Limits and errors as above, and ERR_WORKSPACE (ws not 256-byte aligned).
+ */
+s4dplr_status s4dplr_layer_norm_bwd(const void* x, const float* gamma, const float* mean,
+                                    const float* rstd, const void* dy, void* dx, float* dgamma,
+                                    float* dbeta, long outer, long D, long inner, int dtype,
+                                    void* ws, hipStream_t stream);
+
+/*
+ * Gated delta rule.  Per sequence and value head h, with the key head h Hk / Hv,
+ * a_t = exp(g_t) and the dk x dv state S (fp32):
+ *   n_t = v_t - a_t S^T k_t,   S <- a_t S + beta_t k_t n_t^T,   o_t = scale S^T q_t.
+ * Sequences are packed in rows: q, k [tokens][Hk][dk], v, o [tokens][Hv][dv],
+ * g, beta [tokens][Hv] float32.  With offsets (device, int32 [sequences + 1],
+ * ascending from 0 or more to tokens or less) sequence s has the rows
+ * offsets[s] .. offsets[s + 1]; rows outside every sequence are not read and
+ * their outputs not written.  Without (NULL), every sequence has
+ * tokens / sequences rows.  Sequences may be empty: their state is passed on.
+ * Offsets out of range or order give unspecified results, and no access outside
+ * the buffers.
+ *
+ * Preconditions not checked on the device: finite values, g <= 0 (g = -infinity
+ * is a reset: nothing of the state is kept), and keys of norm about 1 or less
+ * with 0 <= beta <= 1, for which the recurrence does not grow.
+ */
+typedef struct s4dplr_delta_plan s4dplr_delta_plan;
+
+/* Plan flag: reserve what the backward pass needs. */
+#define S4DPLR_DELTA_TRAINING 1u
+
+/*
+ * Plan for `sequences` sequences of together `tokens` rows.  Host-only.
+ * Limits: sequences >= 1, 0 <= tokens < 2^31, 1 <= dk, dv <= 256, Hk >= 1, Hv a
+ * multiple of Hk up to 65535, sequences * Hv <= 2^24 (ERR_SHAPE).  Errors:
+ * ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED (dtype, flags).  A plan is immutable
+ * and may be used from several threads and streams, each with its own workspace.
+ */
+s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, long tokens,
+                                       int Hk, int Hv, int dk, int dv, int dtype, unsigned flags);
+
+/* Bytes of workspace, and of the buffer `saved` that the forward pass of a
+ * training plan fills for the backward pass (0 without the flag; may be NULL).
+ * The workspace holds nothing between calls.  Errors: ERR_NULL. */
+s4dplr_status s4dplr_delta_plan_bytes(const s4dplr_delta_plan* plan, size_t* workspace,
+                                      size_t* saved);
+
+/*
+ * Forward pass.  ldq, ldk, ldv: elements from one row of q, k, v to the next (at
+ * least Hk dk, Hk dk, Hv dv), so the three may be column ranges of one matrix; o
+ * is contiguous.  state: [sequences][Hv][dk][dv] float32, the states before the
+ * first rows, NULL for zeros; state_out: the states after the last rows, may be
+ * NULL (not written) or `state` itself.  saved: NULL, or (plans with
+ * S4DPLR_DELTA_TRAINING) the buffer for s4dplr_delta_bwd, 256-byte aligned.
+ * Short sequences are taken token by token in one launch, longer ones by chunks
+ * of 64 tokens on the matrix cores; with `saved`, all of them by chunks.  Both
+ * compute the same recurrence.  tokens = 0 passes the states on.
+ * Errors: ERR_NULL, ERR_SHAPE (a row pitch; without offsets, tokens not a
+ * multiple of sequences), ERR_ALIGN, ERR_ALIAS (an output overlaps an input,
+ * another output or the workspace), ERR_WORKSPACE (ws or saved not 256-byte
+ * aligned), ERR_UNSUPPORTED (saved without the flag), ERR_HIP.
+ */
+s4dplr_status s4dplr_delta_fwd(const s4dplr_delta_plan* plan, const void* q, long ldq,
+                               const void* k, long ldk, const void* v, long ldv, const float* g,
+                               const float* beta, const int* offsets, float scale,
+                               const float* state, void* o, float* state_out, void* saved,
+                               void* ws, hipStream_t stream);
+
+/*
+ * Gradients of s4dplr_delta_fwd with the same inputs and the buffer it filled:
+ * from dout = dloss/do [tokens][Hv][dv] (contiguous) and dstate_out =
+ * dloss/dstate_out (NULL for zeros) to dq, dk [tokens][Hk][dk], dv
+ * [tokens][Hv][dv] (contiguous, elements of the plan's dtype), dg, dbeta
+ * [tokens][Hv] and dstate [sequences][Hv][dk][dv] (float32; dstate may be
+ * dstate_out itself).  Any output may be NULL (not written); outputs are
+ * overwritten, not accumulated.  Gradients of shared key heads are summed over
+ * their value heads in a fixed order: equal calls give equal bits.  `saved` is
+ * only read.  Errors as for s4dplr_delta_fwd.
+ */
+s4dplr_status s4dplr_delta_bwd(const s4dplr_delta_plan* plan, const void* q, long ldq,
+                               const void* k, long ldk, const void* v, long ldv, const float* g,
+                               const float* beta, const int* offsets, float scale,
+                               const void* saved, const void* dout, const float* dstate_out,
+                               void* dq, void* dk, void* dv, float* dg, float* dbeta,
+                               float* dstate, void* ws, hipStream_t stream);
+
+/* Release a plan (NULL is ignored).  Host-only. */
+void s4dplr_delta_plan_destroy(s4dplr_delta_plan* plan);
+
 #ifdef __cplusplus
 }
 #endif

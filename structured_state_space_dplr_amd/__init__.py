@@ -16,6 +16,12 @@ before the call when the environment variable ``S4DPLR_VALIDATE`` is ``1``;
 a violation raises ``S4DPLRPreconditionError``.  The check copies the
 inputs to host memory and synchronizes, so it is for debugging, not for the
 timed path.
+
+The token-major operators (``layer_norm_fwd`` / ``layer_norm_bwd`` and, on a
+``DeltaPlan``, ``delta_fwd`` / ``delta_bwd``) take float32, bfloat16 or float16
+tensors of any size and alignment, launch on the device of their tensors, and
+``stream=None`` is that device's current stream.  With ``S4DPLR_VALIDATE=1``
+their inputs are checked to be finite and the log decays g to be <= 0.
 """
 from __future__ import annotations
 
@@ -30,7 +36,8 @@ __all__ = [
     "plan_workspace_bytes", "plan_init", "kernel_gen", "generating_function", "conv_fwd",
     "forward", "forward_noalloc",
     "conv_apply", "recurrent_prepare", "recurrent_scan", "conv_bwd", "kernel_gen_bwd",
-    "block_forward",
+    "block_forward", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
+    "DeltaPlan", "delta_fwd", "delta_bwd",
     "plan_destroy", "Plan", "LIB_PATH",
 ]
 
@@ -83,6 +90,26 @@ _lib.s4dplr_kernel_gen_bwd.restype = ctypes.c_int
 _lib.s4dplr_kernel_gen_bwd.argtypes = [_p] * 16
 _lib.s4dplr_block_forward.restype = ctypes.c_int
 _lib.s4dplr_block_forward.argtypes = [_p] * 16
+_l, _i = ctypes.c_long, ctypes.c_int
+_lib.s4dplr_layer_norm_fwd.restype = _i
+_lib.s4dplr_layer_norm_fwd.argtypes = [_p] * 6 + [_l] * 3 + [ctypes.c_float, _i, _p]
+_lib.s4dplr_layer_norm_workspace_bytes.restype = _i
+_lib.s4dplr_layer_norm_workspace_bytes.argtypes = [_l] * 3 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.s4dplr_layer_norm_bwd.restype = _i
+_lib.s4dplr_layer_norm_bwd.argtypes = [_p] * 8 + [_l] * 3 + [_i, _p, _p]
+_lib.s4dplr_delta_plan_create.restype = _i
+_lib.s4dplr_delta_plan_create.argtypes = [ctypes.POINTER(_p), _i, _l, _i, _i, _i, _i, _i,
+                                          ctypes.c_uint]
+_lib.s4dplr_delta_plan_bytes.restype = _i
+_lib.s4dplr_delta_plan_bytes.argtypes = [_p] + [ctypes.POINTER(ctypes.c_size_t)] * 2
+_lib.s4dplr_delta_fwd.restype = _i
+_lib.s4dplr_delta_fwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l] + [_p] * 3 + [ctypes.c_float]
+                                  + [_p] * 6)
+_lib.s4dplr_delta_bwd.restype = _i
+_lib.s4dplr_delta_bwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l] + [_p] * 3 + [ctypes.c_float]
+                                  + [_p] * 11)
+_lib.s4dplr_delta_plan_destroy.restype = None
+_lib.s4dplr_delta_plan_destroy.argtypes = [_p]
 _lib.s4dplr_plan_destroy.restype = None
 _lib.s4dplr_plan_destroy.argtypes = [_p]
 
@@ -392,3 +419,256 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------- token-major operators
+
+_DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
+DELTA_TRAINING = 1
+
+
+def _tensor(t, name, dtype, shape, device=None, optional=False):
+    """Device pointer of a contiguous GPU tensor of that dtype and shape."""
+    if t is None and optional:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name}: must be contiguous")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return t.data_ptr()
+
+
+def _rows(t, name, dtype, shape, device):
+    """Device pointer and row pitch of a [rows, heads, d] tensor whose rows are
+    contiguous (a column range of a wider matrix will do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: must be {dtype}, got {t.dtype}")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+    n, heads, d = shape
+    sr, sh, sd = t.stride()
+    if (d > 1 and sd != 1) or (heads > 1 and sh != d) or (n > 1 and sr < heads * d):
+        raise ValueError(f"{name}: each row must be contiguous and apart from the others, "
+                         f"got strides {tuple(t.stride())}")
+    if t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    return t.data_ptr(), sr if n > 1 else heads * d
+
+
+def _launch(device, stream, call):
+    """``call(stream)`` with ``device`` current."""
+    if device.index is None or device.index == torch.cuda.current_device():
+        return call(_stream(stream))
+    with torch.cuda.device(device):
+        return call(_stream(stream))
+
+
+def _workspace(ws, name, need, device):
+    if not isinstance(ws, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if ws.device != device:
+        raise ValueError(f"{name}: on {ws.device}, expected {device}")
+    if not ws.is_contiguous() or ws.numel() * ws.element_size() < need:
+        raise ValueError(f"{name}: must be contiguous and at least {need} bytes")
+    return ws.data_ptr()
+
+
+def _aligned(nbytes: int, device):
+    """A 256-byte aligned uint8 tensor."""
+    store = torch.empty(nbytes + 256, dtype=torch.uint8, device=device)
+    off = (-store.data_ptr()) % 256
+    return store[off: off + nbytes]
+
+
+def _norm_dims(x, axis):
+    """(outer, D, inner) and the shape of the statistics."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: expected a torch.Tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x: must be float32, bfloat16 or float16, got {x.dtype}")
+    shape = tuple(x.shape)
+    axis = axis + len(shape) if axis < 0 else axis
+    if not 0 <= axis < len(shape):
+        raise ValueError(f"axis: out of range for {len(shape)} dimensions")
+    outer = inner = 1
+    for n in shape[:axis]:
+        outer *= n
+    for n in shape[axis + 1:]:
+        inner *= n
+    if inner == 0:               # no vectors at all
+        outer, inner = 0, 1
+    return outer, shape[axis], inner, shape[:axis] + shape[axis + 1:]
+
+
+def layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, axis: int = -1,
+                   stream=None) -> None:
+    """``y`` = the layer norm of ``x`` along ``axis``; ``mean`` and ``rstd``
+    (float32, the shape of ``x`` without that axis) are what
+    ``layer_norm_bwd`` reads.  gamma, beta: [D] float32 or None (1 and 0)."""
+    outer, D, inner, stat = _norm_dims(x, axis)
+    dev = x.device
+    _validate("layer_norm_fwd", x=x, gamma=gamma, beta=beta)
+    f32 = torch.float32
+    args = (_tensor(x, "x", x.dtype, tuple(x.shape)),
+            _tensor(gamma, "gamma", f32, (D,), dev, True),
+            _tensor(beta, "beta", f32, (D,), dev, True),
+            _tensor(y, "y", x.dtype, tuple(x.shape), dev),
+            _tensor(mean, "mean", f32, stat, dev, True),
+            _tensor(rstd, "rstd", f32, stat, dev, True), outer, D, inner, eps, _DTYPES[x.dtype])
+    _check(_launch(dev, stream, lambda st: _lib.s4dplr_layer_norm_fwd(*args, st)),
+           "layer_norm_fwd")
+
+
+def layer_norm_workspace_bytes(x, axis: int = -1) -> int:
+    """Bytes of workspace of ``layer_norm_bwd`` for this ``x``."""
+    outer, D, inner, _ = _norm_dims(x, axis)
+    n = ctypes.c_size_t()
+    _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)),
+           "layer_norm_workspace_bytes")
+    return n.value
+
+
+def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = -1,
+                   stream=None) -> None:
+    """Gradients of ``layer_norm_fwd``; any of dx, dgamma, dbeta may be None.
+    ``ws``: a 256-byte aligned GPU tensor of ``layer_norm_workspace_bytes``."""
+    outer, D, inner, stat = _norm_dims(x, axis)
+    dev = x.device
+    _validate("layer_norm_bwd", x=x, gamma=gamma, dy=dy)
+    f32, full = torch.float32, tuple(x.shape)
+    n = ctypes.c_size_t()
+    _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)),
+           "layer_norm_bwd")
+    args = (_tensor(x, "x", x.dtype, full), _tensor(gamma, "gamma", f32, (D,), dev, True),
+            _tensor(mean, "mean", f32, stat, dev), _tensor(rstd, "rstd", f32, stat, dev),
+            _tensor(dy, "dy", x.dtype, full, dev), _tensor(dx, "dx", x.dtype, full, dev, True),
+            _tensor(dgamma, "dgamma", f32, (D,), dev, True),
+            _tensor(dbeta, "dbeta", f32, (D,), dev, True), outer, D, inner, _DTYPES[x.dtype],
+            _workspace(ws, "ws", n.value, dev))
+    _check(_launch(dev, stream, lambda st: _lib.s4dplr_layer_norm_bwd(*args, st)),
+           "layer_norm_bwd")
+
+
+class DeltaPlan:
+    """A plan of the gated delta rule: ``sequences`` sequences packed into
+    ``tokens`` rows, Hk key heads of dk and Hv value heads of dv values.
+    ``training`` reserves what ``delta_bwd`` needs."""
+
+    def __init__(self, sequences: int, tokens: int, Hk: int, Hv: int, dk: int, dv: int,
+                 dtype=torch.bfloat16, training: bool = False, device=None):
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype: must be float32, bfloat16 or float16, got {dtype}")
+        self.handle = 0
+        self.sequences, self.tokens, self.Hk, self.Hv = sequences, tokens, Hk, Hv
+        self.dk, self.dv, self.dtype, self.training = dk, dv, dtype, training
+        h = _p()
+        _check(_lib.s4dplr_delta_plan_create(
+            ctypes.byref(h), sequences, tokens, Hk, Hv, dk, dv, _DTYPES[dtype],
+            DELTA_TRAINING if training else 0), "delta_plan_create")
+        self.handle = h.value
+        a, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(_lib.s4dplr_delta_plan_bytes(self.handle, ctypes.byref(a), ctypes.byref(b)),
+               "delta_plan_bytes")
+        self.workspace_bytes, self.saved_bytes = a.value, b.value
+        self.device = torch.device("cuda" if device is None else device)
+        self._ws = None
+
+    def workspace(self):
+        """A workspace tensor, one per plan object: calls that can overlap in
+        time, and graphs that can replay together, need one each."""
+        if self._ws is None:
+            self._ws = _aligned(self.workspace_bytes, self.device)
+        return self._ws
+
+    def saved(self):
+        """A new buffer for ``delta_fwd(saved=...)``, one per layer and step."""
+        if not self.training:
+            raise ValueError("saved: the plan was made without training=True")
+        return _aligned(self.saved_bytes, self.device)
+
+    def close(self) -> None:
+        if self.handle:
+            _lib.s4dplr_delta_plan_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _delta_inputs(where, plan, q, k, v, g, beta, ws, scale, offsets):
+    if not isinstance(plan, DeltaPlan):
+        raise TypeError("pass a DeltaPlan")
+    if not plan.handle:
+        raise ValueError("the plan is closed")
+    if not isinstance(v, torch.Tensor):
+        raise TypeError("v: expected a torch.Tensor")
+    if validation_enabled():
+        check_preconditions(where, q=q, k=k, v=v, beta=beta)
+        bad = ~(_host(g) <= 0)          # -infinity is a reset
+        if bool(bad.any()):
+            idx = tuple(int(i) for i in bad.nonzero()[0])
+            raise S4DPLRPreconditionError(where, f"g must be <= 0, not so at index {idx}")
+    n, dev, dt, f32 = plan.tokens, v.device, plan.dtype, torch.float32
+    keys, heads = (n, plan.Hk, plan.dk), (n, plan.Hv)
+    off = None
+    if offsets is not None:
+        off = _tensor(offsets, "offsets", torch.int32, (plan.sequences + 1,), dev)
+    return dev, (plan.handle, *_rows(q, "q", dt, keys, dev), *_rows(k, "k", dt, keys, dev),
+                 *_rows(v, "v", dt, (n, plan.Hv, plan.dv), dev),
+                 _tensor(g, "g", f32, heads, dev), _tensor(beta, "beta", f32, heads, dev), off,
+                 plan.dk ** -0.5 if scale is None else float(scale)), \
+        _workspace(ws, "ws", plan.workspace_bytes, dev)
+
+
+def delta_fwd(plan: "DeltaPlan", q, k, v, g, beta, state, o, state_out, ws, saved=None,
+              scale=None, offsets=None, stream=None) -> None:
+    """``o`` and the states behind the last rows, from ``state`` (None: zeros).
+
+    q, k: [tokens, Hk, dk]; v, o: [tokens, Hv, dv]; g (log decay), beta:
+    [tokens, Hv] float32; state, state_out: [sequences, Hv, dk, dv] float32, may
+    be one tensor, state_out may be None.  q, k, v may be column ranges of wider
+    matrices.  offsets: [sequences + 1] int32 on the GPU, or None for equal
+    lengths.  scale: None is dk ** -0.5.  saved: ``plan.saved()`` for a later
+    ``delta_bwd``."""
+    dev, args, w = _delta_inputs("delta_fwd", plan, q, k, v, g, beta, ws, scale, offsets)
+    st = (plan.sequences, plan.Hv, plan.dk, plan.dv)
+    f32 = torch.float32
+    args += (_tensor(state, "state", f32, st, dev, True),
+             _tensor(o, "o", plan.dtype, (plan.tokens, plan.Hv, plan.dv), dev),
+             _tensor(state_out, "state_out", f32, st, dev, True),
+             None if saved is None else _workspace(saved, "saved", plan.saved_bytes, dev), w)
+    _check(_launch(dev, stream, lambda s: _lib.s4dplr_delta_fwd(*args, s)), "delta_fwd")
+
+
+def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, dk, dv, dg, dbeta,
+              dstate, ws, scale=None, offsets=None, stream=None) -> None:
+    """Gradients of ``delta_fwd`` with the same inputs and the ``saved`` buffer
+    it filled, from ``dout`` and ``dstate_out`` (None: zeros); any of dq, dk, dv,
+    dg, dbeta, dstate may be None."""
+    dev, args, w = _delta_inputs("delta_bwd", plan, q, k, v, g, beta, ws, scale, offsets)
+    n, dt, f32 = plan.tokens, plan.dtype, torch.float32
+    st = (plan.sequences, plan.Hv, plan.dk, plan.dv)
+    keys, vals, heads = (n, plan.Hk, plan.dk), (n, plan.Hv, plan.dv), (n, plan.Hv)
+    args += (_workspace(saved, "saved", plan.saved_bytes, dev),
+             _tensor(dout, "dout", dt, vals, dev),
+             _tensor(dstate_out, "dstate_out", f32, st, dev, True),
+             _tensor(dq, "dq", dt, keys, dev, True), _tensor(dk, "dk", dt, keys, dev, True),
+             _tensor(dv, "dv", dt, vals, dev, True), _tensor(dg, "dg", f32, heads, dev, True),
+             _tensor(dbeta, "dbeta", f32, heads, dev, True),
+             _tensor(dstate, "dstate", f32, st, dev, True), w)
+    _check(_launch(dev, stream, lambda s: _lib.s4dplr_delta_bwd(*args, s)), "delta_bwd")

@@ -17,7 +17,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libs4dplr.so")
 SOURCES = ["kernels.hip", "big.hip", "recurrent.hip", "backward.hip", "vandermonde.hip", "block.hip",
-           "noalloc.hip", "rank.hip", "api.cpp"]
+           "noalloc.hip", "rank.hip", "norm.hip", "delta_step.hip", "delta_prep.hip",
+           "delta_scan.hip", "delta_grads.hip", "api.cpp", "token_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -111,6 +111,8 @@ void recurrent_shape(int N, long rows, int* ppl_out, int* log2g_out) {
   *log2g_out = lg;
 }
 
+s4dplr_status hip_failure(hipError_t e) { return hip_fail(e); }
+
 }  // namespace s4
 
 extern "C" {

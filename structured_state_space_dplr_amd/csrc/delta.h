@@ -1,0 +1,78 @@
+// Gated delta rule: the plan, the layout of its buffers and the launchers.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstddef>
+
+#include "s4dplr.h"
+
+namespace s4 {
+constexpr int kChunk = 64;    // tokens a chunk
+constexpr int kFrag = 1024;   // bytes of one matrix-instruction operand: 64 lanes x 8 bf16
+}  // namespace s4
+
+struct s4dplr_delta_plan {
+  int sequences;
+  long tokens;
+  int Hk, Hv, dk, dv;
+  int dtype;
+  bool training;
+  int dkp;      // dk rounded up to 64, 128 or 256
+  int parts;    // bf16 parts an input element is the exact sum of: 1 (bf16), 2 (fp16), 3 (fp32)
+  int outs;     // parts kept of an operand that only reaches an output of the input's type
+  long slots;   // chunks of all sequences, at most
+  // Workspace, byte offsets.  "frags" are operands in the register order of the
+  // 16x16x32 bf16 matrix instruction, [part][row tile][k step] of kFrag bytes.
+  size_t off_k, off_q;       // [slot][Hk] frags of K, Q (64 x dk)
+  size_t off_kt, off_qt;     // [slot][Hk] frags of K^T, Q^T (dk x 64); Q^T backward only
+  size_t off_x, off_p;       // [slot][Hv] frags of (I + H diag beta)^-1 and of scale P (64 x 64);
+                             // backward: of their transposes
+  size_t off_vec;            // [slot][Hv] DeltaVec
+  size_t off_dv, off_ds;     // backward: [slot][Hv] fp32 dV [64][dv], dS' [dk][dv]
+  size_t total;
+  // saved (training): [slot][Hv] fp32 N [64][dv], S [dk][dv] (the state before the chunk)
+  size_t off_n, off_s;
+  size_t saved_total;
+};
+
+namespace s4 {
+
+// Per chunk and value head; rows behind the sequence's end have beta = 0 and the
+// decay of the last row.
+struct DeltaVec {
+  float e[kChunk];      // exp(G_i)
+  float d[kChunk];      // exp(G_last - G_i)
+  float beta[kChunk];
+  double G[kChunk];     // inclusive sums of g over the chunk
+};
+
+struct DeltaArgs {
+  const void *q, *k, *v;
+  long ldq, ldk, ldv;         // elements from one token to the next
+  const float *g, *beta;
+  const int* offsets;         // [sequences + 1], or NULL: equal lengths
+  const float* state;         // may be NULL: zeros
+  void* o;
+  float* state_out;           // may be NULL
+  float scale;
+  const void* dout;           // backward
+  const float* dstate_out;    // backward, may be NULL: zeros
+  void *dq, *dk, *dv;
+  float *dg, *dbeta;
+  float* dstate;              // may be NULL
+  unsigned char *ws, *saved;
+  int step_tokens;            // sequences of at most so many tokens go token by token
+};
+
+// Longest sequence that is taken token by token.
+constexpr int kStepTokens = 16;
+
+hipError_t launch_delta_steps(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd,
+                             hipStream_t s);
+hipError_t launch_delta_scan(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_scan_bwd(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
+hipError_t launch_delta_grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
+
+}  // namespace s4

@@ -136,6 +136,8 @@ hipError_t launch_layer_norm(const s4dplr_plan* p, const float* x, const float* 
 hipError_t launch_block_epilogue(const s4dplr_plan* p, const float* x, const float* s,
                                  const float* W, const float* bias, float* out,
                                  unsigned char* ws, hipStream_t st);
+// Record a HIP error for s4dplr_last_hip_error() and return the status for it.
+s4dplr_status hip_failure(hipError_t e);
 // Work split of the scan: poles per lane (1, 2, 4 or 8) and log2 of the lanes
 // per sequence (0..5), chosen from N and the number of sequences.
 void recurrent_shape(int N, long rows, int* ppl, int* log2g);

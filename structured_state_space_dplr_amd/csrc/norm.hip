@@ -1,0 +1,515 @@
+// Layer norm, forward and backward, over the middle axis of x [outer][D][inner]:
+//   m = mean_d x,  r = 1 / sqrt(mean_d (x - m)^2 + eps),  y = (x - m) r gamma + beta,
+//   xh = (x - m) r,  w = dy gamma,
+//   dx = r (w - mean_d w - xh mean_d (w xh)),  dgamma = sum dy xh,  dbeta = sum dy.
+// inner = 1 is the token-major layout (rows of D contiguous values), inner = L
+// the [batch][H][L] layout normalized over its H channels.  Elements are fp32,
+// bf16 or fp16; all arithmetic is fp32, each output is rounded once.  The
+// variance is the mean of squared deviations from the mean (two passes over
+// registers), so a large common offset costs no digits.
+//
+// Both directions are bound by HBM: forward reads x and writes y, backward reads
+// x and dy and writes dx.
+#include "norm.h"
+
+#include "vec.h"
+
+namespace s4 {
+
+namespace {
+
+constexpr int kRowThreads = 256;
+
+// Sum over the WPR waves that share a row (WPR = 1: the wave's own lanes).
+template <int WPR>
+__device__ __forceinline__ float row_sum(float v, float* red) {
+  v = sum64(v);
+  if constexpr (WPR == 1) return v;
+  const int w = threadIdx.x >> 6;
+  if ((threadIdx.x & 63) == 0) red[w] = v;
+  __syncthreads();
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < WPR; ++i) s += red[i];
+  return s;
+}
+
+// A lane's share of a row: NV vectors, vector i at element ((i WPR + wave) 64 + lane) VEC.
+// Elements at and behind D read as 0.
+template <typename T, int NV, int WPR>
+__device__ __forceinline__ void load_row(const T* __restrict__ p, int D, int tid, float* out) {
+  constexpr int VEC = Vec<T>::N;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * WPR * 64 + tid) * VEC;
+    if (c + VEC <= D) {
+      const Vec<T> v = load_vec(p + c);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) out[i * VEC + j] = to_f32(v.v[j]);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) out[i * VEC + j] = c + j < D ? to_f32(p[c + j]) : 0.f;
+    }
+  }
+}
+
+template <typename T, int NV, int WPR>
+__device__ __forceinline__ void store_row(T* __restrict__ p, int D, int tid, const float* in) {
+  constexpr int VEC = Vec<T>::N;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * WPR * 64 + tid) * VEC;
+    if (c + VEC <= D) {
+      Vec<T> v;
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v.v[j] = from_f32<T>(in[i * VEC + j]);
+      store_vec(p + c, v);
+    } else {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j)
+        if (c + j < D) p[c + j] = from_f32<T>(in[i * VEC + j]);
+    }
+  }
+}
+
+// Forward over rows.  WPR waves hold one row in registers; a block of
+// max(256, 64 WPR) threads holds 4 rows (WPR = 1) or one.
+template <typename T, int NV, int WPR>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_kernel(
+    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
+    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, long rows, int D,
+    float eps) {
+  constexpr int VEC = Vec<T>::N, E = NV * VEC;
+  constexpr int RPB = WPR == 1 ? kRowThreads / 64 : 1;
+  __shared__ float red[2][WPR];
+  const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const long row = (long)blockIdx.x * RPB + (WPR == 1 ? threadIdx.x >> 6 : 0);
+  if (row >= rows) return;   // WPR > 1: the whole block
+  float v[E], gm[E], bt[E];
+  load_row<T, NV, WPR>(x + row * D, D, tid, v);
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (i * WPR * 64 + tid) * VEC + j;
+      gm[i * VEC + j] = gamma && c < D ? gamma[c] : 1.f;
+      bt[i * VEC + j] = beta && c < D ? beta[c] : 0.f;
+    }
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < E; ++i) s += v[i];
+  const float m = row_sum<WPR>(s, red[0]) / (float)D;
+  float q = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (i * WPR * 64 + tid) * VEC + j;
+      const float d = v[i * VEC + j] - m;
+      v[i * VEC + j] = d;
+      q += c < D ? d * d : 0.f;
+    }
+  const float r = 1.f / sqrtf(row_sum<WPR>(q, red[1]) / (float)D + eps);
+#pragma unroll
+  for (int i = 0; i < E; ++i) v[i] = fmaf(v[i] * r, gm[i], bt[i]);
+  store_row<T, NV, WPR>(y + row * D, D, tid, v);
+  if (tid == 0) {
+    if (mean) mean[row] = m;
+    if (rstd) rstd[row] = r;
+  }
+}
+
+// Backward over rows.  A block of 256 threads (1024 for WPR = 16) walks over
+// rows blockIdx, blockIdx + gridDim, ... ; every lane keeps the same columns, so
+// the columns' sums of dgamma and dbeta stay in its registers and leave the
+// block once, as row blockIdx of part [2][gridDim][D].
+template <typename T, int NV, int WPR>
+__global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
+    float* __restrict__ part, long rows, int D) {
+  constexpr int VEC = Vec<T>::N, E = NV * VEC;
+  constexpr int RPB = WPR == 1 ? kRowThreads / 64 : 1;
+  __shared__ float red[2][2][WPR];
+  __shared__ float cols[WPR == 1 ? 3 * 64 * E : 1];
+  const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
+  const int sub = WPR == 1 ? threadIdx.x >> 6 : 0;
+  float gm[E], ag[E], ab[E];
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      const int c = (i * WPR * 64 + tid) * VEC + j;
+      gm[i * VEC + j] = gamma && c < D ? gamma[c] : 1.f;
+      ag[i * VEC + j] = ab[i * VEC + j] = 0.f;
+    }
+  int turn = 0;
+  for (long row = (long)blockIdx.x * RPB + sub; row < rows; row += (long)gridDim.x * RPB, turn ^= 1) {
+    float xv[E], gv[E];
+    load_row<T, NV, WPR>(x + row * D, D, tid, xv);
+    load_row<T, NV, WPR>(dy + row * D, D, tid, gv);
+    const float m = mean[row], r = rstd[row];
+    float s1 = 0.f, s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < E; ++i) {
+      // behind D, dy = 0 there: nothing is added
+      const float xh = (xv[i] - m) * r, w = gv[i] * gm[i];
+      xv[i] = xh;
+      s1 += w;
+      s2 = fmaf(w, xh, s2);
+      ag[i] = fmaf(gv[i], xh, ag[i]);
+      ab[i] += gv[i];
+      gv[i] = w;
+    }
+    if (dx) {
+      // two sets of slots in turn, so one barrier a row is enough
+      s1 = sum64(s1);
+      s2 = sum64(s2);
+      if constexpr (WPR > 1) {
+        if ((threadIdx.x & 63) == 0) {
+          red[turn][0][threadIdx.x >> 6] = s1;
+          red[turn][1][threadIdx.x >> 6] = s2;
+        }
+        __syncthreads();
+        s1 = s2 = 0.f;
+#pragma unroll
+        for (int i = 0; i < WPR; ++i) {
+          s1 += red[turn][0][i];
+          s2 += red[turn][1][i];
+        }
+      }
+      s1 /= (float)D;
+      s2 /= (float)D;
+#pragma unroll
+      for (int i = 0; i < E; ++i) gv[i] = r * (gv[i] - s1 - xv[i] * s2);
+      store_row<T, NV, WPR>(dx + row * D, D, tid, gv);
+    }
+  }
+  if (!part) return;
+  float* pg = part + (size_t)blockIdx.x * D;
+  float* pb = part + ((size_t)gridDim.x + blockIdx.x) * D;
+#pragma unroll
+  for (int half = 0; half < 2; ++half) {
+    float* a = half ? ab : ag;
+    if constexpr (WPR == 1) {
+      // the four waves hold the same columns
+      __syncthreads();
+      if (sub)
+#pragma unroll
+        for (int i = 0; i < E; ++i) cols[((sub - 1) * E + i) * 64 + tid] = a[i];
+      __syncthreads();
+      if (sub) continue;
+#pragma unroll
+      for (int i = 0; i < E; ++i)
+        a[i] += (cols[i * 64 + tid] + cols[(E + i) * 64 + tid]) + cols[(2 * E + i) * 64 + tid];
+    }
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        const int c = (i * WPR * 64 + tid) * VEC + j;
+        if (c < D) (half ? pb : pg)[c] = a[i * VEC + j];
+      }
+  }
+}
+
+// dgamma[c] = sum_b part[0][b][c], dbeta[c] = sum_b part[1][b][c], always in the
+// same order.  Block: 64 columns; 16 waves share the partial rows.
+__global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int nb,
+                                                            int D, float* __restrict__ dgamma,
+                                                            float* __restrict__ dbeta) {
+  __shared__ float red[16][64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float* out = blockIdx.y ? dbeta : dgamma;
+  if (!out) return;
+  const float* p = part + (size_t)blockIdx.y * nb * D;
+  float s = 0.f;
+  if (c < D)
+#pragma unroll 4
+    for (int b = w; b < nb; b += 16) s += p[(size_t)b * D + c];
+  red[w][lane] = s;
+  __syncthreads();
+  if (w == 0 && c < D) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < 16; ++i) t += red[i][lane];
+    out[c] = t;
+  }
+}
+
+// ------------------------------------------------------- inner > 1: channels
+
+// Lanes take 64 neighbouring positions (o, i) of the flattened outer x inner
+// axis, so a wave reads a line of one channel; the block's 8 waves take the
+// channels d = w, w + 8, ...  EPT > 0 (D <= 8 EPT): the values stay in
+// registers; EPT = 0: they are read again, from the caches where they fit.
+constexpr int kChWaves = 8;
+
+template <int NS>
+__device__ __forceinline__ void wave_sums(float (&s)[NS], float (*red)[kChWaves][64], int w,
+                                          int lane) {
+#pragma unroll
+  for (int k = 0; k < NS; ++k) red[k][w][lane] = s[k];
+  __syncthreads();
+#pragma unroll
+  for (int k = 0; k < NS; ++k) {
+    float t = 0.f;
+#pragma unroll
+    for (int i = 0; i < kChWaves; ++i) t += red[k][i][lane];
+    s[k] = t;
+  }
+}
+
+template <typename T, int EPT>
+__global__ __launch_bounds__(64 * kChWaves) void norm_channels_kernel(
+    const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* y,
+    float* __restrict__ mean, float* __restrict__ rstd, long outer, int D, long inner, float eps) {
+  __shared__ float red[2][1][kChWaves][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long pos = (long)blockIdx.x * 64 + lane;
+  const bool on = pos < outer * inner;
+  const long o = on ? pos / inner : 0, i0 = on ? pos - o * inner : 0;
+  const T* xp = x + o * D * inner + i0;
+  float v[EPT > 0 ? EPT : 1];
+  float s[1] = {0.f};
+  if constexpr (EPT > 0) {
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int d = w + kChWaves * k;
+      v[k] = on && d < D ? to_f32(xp[d * inner]) : 0.f;
+      s[0] += v[k];
+    }
+  } else if (on) {
+#pragma unroll 8
+    for (int d = w; d < D; d += kChWaves) s[0] += to_f32(xp[d * inner]);
+  }
+  wave_sums(s, red[0], w, lane);
+  const float m = s[0] / (float)D;
+  s[0] = 0.f;
+  if constexpr (EPT > 0) {
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      v[k] -= m;
+      s[0] += w + kChWaves * k < D ? v[k] * v[k] : 0.f;
+    }
+  } else if (on) {
+#pragma unroll 8
+    for (int d = w; d < D; d += kChWaves) {
+      const float t = to_f32(xp[d * inner]) - m;
+      s[0] = fmaf(t, t, s[0]);
+    }
+  }
+  wave_sums(s, red[1], w, lane);
+  const float r = 1.f / sqrtf(s[0] / (float)D + eps);
+  if (!on) return;
+  T* yp = y + o * D * inner + i0;
+  if constexpr (EPT > 0) {
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int d = w + kChWaves * k;
+      if (d < D)
+        yp[d * inner] = from_f32<T>(
+            fmaf(v[k] * r, gamma ? gamma[d] : 1.f, beta ? beta[d] : 0.f));
+    }
+  } else {
+#pragma unroll 8
+    for (int d = w; d < D; d += kChWaves)
+      yp[d * inner] = from_f32<T>(fmaf((to_f32(xp[d * inner]) - m) * r, gamma ? gamma[d] : 1.f,
+                                       beta ? beta[d] : 0.f));
+  }
+  if (w == 0) {
+    if (mean) mean[pos] = m;
+    if (rstd) rstd[pos] = r;
+  }
+}
+
+// Backward: a block walks over tiles of 64 positions.  EPT > 0: dgamma and dbeta
+// of the thread's channels are summed in registers over the tiles and over the
+// lanes at the end; EPT = 0: over the lanes in every tile, into the block's own
+// row of part (no other block touches it).
+template <typename T, int EPT>
+__global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
+    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
+    float* __restrict__ part, long outer, int D, long inner) {
+  __shared__ float red[2][2][kChWaves][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const long positions = outer * inner, tiles = (positions + 63) / 64;
+  float* pg = part ? part + (size_t)blockIdx.x * D : nullptr;
+  float* pb = part ? part + ((size_t)gridDim.x + blockIdx.x) * D : nullptr;
+  constexpr int E = EPT > 0 ? EPT : 1;
+  float ag[E], ab[E];
+#pragma unroll
+  for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
+  int turn = 0;
+  bool first = true;
+  for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1, first = false) {
+    const long pos = tile * 64 + lane;
+    const bool on = pos < positions;
+    const long o = on ? pos / inner : 0, i0 = on ? pos - o * inner : 0;
+    const T* xp = x + o * D * inner + i0;
+    const T* gp = dy + o * D * inner + i0;
+    T* dp = dx ? dx + o * D * inner + i0 : nullptr;
+    const float m = on ? mean[pos] : 0.f, r = on ? rstd[pos] : 0.f;
+    float s[2] = {0.f, 0.f};
+    float xh[E], wv[E];
+    if constexpr (EPT > 0) {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int d = w + kChWaves * k;
+        const bool in = on && d < D;
+        xh[k] = in ? to_f32(xp[d * inner]) : 0.f;
+        wv[k] = in ? to_f32(gp[d * inner]) : 0.f;
+      }
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int d = w + kChWaves * k;
+        const float g = wv[k];
+        xh[k] = (xh[k] - m) * r;
+        ag[k] = fmaf(g, xh[k], ag[k]);
+        ab[k] += g;
+        wv[k] = g * (gamma && d < D ? gamma[d] : 1.f);
+        s[0] += wv[k];
+        s[1] = fmaf(wv[k], xh[k], s[1]);
+      }
+    } else {
+      for (int d = w; d < D; d += kChWaves) {
+        const float g = on ? to_f32(gp[d * inner]) : 0.f;
+        const float h = on ? (to_f32(xp[d * inner]) - m) * r : 0.f;
+        const float wg = g * (gamma ? gamma[d] : 1.f);
+        s[0] += wg;
+        s[1] = fmaf(wg, h, s[1]);
+        if (part) {
+          const float tg = sum64(g * h), tb = sum64(g);
+          if (lane == 0) {
+            pg[d] = first ? tg : pg[d] + tg;
+            pb[d] = first ? tb : pb[d] + tb;
+          }
+        }
+      }
+    }
+    if (!dx) continue;
+    wave_sums(s, red[turn], w, lane);
+    const float a = s[0] / (float)D, b = s[1] / (float)D;
+    if (!on) continue;   // no barrier behind this
+    if constexpr (EPT > 0) {
+#pragma unroll
+      for (int k = 0; k < EPT; ++k) {
+        const int d = w + kChWaves * k;
+        if (d < D) dp[d * inner] = from_f32<T>(r * (wv[k] - a - xh[k] * b));
+      }
+    } else {
+#pragma unroll 4
+      for (int d = w; d < D; d += kChWaves) {
+        const float h = (to_f32(xp[d * inner]) - m) * r;
+        const float wg = to_f32(gp[d * inner]) * (gamma ? gamma[d] : 1.f);
+        dp[d * inner] = from_f32<T>(r * (wg - a - h * b));
+      }
+    }
+  }
+  if constexpr (EPT > 0) {
+    if (!part) return;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int d = w + kChWaves * k;
+      const float tg = sum64(ag[k]), tb = sum64(ab[k]);
+      if (lane == 0 && d < D) {
+        pg[d] = tg;
+        pb[d] = tb;
+      }
+    }
+  }
+}
+
+long ceil_div(long a, long b) { return (a + b - 1) / b; }
+
+// Vectors a lane holds and waves a row takes: one wave up to 2 vectors a lane
+// (forward 4), then 4 waves, then 16.
+template <typename T, int MAX1, typename F>
+void row_shape(int D, F f) {
+  const int vecs = (int)ceil_div(D, 64 * Vec<T>::N);
+  using std::integral_constant;
+#define S4_CASE(nv, wpr) f(integral_constant<int, nv>(), integral_constant<int, wpr>())
+  if (vecs <= 1) return S4_CASE(1, 1);
+  if (vecs <= 2) return S4_CASE(2, 1);
+  if constexpr (MAX1 >= 4) {
+    if (vecs <= 4) return S4_CASE(4, 1);
+  }
+  if (vecs <= 4) return S4_CASE(1, 4);
+  if (vecs <= 8) return S4_CASE(2, 4);
+  if (vecs <= 16) return S4_CASE(4, 4);
+  if (vecs <= 32) return S4_CASE(2, 16);
+  if (vecs <= 64) return S4_CASE(4, 16);
+  if constexpr (sizeof(T) == 4) return S4_CASE(8, 16);
+#undef S4_CASE
+}
+
+template <typename T>
+hipError_t fwd(const NormArgs& a, hipStream_t s) {
+  const T* x = (const T*)a.x;
+  T* y = (T*)a.y;
+  const int D = (int)a.D;
+  if (a.inner == 1) {
+    row_shape<T, 4>(D, [&](auto nv, auto wpr) {
+      constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+      const long blocks = WPR == 1 ? ceil_div(a.outer, kRowThreads / 64) : a.outer;
+      norm_rows_kernel<T, NV, WPR><<<dim3((unsigned)blocks), WPR > 4 ? 64 * WPR : kRowThreads, 0,
+                                     s>>>(x, a.gamma, a.beta, y, a.mean, a.rstd, a.outer, D,
+                                          a.eps);
+    });
+    return hipGetLastError();
+  }
+  const dim3 grid((unsigned)ceil_div(a.outer * a.inner, 64));
+#define S4_GO(ept)                                                                            \
+  norm_channels_kernel<T, ept><<<grid, 64 * kChWaves, 0, s>>>(x, a.gamma, a.beta, y, a.mean,  \
+                                                              a.rstd, a.outer, D, a.inner, a.eps)
+  if (D <= 8 * kChWaves) S4_GO(8);
+  else if (D <= 32 * kChWaves) S4_GO(32);
+  else if (D <= 64 * kChWaves) S4_GO(64);
+  else S4_GO(0);
+#undef S4_GO
+  return hipGetLastError();
+}
+
+template <typename T>
+hipError_t bwd(const NormArgs& a, hipStream_t s) {
+  const T *x = (const T*)a.x, *dy = (const T*)a.dy;
+  T* dx = (T*)a.dx;
+  const int D = (int)a.D;
+  const bool sums = a.dgamma || a.dbeta;
+  float* part = sums ? a.part : nullptr;
+  const int nb = (int)norm_parts(a.outer, a.inner);
+  if (a.inner == 1) {
+    row_shape<T, 2>(D, [&](auto nv, auto wpr) {
+      constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+      norm_rows_bwd_kernel<T, NV, WPR><<<dim3(nb), WPR > 4 ? 64 * WPR : kRowThreads, 0, s>>>(
+          x, a.gamma, a.mean, a.rstd, dy, dx, part, a.outer, D);
+    });
+  } else {
+#define S4_GO(ept)                                                                   \
+  norm_channels_bwd_kernel<T, ept><<<dim3(nb), 64 * kChWaves, 0, s>>>(               \
+      x, a.gamma, a.mean, a.rstd, dy, dx, part, a.outer, D, a.inner)
+    if (D <= 8 * kChWaves) S4_GO(8);
+    else if (D <= 32 * kChWaves) S4_GO(32);
+    else S4_GO(0);
+#undef S4_GO
+  }
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess || !sums) return e;
+  norm_columns_kernel<<<dim3((unsigned)ceil_div(D, 64), 2), 1024, 0, s>>>(part, nb, D, a.dgamma,
+                                                                         a.dbeta);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s) {
+  return dtype == S4DPLR_F32 ? fwd<float>(a, s) : dtype == S4DPLR_BF16 ? fwd<bf16>(a, s) : fwd<f16>(a, s);
+}
+
+hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s) {
+  return dtype == S4DPLR_F32 ? bwd<float>(a, s) : dtype == S4DPLR_BF16 ? bwd<bf16>(a, s) : bwd<f16>(a, s);
+}
+
+}  // namespace s4
