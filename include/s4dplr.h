@@ -437,7 +437,7 @@ s4dplr_status s4dplr_delta_plan_bytes(const s4dplr_delta_plan* plan, size_t* wor
 
 /*
  * Forward pass.  ldq, ldk, ldv: elements from one row of q, k, v to the next (at
- * least Hk dk, Hk dk, Hv dv), so the three may be column ranges of one matrix; o
+ * least Hk dk, Hk dk, Hv dv, below 2^24), so the three may be column ranges of one matrix; o
  * is contiguous.  state: [sequences][Hv][dk][dv] float32, the states before the
  * first rows, NULL for zeros; state_out: the states after the last rows, may be
  * NULL (not written) or `state` itself.  saved: NULL, or (plans with

@@ -15,6 +15,7 @@ constexpr int kFrag = 1024;   // bytes of one matrix-instruction operand: 64 lan
 struct s4dplr_delta_plan {
   int sequences;
   long tokens;
+  int each;     // tokens / sequences
   int Hk, Hv, dk, dv;
   int dtype;
   bool training;

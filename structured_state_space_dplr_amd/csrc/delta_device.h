@@ -13,6 +13,9 @@
 #include "delta.h"
 #include "vec.h"
 
+// for pointers whose address space the compiler does not find out by itself
+#define GLOBAL __attribute__((address_space(1)))
+
 namespace s4 {
 
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
@@ -40,45 +43,66 @@ __device__ __forceinline__ v4f mfma_parts(const v8bf (&a)[PA], const v8bf (&b)[P
   return c;
 }
 
+typedef float v2f __attribute__((ext_vector_type(2)));
+typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
+
+// P bf16 parts whose sum is x (exactly, with three parts), by pairs: the hardware
+// converts two values an instruction.
+template <int P>
+__device__ __forceinline__ void split2(v2f x, v2bf (&out)[P]) {
+#pragma unroll
+  for (int p = 0; p < P; ++p) {
+    out[p] = __builtin_convertvector(x, v2bf);
+    if (p + 1 < P) x -= __builtin_convertvector(out[p], v2f);
+  }
+}
 template <int P>
 __device__ __forceinline__ void split8(const float* x, v8bf (&out)[P]) {
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    float r = x[i];
+  for (int i = 0; i < 8; i += 2) {
+    v2bf t[P];
+    split2<P>(v2f{x[i], x[i + 1]}, t);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const __bf16 h = (__bf16)r;
-      out[p][i] = h;
-      r -= (float)h;
+      out[p][i] = t[p][0];
+      out[p][i + 1] = t[p][1];
     }
   }
 }
 template <int P>
 __device__ __forceinline__ void split4(v4f x, v4bf (&out)[P]) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    float r = x[i];
+  for (int i = 0; i < 4; i += 2) {
+    v2bf t[P];
+    split2<P>(v2f{x[i], x[i + 1]}, t);
 #pragma unroll
     for (int p = 0; p < P; ++p) {
-      const __bf16 h = (__bf16)r;
-      out[p][i] = h;
-      r -= (float)h;
+      out[p][i] = t[p][0];
+      out[p][i + 1] = t[p][1];
     }
   }
 }
 
-// Eight elements of one row, zero behind `n`.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, int n, float* out) {
-  if (n >= 8) {
-    T t[8];
+// N elements of one row, zero behind the first n.
+template <int N, typename T>
+__device__ __forceinline__ void load_n(const T* p, int n, float* out) {
+  if (n >= N) {
+    T t[N];
     __builtin_memcpy(t, p, sizeof(t));
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = to_f32(t[i]);
+    for (int i = 0; i < N; ++i) out[i] = to_f32(t[i]);
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) out[i] = i < n ? to_f32(p[i]) : 0.f;
+    for (int i = 0; i < N; ++i) out[i] = i < n ? to_f32(p[i]) : 0.f;
   }
+}
+template <typename T>
+__device__ __forceinline__ void load8(const T* p, int n, float* out) {
+  load_n<8>(p, n, out);
+}
+template <typename T>
+__device__ __forceinline__ void load4(const T* p, int n, float* out) {
+  load_n<4>(p, n, out);
 }
 
 // LDS written by one lane of a wave is read by another behind this
@@ -87,8 +111,11 @@ __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_wave_barrier();
 }
 
-__device__ __forceinline__ v8bf load_frag(const unsigned char* base, int frag, int lane) {
-  return *reinterpret_cast<const v8bf*>(base + (size_t)frag * kFrag + lane * 16);
+// Operand `frag` (a constant) behind a uniform base; off = 16 lane.  The base takes
+// the multiples of 4 KB, so scalar registers and the instruction's own offset hold
+// the rest of the address.
+__device__ __forceinline__ v8bf load_frag(const unsigned char* base, int frag, unsigned off) {
+  return *reinterpret_cast<const v8bf*>(base + (size_t)(frag & ~3) * kFrag + (off + (frag & 3) * kFrag));
 }
 
 // exp of a difference held in 64 bits, at fp32 accuracy for any size of it
@@ -107,17 +134,17 @@ struct Rows {
   __device__ __forceinline__ long first(int s) const { return start / kChunk + s; }
   __device__ __forceinline__ int chunks() const { return (int)((len + kChunk - 1) / kChunk); }
 };
-__device__ __forceinline__ Rows rows_of(const int* offsets, long tokens, int sequences, int s) {
+__device__ __forceinline__ Rows rows_of(const s4dplr_delta_plan& p, const int* offsets, int s) {
   Rows r;
   if (!offsets) {
-    r.len = tokens / sequences;
-    r.start = r.len * s;
+    r.len = p.each;
+    r.start = (long)p.each * s;
     return r;
   }
-  const long a = offsets[s], b = offsets[s + 1];
-  r.start = a < 0 ? 0 : a > tokens ? tokens : a;
-  r.len = (b > tokens ? tokens : b) - r.start;
-  if (r.len < 0) r.len = 0;
+  const int n = (int)p.tokens, a = offsets[s], b = offsets[s + 1];
+  const int start = a < 0 ? 0 : a > n ? n : a, len = (b > n ? n : b) - start;
+  r.start = start;
+  r.len = len < 0 ? 0 : len;
   return r;
 }
 
@@ -133,13 +160,13 @@ __device__ __forceinline__ bool slice_of(int heads, int slices, int* head, int* 
 
 // The sequence whose chunks include `slot`, by all lanes of a wave together:
 // sequences with first(s) <= slot are counted.
-__device__ __forceinline__ int sequence_of(const int* offsets, long tokens, int sequences,
+__device__ __forceinline__ int sequence_of(const s4dplr_delta_plan& p, const int* offsets,
                                            long slot) {
   const int lane = threadIdx.x & 63;
   int n = 0;
-  for (int s0 = 0; s0 < sequences; s0 += 64) {
+  for (int s0 = 0; s0 < p.sequences; s0 += 64) {
     const int s = s0 + lane;
-    const bool le = s < sequences && rows_of(offsets, tokens, sequences, s).first(s) <= slot;
+    const bool le = s < p.sequences && rows_of(p, offsets, s).first(s) <= slot;
     const int c = __popcll(__ballot(le));
     n += c;
     if (c < 64) break;

@@ -31,8 +31,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   const long slot = blockIdx.x;
   const int h = blockIdx.y, hk = h / (p.Hv / p.Hk);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int s = sequence_of(a.offsets, p.tokens, p.sequences, slot);
-  const Rows r = rows_of(a.offsets, p.tokens, p.sequences, s);
+  const int s = sequence_of(p, a.offsets, slot);
+  const Rows r = rows_of(p, a.offsets, s);
   const long c = slot - r.first(s);
   if (c < 0 || c * kChunk >= r.len || r.len <= a.step_tokens) return;
   const long t0 = r.start + c * kChunk;
@@ -51,13 +51,17 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     unsigned char* qo = a.ws + p.off_q + kslot * kbytes;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      const int col = ks * 32 + (lane >> 4) * 8;
+      // the k order of K's and Q's operands: entry e of lane group lg is column
+      // 16 (e / 4) + 4 lg + e % 4 of the step, as an accumulator holds its rows
+      const int col = ks * 32 + (lane >> 4) * 4;
       const int m = row < n ? p.dk - col : 0;
       float x[8];
       v8bf kk[PARTS];
-      load8(kp + col, m, x);
+      load4(kp + col, m, x);
+      load4(kp + col + 16, m - 16, x + 4);
       split8<PARTS>(x, kk);
-      load8(qp + col, m, x);
+      load4(qp + col, m, x);
+      load4(qp + col + 16, m - 16, x + 4);
       split8<PARTS>(x, qr[ks]);
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
@@ -202,7 +206,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     }
   }
   // K^T (then, through the same memory, Q^T): element (row d, k = i) is lane
-  // (i % 16) + 16 ((d % 32) / 8), entry d % 8 of K's operand [i / 16][d / 32]
+  // (i % 16) + 16 ((d % 16) / 4), entry 4 ((d % 32) / 16) + d % 4 of K's operand
+  // [i / 16][d / 32]
   if (!own_k) return;
 #pragma unroll
   for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
@@ -222,7 +227,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = ks * 32 + (lane >> 4) * 8 + e;
-        t[e] = kf[part][i >> 4][d >> 5][(i & 15) + 16 * ((d & 31) >> 3)][d & 7];
+        t[e] = kf[part][i >> 4][d >> 5][(i & 15) + 4 * (d & 12)][((d & 16) >> 2) + (d & 3)];
       }
       *reinterpret_cast<v8bf*>(to + (size_t)f * kFrag + lane * 16) = t;
     }

@@ -23,7 +23,7 @@ __global__ __launch_bounds__(256) void delta_step_kernel(const s4dplr_delta_plan
   int sh, slice;
   if (!slice_of(p.sequences * p.Hv, (p.dv + kCols - 1) / kCols, &sh, &slice)) return;
   const int s = sh / p.Hv, h = sh % p.Hv, hk = h / (p.Hv / p.Hk);
-  const Rows r = rows_of(a.offsets, p.tokens, p.sequences, s);
+  const Rows r = rows_of(p, a.offsets, s);
   if (r.len > a.step_tokens) return;
   const int col = slice * kCols + 4 * (lane & 7), g = w * 8 + (lane >> 3);
   const int m = p.dv - col;   // columns of this lane: 4 or fewer

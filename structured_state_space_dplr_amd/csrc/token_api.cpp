@@ -147,6 +147,7 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
   if (!p) return S4DPLR_ERR_SHAPE;
   p->sequences = sequences;
   p->tokens = tokens;
+  p->each = (int)(tokens / sequences);
   p->Hk = Hk;
   p->Hv = Hv;
   p->dk = dk;
@@ -204,7 +205,7 @@ static s4dplr_status delta_inputs(const s4dplr_delta_plan* p, const void* q, lon
   if (p->tokens > 0 && (!q || !k || !v || !g || !beta)) return S4DPLR_ERR_NULL;
   if (!ws) return S4DPLR_ERR_NULL;
   const long wk = (long)p->Hk * p->dk, wv = (long)p->Hv * p->dv;
-  constexpr long most = 1L << 31;
+  constexpr long most = 1L << 24;   // offsets inside a chunk fit 32 bits
   if (ldq < wk || ldk < wk || ldv < wv || ldq >= most || ldk >= most || ldv >= most)
     return S4DPLR_ERR_SHAPE;
   if (!offsets && p->tokens % p->sequences) return S4DPLR_ERR_SHAPE;
