@@ -31,6 +31,7 @@ struct s4dplr_delta_plan {
                              // backward: of their transposes
   size_t off_vec;            // [slot][Hv] DeltaVec
   size_t off_dv, off_ds;     // backward: [slot][Hv] fp32 dV [64][dv], dS' [dk][dv]
+  size_t off_gates;          // backward, dk > 64: [ceil(dk / 64)][2][tokens][Hv] fp32 parts of dg, dbeta
   size_t total;
   // saved (training): [slot][Hv] fp32 N [64][dv], S [dk][dv] (the state before the chunk)
   size_t off_n, off_s;

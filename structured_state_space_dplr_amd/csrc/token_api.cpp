@@ -176,6 +176,7 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
     p->off_qt = take(ks * kb);
     p->off_dv = take(vs * s4::kChunk * dv * sizeof(float));
     p->off_ds = take(vs * dk * dv * sizeof(float));
+    p->off_gates = take(dk > 64 ? (size_t)((dk + 63) / 64) * 2 * tokens * Hv * sizeof(float) : 0);
   }
   p->total = off;
   off = 0;
