@@ -43,10 +43,10 @@ namespace s4 {
 // Per chunk and value head; rows behind the sequence's end have beta = 0 and the
 // decay of the last row.
 struct DeltaVec {
-  float e[kChunk];      // exp(G_i)
-  float d[kChunk];      // exp(G_last - G_i)
+  float e[kChunk];      // 2^G_i
+  float d[kChunk];      // 2^(G_last - G_i)
   float beta[kChunk];
-  double G[kChunk];     // inclusive sums of g over the chunk
+  double G[kChunk];     // inclusive sums of g / log 2 over the chunk
 };
 
 struct DeltaArgs {

@@ -118,10 +118,11 @@ __device__ __forceinline__ v8bf load_frag(const unsigned char* base, int frag, u
   return *reinterpret_cast<const v8bf*>(base + (size_t)(frag & ~3) * kFrag + (off + (frag & 3) * kFrag));
 }
 
-// exp of a difference held in 64 bits, at fp32 accuracy for any size of it
+// 2^x for a difference x held in 64 bits, at fp32 accuracy for any size of it: the
+// hardware's 2^f for |f| <= 1 / 2, scaled by the whole part.
 __device__ __forceinline__ float exp_diff(double x) {
-  const float h = (float)x;
-  return h > -126.f ? expf(h) * (1.f + (float)(x - (double)h)) : expf(h);
+  const double n = __builtin_rint(x);
+  return ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
 }
 
 // Where a sequence lies in the packed rows, and its chunks in the slots.  Chunks

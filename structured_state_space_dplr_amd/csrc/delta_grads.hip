@@ -60,6 +60,12 @@ struct Tile {
   // m: the tile's first element; rows, cols: what is left of the matrix.  Loads outside
   // are led to element 0 and replaced by 0: no branches.
   __device__ __forceinline__ void load(const float* m, int ld, int rows, int cols, int tid) {
+    if (rows >= 32 && cols >= 64 && ld % 4 == 0) {   // a whole tile, uniformly
+      const unsigned o = (unsigned)((tid >> 4) * ld + (tid & 15) * 4);
+      x[0] = *reinterpret_cast<const v4f*>(m + o);
+      x[1] = *reinterpret_cast<const v4f*>(m + 16 * (size_t)ld + o);
+      return;
+    }
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const int r = (tid >> 4) + 16 * i, c = (tid & 15) * 4;
@@ -303,25 +309,36 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
       load_kq(1);
     }
     __syncthreads();   // the stage's memory becomes the pair matrices'
+    double Gi[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Gi[e] = vec->G[i0 + e];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 16 * i + lr;
-      const float bj = vec->beta[j];
-      const double Gj = vec->G[j];
       float cs = 0.f;
+      if (i <= w) {
+        const float bj = vec->beta[j];
+        const double Gj = vec->G[j];
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int q = i0 + e;
-        const float gam = q >= j ? exp_diff(vec->G[q] - Gj) : 0.f;
-        const float py = q >= j ? a.scale * gam * pp[i][e] * y[i][e] : 0.f;
-        const float hw = q > j ? gam * hh[i][e] * wv[i][e] : 0.f;
-        cs += py - hw;
-        mem.pr.ym[q][j] = q >= j ? a.scale * bj * gam * y[i][e] : 0.f;
-        mem.pr.bm[q][j] = q > j ? bj * gam * wv[i][e] : 0.f;
-        mem.pr.xm[q][j] = q > j ? bj * (py - hw) : 0.f;
+        for (int e = 0; e < 4; ++e) {
+          const int q = i0 + e;
+          const bool low = q > j, diag = q >= j;
+          const float gam = exp_diff(diag ? Gi[e] - Gj : 0.0);
+          const float gy = diag ? a.scale * gam * y[i][e] : 0.f;
+          const float gw = low ? gam * wv[i][e] : 0.f;
+          const float t = gy * pp[i][e] - gw * hh[i][e];
+          cs += t;
+          mem.pr.ym[q][j] = bj * gy;
+          mem.pr.bm[q][j] = bj * gw;
+          mem.pr.xm[q][j] = low ? bj * t : 0.f;
+        }
+        cs += __shfl_xor(cs, 16);
+        cs += __shfl_xor(cs, 32);
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          mem.pr.ym[i0 + e][j] = mem.pr.bm[i0 + e][j] = mem.pr.xm[i0 + e][j] = 0.f;
       }
-      cs += __shfl_xor(cs, 16);
-      cs += __shfl_xor(cs, 32);
       if (lg == 0) colsum[w][j] = cs;
     }
     __syncthreads();

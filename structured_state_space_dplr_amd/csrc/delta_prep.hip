@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     const bool on = lane < n;
     const float g = on ? a.g[(size_t)(t0 + lane) * p.Hv + h] : 0.f;
     const float b = on ? a.beta[(size_t)(t0 + lane) * p.Hv + h] : 0.f;
-    double x = g < -200.f ? -200.0 : (double)g;
+    double x = (g < -200.f ? -200.0 : (double)g) * 1.4426950408889634;   // powers of 2
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double y = __shfl_up(x, off);
