@@ -105,6 +105,17 @@ __device__ __forceinline__ void load4(const T* p, int n, float* out) {
   load_n<4>(p, n, out);
 }
 
+// Eight floats, the first n of them.
+__device__ __forceinline__ void store8(float* p, int n, const float* x) {
+  if (n >= 8) {
+    __builtin_memcpy(p, x, 32);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (i < n) p[i] = x[i];
+  }
+}
+
 // LDS written by one lane of a wave is read by another behind this
 __device__ __forceinline__ void wave_sync() {
   __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");

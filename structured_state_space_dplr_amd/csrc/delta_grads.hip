@@ -33,16 +33,18 @@ constexpr int kLdS = 64 + 16;   // bf16 from row to row of a staged tile: 8 bank
 constexpr int kCols = 64;       // columns of dk of a block
 
 // Operand of 16 columns (the fast index of m [32][LD]) by 32 k (its rows): lane
-// (lr, lg) gets column lr, rows 8 lg .. + 8.  In the transposing read 16 lanes
-// fetch 4 rows of 16 columns and lane i receives column i.
-template <int P>
+// (lr, lg) gets its column, rows 8 lg .. + 8.  In the transposing read 16 lanes
+// fetch 4 rows of 4 groups of 4 columns, and lane i receives column i of the 16.  The
+// groups are STEP columns apart: 4, or 8 for the tiles of dk, which come in the order of
+// K^T's rows.
+template <int P, int STEP = 4>
 __device__ __forceinline__ void get_tr(const __bf16 (*m)[32][kLdS], int c0, int lr, int lg,
                                        v8bf (&out)[P]) {
   typedef short v4s __attribute__((ext_vector_type(4)));
   typedef __attribute__((address_space(3))) v4s lds4;
 #pragma unroll
   for (int q = 0; q < P; ++q) {
-    const __bf16* a = &m[q][8 * lg + (lr >> 2)][c0 + 4 * (lr & 3)];
+    const __bf16* a = &m[q][8 * lg + (lr >> 2)][c0 + STEP * (lr & 3)];
     union {
       v4s h[2];
       v8bf v;
@@ -208,7 +210,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
       get_tr<3>(mem.st.v, 16 * w, lr, lg, va);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        get_tr<3>(mem.st.s, 16 * i, lr, lg, b);
+        get_tr<3, 8>(mem.st.s, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
         g1[i] = mfma_parts<3>(b, oa, g1[i]);
         g2[i] = mfma_parts<3>(b, va, g2[i]);
       }
@@ -225,7 +227,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        get_tr<3>(mem.st.s, 16 * i, lr, lg, b);
+        get_tr<3, 8>(mem.st.s, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
         f[i] = mfma_parts<3>(b, na, f[i]);
       }
     }
@@ -413,7 +415,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
   const size_t to = ((size_t)(t0 + row) * p.Hk + hk) * p.dk + c0;
 #pragma unroll
   for (int i = 0; i < CT; ++i) {
-    const int d = 16 * i + 4 * lg;
+    const int d = 32 * (i >> 1) + 8 * lg + 4 * (i & 1);
     if (a.dq) store4((T*)a.dq + to + d, dcols - d, dq[i]);
     if (a.dk) store4((T*)a.dk + to + d, dcols - d, dk[i]);
   }

@@ -51,17 +51,13 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     unsigned char* qo = a.ws + p.off_q + kslot * kbytes;
 #pragma unroll
     for (int ks = 0; ks < KS; ++ks) {
-      // the k order of K's and Q's operands: entry e of lane group lg is column
-      // 16 (e / 4) + 4 lg + e % 4 of the step, as an accumulator holds its rows
-      const int col = ks * 32 + (lane >> 4) * 4;
+      const int col = ks * 32 + (lane >> 4) * 8;
       const int m = row < n ? p.dk - col : 0;
       float x[8];
       v8bf kk[PARTS];
-      load4(kp + col, m, x);
-      load4(kp + col + 16, m - 16, x + 4);
+      load8(kp + col, m, x);
       split8<PARTS>(x, kk);
-      load4(qp + col, m, x);
-      load4(qp + col + 16, m - 16, x + 4);
+      load8(qp + col, m, x);
       split8<PARTS>(x, qr[ks]);
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
@@ -187,6 +183,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     unsigned char* po = a.ws + p.off_p + vslot * (OUTS * 8 * kFrag);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
+      if (BWD ? ks < w / 2 : ks > w / 2) continue;   // zero, and never read
       const int k0 = ks * 32 + (lane >> 4) * 8;
       float x[8], y[8];
 #pragma unroll
@@ -205,9 +202,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
         *reinterpret_cast<v8bf*>(po + (size_t)((i * 4 + w) * 2 + ks) * kFrag + lane * 16) = ps[i];
     }
   }
-  // K^T (then, through the same memory, Q^T): element (row d, k = i) is lane
-  // (i % 16) + 16 ((d % 16) / 4), entry 4 ((d % 32) / 16) + d % 4 of K's operand
-  // [i / 16][d / 32]
+  // K^T (then, through the same memory, Q^T).  Row 4 g + e of tile t of a k step of dk is
+  // column 8 g + 4 t + e of the step, so that the two tiles' accumulators hold 8
+  // neighbouring rows of the state a lane.  Element (column d, k = i) is lane
+  // (i % 16) + 16 ((d % 32) / 8), entry d % 8 of K's operand [i / 16][d / 32].
   if (!own_k) return;
 #pragma unroll
   for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
@@ -222,12 +220,12 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     }
     for (int f = w; f < PARTS * (DKP / 16) * 2; f += 4) {
       const int ks = f & 1, rt = (f >> 1) % (DKP / 16), part = f / (DKP / 8);
-      const int d = rt * 16 + (lane & 15);
+      const int d = (rt >> 1) * 32 + 8 * ((lane & 15) >> 2) + 4 * (rt & 1) + (lane & 3);
       v8bf t;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         const int i = ks * 32 + (lane >> 4) * 8 + e;
-        t[e] = kf[part][i >> 4][d >> 5][(i & 15) + 4 * (d & 12)][((d & 16) >> 2) + (d & 3)];
+        t[e] = kf[part][i >> 4][d >> 5][(i & 15) + 16 * ((d & 31) >> 3)][d & 7];
       }
       *reinterpret_cast<v8bf*>(to + (size_t)f * kFrag + lane * 16) = t;
     }

@@ -5,13 +5,16 @@
 //
 // A step is a chain of small products with an exchange between waves after each,
 // so its time is latency and instruction issue, not bandwidth.  Of the 8 waves, 0 - 3
-// walk the chain: wave w owns a quarter of S's rows in fp32 accumulators.  The
-// accumulator layout (lane: column l % 16, rows 4 (l / 16) ..) is a matrix operand's
-// layout with its k index permuted, and K and Q are stored in that permutation, so S
-// enters K S and Q S straight from registers as three bf16 parts; the waves' partial
-// sums meet in LDS.  R and d . U pass through LDS as bf16 parts.  Waves 4 - 7 sum Q S
-// and compute and store O beside the chain.  The row tiles of X, P and K^T belong to
-// one wave each: those operands go from memory to registers, a chunk ahead.
+// walk the chain: wave w owns a quarter of S's rows in fp32 accumulators.  K^T is
+// stored with its rows permuted so that the two accumulator tiles of 32 rows hold 8
+// neighbouring rows a lane: a matrix operand's layout, so S enters K S straight from
+// registers as three bf16 parts; the waves' partial sums meet in LDS.  R and d . U pass
+// through LDS as bf16 parts.  Waves 4, 5 compute O beside the chain.  Waves 6, 7 only
+// store (a wave that stores waits for its stores before loads that it issued behind
+// them) and touch the operands three chunks ahead, a line a lane, since a step is
+// shorter than a load from HBM takes: the chain's own loads then hit the XCD's L2,
+// which the slices of a head share (each touches its part).  Row tiles of X and K^T
+// belong to one wave each: those operands go from memory to registers, a chunk ahead.
 #include "delta_device.h"
 
 namespace s4 {
@@ -37,15 +40,15 @@ struct Own {
 
 // What both scans start from.
 struct Place {
-  int sh, h, hk, nc, col, ccol, lr, lg;
+  int sh, h, hk, nc, slice, slices, col0, col, ccol, lr, lg;
   bool colon;
   Rows r;
   long slot0;
 };
 __device__ __forceinline__ bool place_of(const s4dplr_delta_plan& p, const DeltaArgs& a, int lane,
                                          Place* o) {
-  int slice;
-  if (!slice_of(p.sequences * p.Hv, (p.dv + DS - 1) / DS, &o->sh, &slice)) return false;
+  o->slices = (p.dv + DS - 1) / DS;
+  if (!slice_of(p.sequences * p.Hv, o->slices, &o->sh, &o->slice)) return false;
   const int s = o->sh / p.Hv;
   o->h = o->sh % p.Hv;
   o->hk = o->h / (p.Hv / p.Hk);
@@ -54,14 +57,15 @@ __device__ __forceinline__ bool place_of(const s4dplr_delta_plan& p, const Delta
   o->slot0 = o->r.first(s);
   o->lr = lane & 15;
   o->lg = lane >> 4;
-  o->col = slice * DS + o->lr;
+  o->col0 = o->slice * DS;
+  o->col = o->col0 + o->lr;
   o->colon = o->col < p.dv;
   o->ccol = o->colon ? o->col : 0;
   return true;
 }
 
-// The wave's rows of a state [dk][dv] in fp32: tile t of k step k is rows 32 k + 16 t
-// + 4 lg ..
+// The wave's rows of a state [dk][dv] in fp32: tile t of k step k, accumulator entry e,
+// is row 32 k + 8 lg + 4 t + e.
 template <int KW>
 __device__ __forceinline__ void load_state(v4f (&S)[KW][2], const float* state, int k0,
                                            const s4dplr_delta_plan& p, const Place& at) {
@@ -71,7 +75,7 @@ __device__ __forceinline__ void load_state(v4f (&S)[KW][2], const float* state, 
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int d = 32 * (k0 + i) + 16 * t + 4 * at.lg + e;
+        const int d = 32 * (k0 + i) + 8 * at.lg + 4 * t + e;
         S[i][t][e] = state && at.colon && d < p.dk
                          ? state[((size_t)at.sh * p.dk + d) * p.dv + at.col] : 0.f;
       }
@@ -86,26 +90,9 @@ __device__ __forceinline__ void store_state(const v4f (&S)[KW][2], float* state,
     for (int t = 0; t < 2; ++t)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const int d = 32 * (k0 + i) + 16 * t + 4 * at.lg + e;
+        const int d = 32 * (k0 + i) + 8 * at.lg + 4 * t + e;
         if (d < p.dk) state[((size_t)at.sh * p.dk + d) * p.dv + at.col] = S[i][t][e];
       }
-}
-// A chunk's state for stage 3 of the backward pass, [dv][dk]: `to` is the lane's column.
-template <int KW>
-__device__ __forceinline__ void keep_state(const v4f (&S)[KW][2], float* to, int k0, int dk, int lg) {
-#pragma unroll
-  for (int i = 0; i < KW; ++i)
-#pragma unroll
-    for (int t = 0; t < 2; ++t) {
-      const int d = 32 * (k0 + i) + 16 * t + 4 * lg;
-      if (d + 4 <= dk) {
-        __builtin_memcpy(to + d, &S[i][t], 16);
-      } else {
-#pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (d + e < dk) to[d + e] = S[i][t][e];
-      }
-    }
 }
 // The rows of a k step as an operand of three parts.
 __device__ __forceinline__ void state_operand(const v4f (&S)[2], v8bf (&out)[3]) {
@@ -131,6 +118,133 @@ __device__ __forceinline__ void get8(const __bf16 (*from)[DS][kLdT], v8bf (&x)[N
   for (int q = 0; q < N; ++q) x[q] = *reinterpret_cast<const v8bf*>(&from[q][lr][k]);
 }
 
+// The storing waves: j = 0, 1.  A matrix [DS][LD] in LDS to [dv][n] in memory (`to`:
+// the slice's first column), rows of n floats.
+template <int LD>
+__device__ __forceinline__ void store_columns(float* to, const float (*m)[LD], int n, int cols,
+                                              int j, int lane) {
+  constexpr int G = (LD - 4) / 4;   // groups of 4 a column
+#pragma unroll
+  for (int i = 0; i < DS * G / 128; ++i) {
+    const int at = (i * 2 + j) * 64 + lane, c = at / G, d = at % G * 4;
+    const v4f x = *reinterpret_cast<const v4f*>(&m[c][d]);
+    if (c >= cols) continue;
+    float* t = to + (unsigned)(c * n + d);
+    if (d + 4 <= n) {
+      __builtin_memcpy(t, &x, 16);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 3; ++e)
+        if (d + e < n) t[e] = x[e];
+    }
+  }
+}
+// The state's columns from its three parts in LDS (their sum is exact) to [dv][dk].
+template <int DKP>
+__device__ __forceinline__ void store_parts(float* to, const __bf16 (*m)[DS][DKP + 8], int dk,
+                                            int cols, int j, int lane) {
+#pragma unroll
+  for (int i = 0; i < DS * DKP / 8 / 128; ++i) {
+    const int at = (i * 2 + j) * 64 + lane, c = at / (DKP / 8), d = at % (DKP / 8) * 8;
+    const v8bf x = *reinterpret_cast<const v8bf*>(&m[0][c][d]);
+    const v8bf y = *reinterpret_cast<const v8bf*>(&m[1][c][d]);
+    const v8bf z = *reinterpret_cast<const v8bf*>(&m[2][c][d]);
+    float t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = (float)x[e] + ((float)y[e] + (float)z[e]);
+    if (c < cols) store8(to + (unsigned)(c * dk + d), dk - d, t);
+  }
+}
+// A chunk's rows from LDS [column][row] to memory: 8 columns of one row a lane.
+template <typename T>
+__device__ __forceinline__ void store_rows(T* to, unsigned ld, const float (*m)[kLdF], int cols,
+                                           int n, int j, int lane) {
+  const int row = j * 32 + (lane >> 1), c = (lane & 1) * 8;
+  T t[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) t[q] = from_f32<T>(m[c + q][row]);
+  if (row >= n) return;
+  T* o = to + (unsigned)(row * ld + c);
+  if (c + 8 <= cols) {
+    __builtin_memcpy(o, t, sizeof(t));
+  } else {
+#pragma unroll
+    for (int q = 0; q < 8; ++q)
+      if (c + q < cols) o[q] = t[q];
+  }
+}
+
+// Lines of a chunk's operands to bring into the L2: K, then Q (forward) or Q^T
+// (backward), K^T, X, P, shared among the slices of a head; and the slice's own rows
+// of V or dO with the decays.  Chunks are counted from the sequence's first.
+template <int PARTS, int OUTS, int DKP, bool BWD>
+struct Ahead {
+  static constexpr int kTouch = 5;            // lines a lane and chunk, at most
+  static constexpr int kSets = 4;             // chunks in flight
+  static constexpr int KL = PARTS * DKP;      // lines of a 64 x DKP operand (128 bytes each)
+  static constexpr int XL = 3 * 8 * kFrag / 128, PL = OUTS * 8 * kFrag / 128;
+  static constexpr int kLines = 3 * KL + XL + PL;
+  const unsigned char *k, *q, *t, *x, *p, *v, *d;
+  long ldv;                                   // bytes from row to row of V or dO
+  size_t kstep, xstep, pstep, dstep;
+  int id, first, step;                        // this lane's lines: first + i step
+  static constexpr int kSize = PARTS == 3 ? 4 : 2;   // bytes of an element
+
+  __device__ __forceinline__ void set(const s4dplr_delta_plan& pl, const DeltaArgs& a,
+                                      const Place& at, int lane) {
+    constexpr size_t kbytes = (size_t)KL * 128;
+    const size_t f = ((size_t)at.slot0 * pl.Hk + at.hk) * kbytes;
+    const size_t g = (size_t)at.slot0 * pl.Hv + at.h;
+    k = a.ws + pl.off_k + f;
+    q = a.ws + (BWD ? pl.off_qt : pl.off_q) + f;
+    t = a.ws + pl.off_kt + f;
+    x = a.ws + pl.off_x + g * (XL * 128);
+    p = a.ws + pl.off_p + g * (PL * 128);
+    v = (const unsigned char*)(BWD ? a.dout : a.v);
+    ldv = (BWD ? (long)pl.Hv * pl.dv : a.ldv) * kSize;
+    v += at.r.start * ldv + ((size_t)at.h * pl.dv + at.col0) * kSize;
+    d = a.ws + pl.off_vec + g * sizeof(DeltaVec);
+    dstep = (size_t)pl.Hv * sizeof(DeltaVec);
+    id = lane;
+    kstep = (size_t)pl.Hk * kbytes;
+    xstep = (size_t)pl.Hv * (XL * 128);
+    pstep = (size_t)pl.Hv * (PL * 128);
+    first = at.slice * 128 + lane;
+    step = at.slices * 128;
+  }
+  // A whole chunk c.
+  __device__ __forceinline__ void touch(long c, unsigned (&h)[kTouch]) const {
+#pragma unroll
+    for (int i = 0; i < kTouch - 1; ++i) {
+      if (i * step >= kLines) continue;   // uniform
+      int l = first + i * step;
+      if (l >= kLines) l = 0;
+      const unsigned char* from;
+      if (l < KL) {
+        from = k + c * (long)kstep + l * 128;
+      } else if ((l -= KL) < KL) {
+        from = q + c * (long)kstep + l * 128;
+      } else if ((l -= KL) < KL) {
+        from = t + c * (long)kstep + l * 128;
+      } else if ((l -= KL) < XL) {
+        from = x + c * (long)xstep + l * 128;
+      } else {
+        from = p + c * (long)pstep + (l - XL) * 128;
+      }
+      h[i] = *(const GLOBAL unsigned char*)from;
+    }
+    const long line = id - 64 < (int)sizeof(DeltaVec) / 128 ? id - 64 : 0;
+    const unsigned char* from =
+        id < 64 ? v + (c * 64 + id) * ldv : d + c * (long)dstep + line * 128;
+    h[kTouch - 1] = *(const GLOBAL unsigned char*)from;
+  }
+  // What was touched some chunks ago has to have arrived: its registers are free again.
+  __device__ static __forceinline__ void settle(const unsigned (&h)[kTouch]) {
+#pragma unroll
+    for (int i = 0; i < kTouch; ++i) asm volatile("" ::"v"(h[i]));
+  }
+};
+
 }  // namespace
 
 template <typename T, int PARTS, int OUTS, int DKP, bool SAVE>
@@ -139,14 +253,16 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
   using O = Own<DKP>;
   constexpr int KS = O::KS, KW = O::KW, RT = O::RT;
   __shared__ __attribute__((aligned(16))) float pk[O::WAVES][DS][kLdF];   // K S, by owner
-  __shared__ __attribute__((aligned(16))) float pq[O::WAVES][DS][kLdF];   // Q S
+  __shared__ __attribute__((aligned(16))) float os[DS][kLdF];             // O
+  __shared__ __attribute__((aligned(16))) float ns[SAVE ? DS : 1][kLdF];  // N
+  __shared__ __attribute__((aligned(16))) __bf16 st[3][DS][DKP + 8];      // S
   __shared__ __attribute__((aligned(16))) __bf16 rt[3][DS][kLdT];         // R
   __shared__ __attribute__((aligned(16))) __bf16 ut[OUTS][DS][kLdT];      // U
   __shared__ __attribute__((aligned(16))) __bf16 du[3][DS][kLdT];         // d . U
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place at;
   if (!place_of(p, a, lane, &at) || at.r.len <= a.step_tokens) return;
-  const int lr = at.lr, lg = at.lg, w = wave & 3, i0 = 16 * w + 4 * lg, nc = at.nc;
+  const int lr = at.lr, lg = at.lg, nc = at.nc;
   constexpr size_t kbytes = (size_t)PARTS * 4 * KS * kFrag;
   const size_t k0 = ((size_t)at.slot0 * p.Hk + at.hk) * kbytes;
   const size_t v0 = (size_t)at.slot0 * p.Hv + at.h;
@@ -157,36 +273,30 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
 
   if (wave < 4) {
     __builtin_amdgcn_s_setprio(1);
-    const int kw = O::kw(w) * KW, rt0 = O::rt(w);
+    const int w = wave, i0 = 16 * w + 4 * lg, kw = O::kw(w) * KW, rt0 = O::rt(w);
     v4f S[KW][2];
     load_state<KW>(S, a.state, kw, p, at);
 
     // Operands of one chunk, each set loaded right after its last use.
-    v8bf ka[KW][RT][PARTS], qa[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS];
+    v8bf ka[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS];
     v4f ev, dv, bv;
     float el;
     T vv[4];
-    const size_t kq0 = k0 + (size_t)(rt0 * KS + kw) * kFrag;
-    const unsigned char* kp = a.ws + p.off_k + kq0;
-    const unsigned char* qp = a.ws + p.off_q + kq0;
+    const unsigned char* kp = a.ws + p.off_k + k0 + (size_t)(rt0 * KS + kw) * kFrag;
     const unsigned char* tp = a.ws + p.off_kt + k0 + (size_t)kw * 4 * kFrag;
     const unsigned char* xp = a.ws + p.off_x + v0 * (3 * 8 * kFrag) + (size_t)w * 2 * kFrag;
     const T* vp = (const T*)a.v + at.r.start * a.ldv + (size_t)at.h * p.dv;
-    float* np = SAVE ? reinterpret_cast<float*>(a.saved + p.off_n) + v0 * kChunk * p.dv +
-                           (size_t)at.ccol * kChunk + i0 : nullptr;
-    float* sp = SAVE ? reinterpret_cast<float*>(a.saved + p.off_s) + v0 * p.dk * p.dv +
-                           (size_t)at.ccol * p.dk : nullptr;
     const unsigned ldv = (unsigned)a.ldv;
     unsigned voff[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) voff[e] = (unsigned)(i0 + e) * ldv + at.ccol;
-    auto load_kq = [&](const unsigned char* from, v8bf (&to)[KW][RT][PARTS]) {
+    auto load_k = [&] {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
 #pragma unroll
         for (int t = 0; t < RT; ++t)
 #pragma unroll
-          for (int i = 0; i < KW; ++i) to[i][t][q] = load_frag(from, (q * 4 + t) * KS + i, off);
+          for (int i = 0; i < KW; ++i) ka[i][t][q] = load_frag(kp, (q * 4 + t) * KS + i, off);
     };
     auto load_x = [&] {
 #pragma unroll
@@ -209,8 +319,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
     // A partial chunk's rows behind the end read the sequence's last row: their
     // K, Q and beta are zero, so their values reach nothing.  (A load under a
     // condition would be waited for at once.)
-    auto load_v = [&](int c) {
-      const int n = (int)(at.r.len - (long)c * kChunk);
+    auto load_v = [&](int n) {
       if (n >= kChunk) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) vv[e] = vp[voff[e]];
@@ -226,66 +335,56 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       bv = *reinterpret_cast<const v4f*>(dp->beta + i0);
       el = dp->e[kChunk - 1];
     };
+    int n = (int)at.r.len;   // rows left from the loaded chunk on
     if (nc > 0) {
-      load_kq(kp, ka);
-      load_v(0);
+      load_k();
+      load_v(n);
       load_d();
-      load_kq(qp, qa);
       load_x();
       load_t();
     }
     for (int c = 0; c < nc; ++c) {
-      const bool more = c + 1 < nc;   // else the same operands once more
-      if (more) {
+      if (c + 1 < nc) {   // else the same operands once more
+        n -= kChunk;
         kp += kstep;
-        qp += kstep;
         tp += kstep;
         xp += (size_t)p.Hv * (3 * 8 * kFrag);
         dp += p.Hv;
         vp += (size_t)kChunk * ldv;
       }
-      v8bf sb[KW][3];
-#pragma unroll
-      for (int i = 0; i < KW; ++i) state_operand(S[i], sb[i]);
       {
         v4f x[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) x[t] = zero;
 #pragma unroll
-        for (int i = 0; i < KW; ++i)
+        for (int i = 0; i < KW; ++i) {
+          v8bf sb[3];
+          state_operand(S[i], sb);
 #pragma unroll
-          for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(ka[i][t], sb[i], x[t]);
-        if (SAVE && at.colon && O::first(w)) keep_state<KW>(S, sp, kw, p.dk, lg);
-        if constexpr (SAVE) sp += (size_t)p.Hv * p.dk * p.dv;
+          for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(ka[i][t], sb, x[t]);
+          if (O::first(w))
+#pragma unroll
+            for (int q = 0; q < 3; ++q)
+              *reinterpret_cast<v8bf*>(&st[q][lr][32 * (kw + i) + 8 * lg]) = sb[q];
+        }
 #pragma unroll
         for (int t = 0; t < RT; ++t)
           *reinterpret_cast<v4f*>(&pk[O::kw(w)][lr][16 * (rt0 + t) + 4 * lg]) = x[t];
       }
-      load_kq(kp, ka);
       __syncthreads();
       {
         v4f ks[O::WAVES];
 #pragma unroll
         for (int i = 0; i < O::WAVES; ++i) ks[i] = *reinterpret_cast<const v4f*>(&pk[i][lr][i0]);
-        // off the chain: Q S
-        v4f x[RT];
-#pragma unroll
-        for (int t = 0; t < RT; ++t) x[t] = zero;
-#pragma unroll
-        for (int i = 0; i < KW; ++i)
-#pragma unroll
-          for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(qa[i][t], sb[i], x[t]);
+        load_k();
         v4f R;
 #pragma unroll
         for (int e = 0; e < 4; ++e) R[e] = to_f32(vv[e]);
         v4f sum = ks[0] + ks[1];
         if constexpr (O::WAVES == 4) sum += ks[2] + ks[3];
         put4<3>(rt, R - ev * sum, lr, i0);
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-          *reinterpret_cast<v4f*>(&pq[O::kw(w)][lr][16 * (rt0 + t) + 4 * lg]) = x[t];
       }
-      load_v(c + more);
+      load_v(n);
       __syncthreads();
       v4f N = zero, n1 = zero;
       {
@@ -302,13 +401,9 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
         const v4f U = bv * N;
         put4<3>(du, dv * U, lr, i0);
         put4<OUTS>(ut, U, lr, i0);
+        if constexpr (SAVE) *reinterpret_cast<v4f*>(&ns[lr][i0]) = N;
       }
-      load_kq(qp, qa);
       load_x();
-      if constexpr (SAVE) {
-        if (at.colon) *reinterpret_cast<v4f*>(np) = N;
-        np += (size_t)p.Hv * kChunk * p.dv;
-      }
       __syncthreads();
       v8bf ub[2][3];
 #pragma unroll
@@ -326,58 +421,117 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       load_d();
       load_t();
     }
+    __syncthreads();
     if (O::first(w)) store_state<KW>(S, a.state_out, kw, p, at);
-  } else {
-    v8bf pa[2][OUTS];
-    v4f ev;
-    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag) + (size_t)w * 2 * kFrag;
-    const unsigned ldo = (unsigned)(p.Hv * p.dv);
-    T* op = (T*)a.o + (size_t)at.r.start * ldo + (size_t)at.h * p.dv;
-    unsigned ooff[4];
+  } else if (wave < 6) {
+    // row tiles j and 3 - j of O: one of them reaches over both k steps of P
+    const int j = wave - 4;
+    v8bf p0[OUTS], p1[2][OUTS], qa[2][KS][PARTS];
+    v4f ev[2];
+    const unsigned char* qp = a.ws + p.off_q + k0;
+    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag);
+    auto load_q = [&] {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ooff[e] = (unsigned)(i0 + e) * ldo + at.ccol;
-    auto load_p = [&] {
-      ev = *reinterpret_cast<const v4f*>(dp->e + i0);
+      for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-      for (int q = 0; q < OUTS; ++q) pa[0][q] = load_frag(pp, q * 8, off);
-      if (w >= 2)
-#pragma unroll
-        for (int q = 0; q < OUTS; ++q) pa[1][q] = load_frag(pp, q * 8 + 1, off);
+        for (int ks = 0; ks < KS; ++ks) {
+          qa[0][ks][q] = load_frag(qp + (size_t)j * KS * kFrag, q * 4 * KS + ks, off);
+          qa[1][ks][q] = load_frag(qp + (size_t)(3 - j) * KS * kFrag, q * 4 * KS + ks, off);
+        }
+      ev[0] = *reinterpret_cast<const v4f*>(dp->e + 16 * j + 4 * lg);
+      ev[1] = *reinterpret_cast<const v4f*>(dp->e + 16 * (3 - j) + 4 * lg);
     };
-    if (nc > 0) load_p();
+    auto load_p = [&] {
+#pragma unroll
+      for (int q = 0; q < OUTS; ++q) {
+        p0[q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8, off);
+        p1[0][q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8, off);
+        p1[1][q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8 + 1, off);
+      }
+    };
+    if (nc > 0) {
+      load_q();
+      load_p();
+    }
     for (int c = 0; c < nc; ++c) {
       if (c + 1 < nc) {
+        qp += kstep;
         pp += (size_t)p.Hv * (OUTS * 8 * kFrag);
         dp += p.Hv;
       }
       __syncthreads();
-      __syncthreads();
-      v4f o = *reinterpret_cast<const v4f*>(&pq[0][lr][i0]);
+      v4f o[2] = {zero, zero};
 #pragma unroll
-      for (int i = 1; i < O::WAVES; ++i) o += *reinterpret_cast<const v4f*>(&pq[i][lr][i0]);
-      o *= ev * a.scale;
-      __syncthreads();
-      v8bf ub[OUTS];
-      get8<OUTS>(ut, ub, lr, lg * 8);
-      o = mfma_parts<OUTS>(pa[0], ub, o);
-      if (w >= 2) {
-        get8<OUTS>(ut, ub, lr, 32 + lg * 8);
-        o = mfma_parts<OUTS>(pa[1], ub, o);
+      for (int ks = 0; ks < KS; ++ks) {
+        v8bf sb[3];
+#pragma unroll
+        for (int q = 0; q < 3; ++q)
+          sb[q] = *reinterpret_cast<const v8bf*>(&st[q][lr][32 * ks + 8 * lg]);
+        o[0] = mfma_parts<3>(qa[0][ks], sb, o[0]);
+        o[1] = mfma_parts<3>(qa[1][ks], sb, o[1]);
       }
+      o[0] *= ev[0] * a.scale;
+      o[1] *= ev[1] * a.scale;
+      load_q();
+      __syncthreads();
+      __syncthreads();
+      v8bf ub[2][OUTS];
+      get8<OUTS>(ut, ub[0], lr, lg * 8);
+      get8<OUTS>(ut, ub[1], lr, 32 + lg * 8);
+      o[0] = mfma_parts<OUTS>(p0, ub[0], o[0]);
+      o[1] = mfma_parts<OUTS>(p1[0], ub[0], o[1]);
+      o[1] = mfma_parts<OUTS>(p1[1], ub[1], o[1]);
+      *reinterpret_cast<v4f*>(&os[lr][16 * j + 4 * lg]) = o[0];
+      *reinterpret_cast<v4f*>(&os[lr][16 * (3 - j) + 4 * lg]) = o[1];
       load_p();
-      const int n = (int)(at.r.len - (long)c * kChunk);
-      if (at.colon) {
-        if (n >= kChunk) {
+    }
+    __syncthreads();
+  } else {
+    const int j = wave - 6, cols = p.dv - at.col0;
+    const unsigned ldo = (unsigned)(p.Hv * p.dv);
+    T* op = (T*)a.o + (size_t)at.r.start * ldo + (size_t)at.h * p.dv + at.col0;
+    float *np = nullptr, *sp = nullptr;
+    if constexpr (SAVE) {
+      np = reinterpret_cast<float*>(a.saved + p.off_n) + (v0 * p.dv + at.col0) * kChunk;
+      sp = reinterpret_cast<float*>(a.saved + p.off_s) + (v0 * p.dv + at.col0) * p.dk;
+    }
+    using A = Ahead<PARTS, OUTS, DKP, false>;
+    A ahead;
+    ahead.set(p, a, at, j * 64 + lane);
+    const int whole = (int)(at.r.len / kChunk);   // chunks read in place
+    // chunks behind the last whole one are not touched: their rows need not exist
+    auto touch = [&](int c, unsigned (&h)[A::kTouch]) {
+      if (c < whole) ahead.touch(c, h);
+    };
+    unsigned held[A::kSets][A::kTouch] = {};
+    touch(1, held[1]);
+    touch(2, held[2]);
+    for (int c4 = 0; c4 < nc; c4 += A::kSets)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) op[ooff[e]] = from_f32<T>(o[e]);
-        } else {
-#pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (i0 + e < n) op[ooff[e]] = from_f32<T>(o[e]);
+      for (int u = 0; u < A::kSets; ++u) {
+        const int c = c4 + u;
+        if (c < nc) {
+        A::settle(held[(u + 3) % A::kSets]);
+        touch(c + 3, held[(u + 3) % A::kSets]);
+        __syncthreads();
+        if constexpr (SAVE) {
+          store_parts<DKP>(sp, st, p.dk, cols, j, lane);
+          sp += (size_t)p.Hv * p.dk * p.dv;
+        }
+        if (c > 0) {
+          store_rows<T>(op, ldo, os, cols, kChunk, j, lane);
+          op += (size_t)kChunk * ldo;
+        }
+        __syncthreads();
+        __syncthreads();
+        if constexpr (SAVE) {
+          store_columns<kLdF>(np, ns, kChunk, cols, j, lane);
+          np += (size_t)p.Hv * kChunk * p.dv;
+        }
         }
       }
-      op += (size_t)kChunk * ldo;
-    }
+    __syncthreads();
+    if (nc > 0) store_rows<T>(op, ldo, os, cols, (int)(at.r.len - (long)(nc - 1) * kChunk), j, lane);
   }
 }
 
@@ -385,9 +539,9 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
 // formulas):
 //   dU = (scale P)^T dO + d . (K Z),  dV = X^T (beta . dU),
 //   Z <- e_last Z + Q^T (scale e . dO) - K^T (e . dV).
-// Waves 0 - 3 walk this chain; waves 4 - 7 prepare the products with dO a chunk
-// ahead and store dV (the gradient of v, and fp32 [dv][64] for stage 3).  Z before
-// its update is kept for stage 3.
+// Waves 0 - 3 walk this chain, 4 and 5 prepare the products with dO a chunk ahead, 6
+// and 7 store dV (the gradient of v, and fp32 [dv][64] for stage 3) and Z before its
+// update ([dv][dk], for stage 3).
 template <typename T, int PARTS, int OUTS, int DKP>
 __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_plan p,
                                                              const DeltaArgs a) {
@@ -396,14 +550,16 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
   __shared__ __attribute__((aligned(16))) float pk[O::WAVES][DS][kLdF];   // K Z, by owner
   __shared__ __attribute__((aligned(16))) float d1[2][DS][kLdF];          // (scale P)^T dO
   __shared__ __attribute__((aligned(16))) float vs[DS][kLdF];             // dV
+  __shared__ __attribute__((aligned(16))) float ss[DS][DKP + 4];          // Z
   __shared__ __attribute__((aligned(16))) __bf16 ot[PARTS][DS][kLdT];     // dO
-  __shared__ __attribute__((aligned(16))) __bf16 et[2][3][DS][kLdT];      // scale e . dO
+  __shared__ __attribute__((aligned(16))) float eq[2][DS][DKP + 4];       // Q^T (scale e . dO)
+  __shared__ __attribute__((aligned(16))) __bf16 et[3][DS][kLdT];         // scale e . dO
   __shared__ __attribute__((aligned(16))) __bf16 ut[3][DS][kLdT];         // beta . dU
   __shared__ __attribute__((aligned(16))) __bf16 vt[3][DS][kLdT];         // -e . dV
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place at;
   if (!place_of(p, a, lane, &at)) return;
-  const int lr = at.lr, lg = at.lg, w = wave & 3, i0 = 16 * w + 4 * lg, nc = at.nc;
+  const int lr = at.lr, lg = at.lg, nc = at.nc;
   constexpr size_t kbytes = (size_t)PARTS * 4 * KS * kFrag;
   const long slot1 = at.slot0 + nc - 1;   // the last chunk
   const size_t k0 = ((size_t)slot1 * p.Hk + at.hk) * kbytes;
@@ -412,22 +568,22 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
   const unsigned off = lane * 16;
   const DeltaVec* dp = reinterpret_cast<const DeltaVec*>(a.ws + p.off_vec) + v0;
   const v4f zero = {0.f, 0.f, 0.f, 0.f};
+  const unsigned ldo = (unsigned)(p.Hv * p.dv);
+  const size_t row1 = (size_t)at.r.start + (size_t)(nc - 1) * kChunk;
+  const int last = (int)(at.r.len - (long)(nc - 1) * kChunk);   // rows of the last chunk
 
   if (wave < 4) {
     __builtin_amdgcn_s_setprio(1);
-    const int kw = O::kw(w) * KW, rt0 = O::rt(w);
+    const int w = wave, i0 = 16 * w + 4 * lg, kw = O::kw(w) * KW, rt0 = O::rt(w);
     v4f Z[KW][2];
     load_state<KW>(Z, a.dstate_out, kw, p, at);
     if (nc > 0) {
-      v8bf ka[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS], qa[KW][2][2][PARTS];
+      v8bf ka[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS];
       v4f ev, dv, bv;
       float el;
       const unsigned char* kp = a.ws + p.off_k + k0 + (size_t)(rt0 * KS + kw) * kFrag;
       const unsigned char* tp = a.ws + p.off_kt + k0 + (size_t)kw * 4 * kFrag;
-      const unsigned char* qp = a.ws + p.off_qt + k0 + (size_t)kw * 4 * kFrag;
       const unsigned char* xp = a.ws + p.off_x + v0 * (3 * 8 * kFrag) + (size_t)w * 2 * kFrag;
-      float* zp = reinterpret_cast<float*>(a.ws + p.off_ds) + v0 * p.dk * p.dv +
-                  (size_t)at.ccol * p.dk;
       auto load_k = [&] {
 #pragma unroll
         for (int q = 0; q < PARTS; ++q)
@@ -443,7 +599,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
 #pragma unroll
           for (int i = 0; i < 3; ++i) xa[0][i] = load_frag(xp, i * 8, off);
       };
-      auto load_t = [&](const unsigned char* from, v8bf (&to)[KW][2][2][PARTS]) {
+      auto load_t = [&] {
 #pragma unroll
         for (int q = 0; q < PARTS; ++q)
 #pragma unroll
@@ -452,7 +608,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
             for (int t = 0; t < 2; ++t)
 #pragma unroll
               for (int ks = 0; ks < 2; ++ks)
-                to[i][t][ks][q] = load_frag(from, (q * (DKP / 16) + 2 * i + t) * 2 + ks, off);
+                ta[i][t][ks][q] = load_frag(tp, (q * (DKP / 16) + 2 * i + t) * 2 + ks, off);
       };
       auto load_d = [&] {
         ev = *reinterpret_cast<const v4f*>(dp->e + i0);
@@ -463,14 +619,12 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
       load_k();
       load_d();
       load_x();
-      load_t(qp, qa);
-      load_t(tp, ta);
+      load_t();
       __syncthreads();   // the others' first products
       __syncthreads();
       for (int c = nc - 1; c >= 0; --c) {
         if (c > 0) {   // else the same operands once more
           kp -= kstep;
-          qp -= kstep;
           tp -= kstep;
           xp -= (size_t)p.Hv * (3 * 8 * kFrag);
           dp -= p.Hv;
@@ -487,8 +641,12 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
 #pragma unroll
             for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(ka[i][t], sb, x[t]);
           }
-          if (at.colon && O::first(w)) keep_state<KW>(Z, zp, kw, p.dk, lg);
-          zp -= (size_t)p.Hv * p.dk * p.dv;
+          if (O::first(w))
+#pragma unroll
+            for (int i = 0; i < KW; ++i)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                *reinterpret_cast<v4f*>(&ss[lr][32 * (kw + i) + 8 * lg + 4 * t]) = Z[i][t];
 #pragma unroll
           for (int t = 0; t < RT; ++t)
             *reinterpret_cast<v4f*>(&pk[O::kw(w)][lr][16 * (rt0 + t) + 4 * lg]) = x[t];
@@ -502,20 +660,12 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
           const v4f g = *reinterpret_cast<const v4f*>(&d1[b][lr][i0]);
           put4<3>(ut, bv * (g + dv * kz), lr, i0);
         }
-        // off the chain: Q^T (scale e . dO)
 #pragma unroll
         for (int i = 0; i < KW; ++i)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) Z[i][t] *= el;
-#pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          v8bf eb[3];
-          get8<3>(et[b], eb, lr, ks * 32 + lg * 8);
-#pragma unroll
-          for (int i = 0; i < KW; ++i)
-#pragma unroll
-            for (int t = 0; t < 2; ++t) Z[i][t] = mfma_parts<3>(qa[i][t][ks], eb, Z[i][t]);
-        }
+          for (int t = 0; t < 2; ++t)
+            Z[i][t] = Z[i][t] * el +
+                      *reinterpret_cast<const v4f*>(&eq[b][lr][32 * (kw + i) + 8 * lg + 4 * t]);
         __syncthreads();
         v4f dV = zero, dV1 = zero;
         {
@@ -530,7 +680,6 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
         }
         put4<3>(vt, -(ev * dV), lr, i0);
         *reinterpret_cast<v4f*>(&vs[lr][i0]) = dV;
-        load_t(qp, qa);
         load_x();
         load_d();
         __syncthreads();
@@ -543,99 +692,153 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
 #pragma unroll
             for (int t = 0; t < 2; ++t) Z[i][t] = mfma_parts<3>(ta[i][t][ks], vb, Z[i][t]);
         }
-        load_t(tp, ta);
+        load_t();
       }
     }
     if (O::first(w)) store_state<KW>(Z, a.dstate, kw, p, at);
-  } else if (nc > 0) {
-    v8bf pa[2][OUTS];
-    v4f ev;
-    T go[4];
-    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag) + (size_t)w * 2 * kFrag;
-    const unsigned ldo = (unsigned)(p.Hv * p.dv);
-    const size_t row1 = (size_t)at.r.start + (size_t)(nc - 1) * kChunk;
+  } else if (nc > 0 && wave < 6) {
+    // row tiles j and 3 - j: one of them reaches over both k steps of P^T
+    const int j = wave - 4, ra = 16 * j + 4 * lg, rb = 16 * (3 - j) + 4 * lg;
+    constexpr int QT = DKP / 32;   // tiles of Q^T a wave
+    v8bf p0[2][OUTS], p1[OUTS], qa[QT][2][PARTS];
+    v4f ev[2];
+    T go[2][4];
+    const unsigned char* qp = a.ws + p.off_qt + k0 + (size_t)j * QT * 2 * kFrag;
+    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag);
     const T* gp = (const T*)a.dout + row1 * ldo + (size_t)at.h * p.dv;
-    T* op = (T*)a.dv + row1 * ldo + (size_t)at.h * p.dv;
-    float* fp = reinterpret_cast<float*>(a.ws + p.off_dv) + v0 * kChunk * p.dv +
-                (size_t)at.ccol * kChunk + i0;
-    unsigned ooff[4];
+    unsigned ooff[2][4];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) ooff[e] = (unsigned)(i0 + e) * ldo + at.ccol;
-    auto rows = [&](int c) { return (int)(at.r.len - (long)c * kChunk); };
-    auto load = [&](int c) {   // chunk c's, by the moving pointers
-      ev = *reinterpret_cast<const v4f*>(dp->e + i0);
-      const int n = rows(c);
-      if (n >= kChunk) {
+    for (int e = 0; e < 4; ++e) {
+      ooff[0][e] = (unsigned)(ra + e) * ldo + at.ccol;
+      ooff[1][e] = (unsigned)(rb + e) * ldo + at.ccol;
+    }
+    auto load = [&](bool whole) {   // by the moving pointers
+      ev[0] = *reinterpret_cast<const v4f*>(dp->e + ra);
+      ev[1] = *reinterpret_cast<const v4f*>(dp->e + rb);
+      if (whole) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) go[e] = ((const GLOBAL T*)gp)[ooff[e]];
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) go[t][e] = ((const GLOBAL T*)gp)[ooff[t][e]];
       } else {   // rows behind the end: Q and P are zero there
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          go[e] = ((const GLOBAL T*)gp)[(unsigned)(i0 + e < n ? i0 + e : n - 1) * ldo + at.ccol];
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const int i = (t ? rb : ra) + e;
+            go[t][e] = ((const GLOBAL T*)gp)[(unsigned)(i < last ? i : last - 1) * ldo + at.ccol];
+          }
       }
 #pragma unroll
-      for (int q = 0; q < OUTS; ++q) pa[1][q] = load_frag(pp, q * 8 + 1, off);
-      if (w < 2)
+      for (int q = 0; q < OUTS; ++q) {
+        p0[0][q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8, off);
+        p0[1][q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8 + 1, off);
+        p1[q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8 + 1, off);
+      }
 #pragma unroll
-        for (int q = 0; q < OUTS; ++q) pa[0][q] = load_frag(pp, q * 8, off);
-    };
-    auto put = [&](int c) {
-      v4f g;
+      for (int q = 0; q < PARTS; ++q)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) g[e] = to_f32(go[e]);
-      put4<PARTS>(ot, g, lr, i0);
-      put4<3>(et[c & 1], g * (ev * a.scale), lr, i0);
+        for (int t = 0; t < QT; ++t)
+#pragma unroll
+          for (int ks = 0; ks < 2; ++ks)
+            qa[t][ks][q] = load_frag(qp, (q * (DKP / 16) + t) * 2 + ks, off);
     };
-    auto product = [&](int c) {
-      v4f g = zero;
-      v8bf ob[PARTS];
+    auto put = [&] {
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+        v4f g;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) g[e] = to_f32(go[t][e]);
+        put4<PARTS>(ot, g, lr, t ? rb : ra);
+        put4<3>(et, g * (ev[t] * a.scale), lr, t ? rb : ra);
+      }
+    };
+    auto product = [&](int b) {
+      v4f g0 = zero, g1 = zero;
+      v8bf oa[PARTS], ob[PARTS];
+      get8<PARTS>(ot, oa, lr, lg * 8);
       get8<PARTS>(ot, ob, lr, 32 + lg * 8);
-      g = mfma_parts<3>(pa[1], ob, g);
-      if (w < 2) {
-        get8<PARTS>(ot, ob, lr, lg * 8);
-        g = mfma_parts<3>(pa[0], ob, g);
+      g0 = mfma_parts<3>(p0[0], oa, g0);
+      g1 = mfma_parts<3>(p1, ob, g1);
+      g0 = mfma_parts<3>(p0[1], ob, g0);
+      *reinterpret_cast<v4f*>(&d1[b][lr][ra]) = g0;
+      *reinterpret_cast<v4f*>(&d1[b][lr][rb]) = g1;
+      v4f x[QT];
+#pragma unroll
+      for (int t = 0; t < QT; ++t) x[t] = zero;
+#pragma unroll
+      for (int ks = 0; ks < 2; ++ks) {
+        v8bf eb[3];
+        get8<3>(et, eb, lr, ks * 32 + lg * 8);
+#pragma unroll
+        for (int t = 0; t < QT; ++t) x[t] = mfma_parts<3>(qa[t][ks], eb, x[t]);
       }
-      *reinterpret_cast<v4f*>(&d1[c & 1][lr][i0]) = g;
+#pragma unroll
+      for (int t = 0; t < QT; ++t) {
+        const int rt = j * QT + t;
+        *reinterpret_cast<v4f*>(&eq[b][lr][32 * (rt >> 1) + 8 * lg + 4 * (rt & 1)]) = x[t];
+      }
     };
-    auto back = [&](int c) {   // to chunk c - 1
+    auto back = [&](int c) {   // chunk c's operands are used up: the next
       if (c > 0) {
         pp -= (size_t)p.Hv * (OUTS * 8 * kFrag);
+        qp -= kstep;
         gp -= (size_t)kChunk * ldo;
         dp -= p.Hv;
       }
-      load(c > 0 ? c - 1 : 0);
+      load(c > 0 || last >= kChunk);
     };
-    load(nc - 1);
-    put(nc - 1);
+    load(last >= kChunk);
+    put();
     __syncthreads();
-    product(nc - 1);
+    product((nc - 1) & 1);
     back(nc - 1);
     __syncthreads();
     for (int c = nc - 1; c >= 0; --c) {
       __syncthreads();
-      put(c + 1);        // chunk c - 1's slot: the parity of c + 1
+      put();       // chunk c - 1
       __syncthreads();
-      product(c + 1);
+      product((c + 1) & 1);
       back(c > 0 ? c - 1 : 0);
       __syncthreads();
-      const v4f dV = *reinterpret_cast<const v4f*>(&vs[lr][i0]);
-      if (at.colon) {
-        *reinterpret_cast<v4f*>(fp) = dV;
-        if (a.dv) {
-          const int n = rows(c);
-          if (n >= kChunk) {
+    }
+  } else if (nc > 0) {
+    const int j = wave - 6, cols = p.dv - at.col0;
+    T* op = a.dv ? (T*)a.dv + row1 * ldo + (size_t)at.h * p.dv + at.col0 : nullptr;
+    float* fp = reinterpret_cast<float*>(a.ws + p.off_dv) + (v0 * p.dv + at.col0) * kChunk;
+    float* zp = reinterpret_cast<float*>(a.ws + p.off_ds) + (v0 * p.dv + at.col0) * p.dk;
+    using A = Ahead<PARTS, OUTS, DKP, true>;
+    A ahead;
+    ahead.set(p, a, at, j * 64 + lane);
+    auto touch = [&](int c, unsigned (&h)[A::kTouch]) {
+      // the last chunk, where partial, is the first to be used: too late to touch
+      if (c >= 0) ahead.touch(c, h);
+    };
+    unsigned held[A::kSets][A::kTouch] = {};
+    touch(nc - 2, held[1]);
+    touch(nc - 3, held[2]);
+    __syncthreads();
+    __syncthreads();
+    for (int c4 = nc - 1; c4 >= 0; c4 -= A::kSets)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) op[ooff[e]] = from_f32<T>(dV[e]);
-          } else {
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-              if (i0 + e < n) op[ooff[e]] = from_f32<T>(dV[e]);
-          }
+      for (int u = 0; u < A::kSets; ++u) {
+        const int c = c4 - u;
+        if (c >= 0) {
+        A::settle(held[(u + 3) % A::kSets]);
+        touch(c - 3, held[(u + 3) % A::kSets]);
+        __syncthreads();
+        store_columns<DKP + 4>(zp, ss, p.dk, cols, j, lane);
+        zp -= (size_t)p.Hv * p.dk * p.dv;
+        __syncthreads();
+        __syncthreads();
+        store_columns<kLdF>(fp, vs, kChunk, cols, j, lane);
+        fp -= (size_t)p.Hv * kChunk * p.dv;
+        if (op) {
+          store_rows<T>(op, ldo, vs, cols, c == nc - 1 ? last : kChunk, j, lane);
+          op -= (size_t)kChunk * ldo;
+        }
         }
       }
-      fp -= (size_t)p.Hv * kChunk * p.dv;
-      op -= (size_t)kChunk * ldo;
-    }
   }
 }
 
