@@ -8,7 +8,7 @@
 namespace s4 {
 
 constexpr long kNormMaxD = 32768;      // a row of 16 waves, 32 values a lane
-constexpr long kNormParts = 512;       // blocks of the backward pass: two per CU
+constexpr long kNormBlocks = 2048;     // blocks of the forward pass over rows: eight a CU
 
 struct NormArgs {
   const void* x;
@@ -23,10 +23,12 @@ struct NormArgs {
 };
 
 // Blocks of the backward pass, the rows of its partial sums [2][parts][D]: one
-// per tile of work (4 rows, or 64 positions) up to kNormParts.
-inline long norm_parts(long outer, long inner) {
-  const long tiles = inner == 1 ? (outer + 3) / 4 : (outer * inner + 63) / 64;
-  return tiles < 1 ? 1 : tiles < kNormParts ? tiles : kNormParts;
+// per tile of work (a row, 4 rows up to 1024 values, or 64 positions) up to four a CU,
+// one where a row takes 16 waves.
+inline long norm_parts(long outer, long D, long inner) {
+  const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;
+  const long most = inner > 1 ? 512 : D > 4096 ? 256 : 1024;
+  return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s);

@@ -20,139 +20,205 @@ namespace {
 
 constexpr int kRowThreads = 256;
 
-// Sum over the WPR waves that share a row (WPR = 1: the wave's own lanes).
-template <int WPR>
-__device__ __forceinline__ float row_sum(float v, float* red) {
-  v = sum64(v);
-  if constexpr (WPR == 1) return v;
-  const int w = threadIdx.x >> 6;
-  if ((threadIdx.x & 63) == 0) red[w] = v;
-  __syncthreads();
-  float s = 0.f;
+// A lane's share of a row as it lies in memory: NV vectors, vector i at element
+// ((i WPR + wave) 64 + lane) VEC.  WHOLE: D is a multiple of VEC, so a vector is
+// inside or outside; one outside is read from the row's start and replaced by 0, with
+// no branch for the loads to wait at.
+template <typename T, int NV, int WPR, bool WHOLE>
+struct RowPart {
+  static constexpr int VEC = Vec<T>::N, E = NV * VEC;
+  Vec<T> v[NV];
+  __device__ __forceinline__ static int at(int i, int tid) { return (i * WPR * 64 + tid) * VEC; }
+  __device__ __forceinline__ void load(const T* __restrict__ p, int D, int tid) {
 #pragma unroll
-  for (int i = 0; i < WPR; ++i) s += red[i];
-  return s;
-}
-
-// A lane's share of a row: NV vectors, vector i at element ((i WPR + wave) 64 + lane) VEC.
-// Elements at and behind D read as 0.
-template <typename T, int NV, int WPR>
-__device__ __forceinline__ void load_row(const T* __restrict__ p, int D, int tid, float* out) {
-  constexpr int VEC = Vec<T>::N;
+    for (int i = 0; i < NV; ++i) {
+      const int c = at(i, tid);
+      if constexpr (WHOLE) {
+        v[i] = load_vec(p + (c < D ? c : 0));
+      } else if (c + VEC <= D) {
+        v[i] = load_vec(p + c);
+      } else {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * WPR * 64 + tid) * VEC;
-    if (c + VEC <= D) {
-      const Vec<T> v = load_vec(p + c);
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) out[i * VEC + j] = to_f32(v.v[j]);
-    } else {
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) out[i * VEC + j] = c + j < D ? to_f32(p[c + j]) : 0.f;
+        for (int j = 0; j < VEC; ++j) v[i].v[j] = c + j < D ? p[c + j] : (T)0.f;
+      }
     }
   }
-}
-
-template <typename T, int NV, int WPR>
-__device__ __forceinline__ void store_row(T* __restrict__ p, int D, int tid, const float* in) {
-  constexpr int VEC = Vec<T>::N;
+  __device__ __forceinline__ void get(int D, int tid, float* out) const {
 #pragma unroll
-  for (int i = 0; i < NV; ++i) {
-    const int c = (i * WPR * 64 + tid) * VEC;
-    if (c + VEC <= D) {
-      Vec<T> v;
-#pragma unroll
-      for (int j = 0; j < VEC; ++j) v.v[j] = from_f32<T>(in[i * VEC + j]);
-      store_vec(p + c, v);
-    } else {
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j)
-        if (c + j < D) p[c + j] = from_f32<T>(in[i * VEC + j]);
+        out[i * VEC + j] = !WHOLE || at(i, tid) < D ? to_f32(v[i].v[j]) : 0.f;
+  }
+  __device__ __forceinline__ static void store(T* __restrict__ p, int D, int tid, const float* in) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = at(i, tid);
+      if (c + VEC <= D) {
+        Vec<T> t;
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) t.v[j] = from_f32<T>(in[i * VEC + j]);
+        store_vec(p + c, t);
+      } else if constexpr (!WHOLE) {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j)
+          if (c + j < D) p[c + j] = from_f32<T>(in[i * VEC + j]);
+      }
     }
   }
-}
+  // the same columns of a vector of D floats; `other` where there is none
+  __device__ __forceinline__ static void columns(const float* __restrict__ p, int D, int tid,
+                                                 float other, float* out) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = at(i, tid);
+      if (p && c + VEC <= D) {
+        __builtin_memcpy(out + i * VEC, p + c, VEC * sizeof(float));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) out[i * VEC + j] = p && c + j < D ? p[c + j] : other;
+      }
+    }
+  }
+};
 
-// Forward over rows.  WPR waves hold one row in registers; a block of
-// max(256, 64 WPR) threads holds 4 rows (WPR = 1) or one.
-template <typename T, int NV, int WPR>
+// Forward over rows.  WPR waves share a row (blocks of 256 threads hold 4 rows at WPR =
+// 1), and a block walks over rows blockIdx, blockIdx + gridDim, ..., the next row on its
+// way while one is computed: gamma and beta are read once.  A wave takes mean and
+// squared deviations of its own part; the parts are joined by
+//   m = sum n_w m_w / D,  M = sum M_w + n_w (m_w - m)^2,
+// with one barrier a row (two sets of slots in turn).
+template <typename T, int NV, int WPR, bool WHOLE>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_kernel(
-    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ beta,
-    T* __restrict__ y, float* __restrict__ mean, float* __restrict__ rstd, long rows, int D,
-    float eps) {
-  constexpr int VEC = Vec<T>::N, E = NV * VEC;
+    const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* y,
+    float* __restrict__ mean, float* __restrict__ rstd, long rows, int D, float eps) {
+  using Part = RowPart<T, NV, WPR, WHOLE>;
+  constexpr int VEC = Part::VEC, E = Part::E;
   constexpr int RPB = WPR == 1 ? kRowThreads / 64 : 1;
-  __shared__ float red[2][WPR];
+  __shared__ float red[2][2][WPR];
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
-  const long row = (long)blockIdx.x * RPB + (WPR == 1 ? threadIdx.x >> 6 : 0);
+  const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  long row = (long)blockIdx.x * RPB + (WPR == 1 ? w : 0);
   if (row >= rows) return;   // WPR > 1: the whole block
-  float v[E], gm[E], bt[E];
-  load_row<T, NV, WPR>(x + row * D, D, tid, v);
+  Part next;
+  next.load(x + row * D, D, tid);
+  float gm[E], bt[E];
+  Part::columns(gamma, D, tid, 1.f, gm);
+  Part::columns(beta, D, tid, 0.f, bt);
+  // elements of the wave's part
+  float n = (float)D;
+  if constexpr (WPR > 1) {
+    int c = 0;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = (i * WPR * 64 + tid) * VEC + j;
-      gm[i * VEC + j] = gamma && c < D ? gamma[c] : 1.f;
-      bt[i * VEC + j] = beta && c < D ? beta[c] : 0.f;
+    for (int i = 0; i < NV; ++i) {
+      const int left = D - Part::at(i, 64 * w);
+      c += left < 0 ? 0 : left < 64 * VEC ? left : 64 * VEC;
     }
-  float s = 0.f;
+    n = (float)c;
+  }
+  int turn = 0;
+  for (; row < rows; turn ^= 1) {
+    float v[E];
+    next.get(D, tid, v);
+    const long here = row;
+    row += (long)gridDim.x * RPB;
+    if (row < rows) next.load(x + row * D, D, tid);
+    float s = 0.f, q = 0.f;
 #pragma unroll
-  for (int i = 0; i < E; ++i) s += v[i];
-  const float m = row_sum<WPR>(s, red[0]) / (float)D;
-  float q = 0.f;
+    for (int i = 0; i < E; ++i) s += v[i];
+    float m = n > 0.f ? sum64(s) / n : 0.f;
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i)
 #pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = (i * WPR * 64 + tid) * VEC + j;
-      const float d = v[i * VEC + j] - m;
-      v[i * VEC + j] = d;
-      q += c < D ? d * d : 0.f;
+      for (int j = 0; j < VEC; ++j) {
+        const float d = v[i * VEC + j] - m;
+        q += Part::at(i, tid) + j < D ? d * d : 0.f;
+      }
+    q = sum64(q);
+    if constexpr (WPR > 1) {
+      if (tid % 64 == 0) {
+        red[turn][0][w] = m;
+        red[turn][1][w] = q;
+      }
+      __syncthreads();
+      float part[WPR], len[WPR];
+      m = q = 0.f;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) {
+        int c = 0;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+          const int left = D - Part::at(i, 64 * k);
+          c += left < 0 ? 0 : left < 64 * VEC ? left : 64 * VEC;
+        }
+        len[k] = (float)c;
+        part[k] = red[turn][0][k];
+        m = fmaf(len[k], part[k], m);
+      }
+      m /= (float)D;
+#pragma unroll
+      for (int k = 0; k < WPR; ++k) {
+        const float d = part[k] - m;
+        q += fmaf(len[k] * d, d, red[turn][1][k]);
+      }
     }
-  const float r = 1.f / sqrtf(row_sum<WPR>(q, red[1]) / (float)D + eps);
+    const float r = 1.f / sqrtf(q / (float)D + eps);
 #pragma unroll
-  for (int i = 0; i < E; ++i) v[i] = fmaf(v[i] * r, gm[i], bt[i]);
-  store_row<T, NV, WPR>(y + row * D, D, tid, v);
-  if (tid == 0) {
-    if (mean) mean[row] = m;
-    if (rstd) rstd[row] = r;
+    for (int i = 0; i < E; ++i) v[i] = fmaf((v[i] - m) * r, gm[i], bt[i]);
+    Part::store(y + here * D, D, tid, v);
+    if (tid == 0) {
+      if (mean) mean[here] = m;
+      if (rstd) rstd[here] = r;
+    }
   }
 }
 
-// Backward over rows.  A block of 256 threads (1024 for WPR = 16) walks over
-// rows blockIdx, blockIdx + gridDim, ... ; every lane keeps the same columns, so
-// the columns' sums of dgamma and dbeta stay in its registers and leave the
-// block once, as row blockIdx of part [2][gridDim][D].
-template <typename T, int NV, int WPR>
+// Backward over rows.  A block walks over rows as in the forward pass; every lane
+// keeps the same columns, so the columns' sums of dgamma and dbeta stay in its
+// registers and leave the block once, as row blockIdx of part [2][gridDim][D].
+template <typename T, int NV, int WPR, bool WHOLE>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
     const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
     float* __restrict__ part, long rows, int D) {
-  constexpr int VEC = Vec<T>::N, E = NV * VEC;
+  using Part = RowPart<T, NV, WPR, WHOLE>;
+  constexpr int VEC = Part::VEC, E = Part::E;
   constexpr int RPB = WPR == 1 ? kRowThreads / 64 : 1;
   __shared__ float red[2][2][WPR];
   __shared__ float cols[WPR == 1 ? 3 * 64 * E : 1];
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int sub = WPR == 1 ? threadIdx.x >> 6 : 0;
   float gm[E], ag[E], ab[E];
+  Part nx, ng;
+  float nm = 0.f, nr = 0.f;
+  long row = (long)blockIdx.x * RPB + sub;
+  if (row < rows) {
+    nx.load(x + row * D, D, tid);
+    ng.load(dy + row * D, D, tid);
+    nm = mean[row];
+    nr = rstd[row];
+  }
+  Part::columns(gamma, D, tid, 1.f, gm);
 #pragma unroll
-  for (int i = 0; i < NV; ++i)
-#pragma unroll
-    for (int j = 0; j < VEC; ++j) {
-      const int c = (i * WPR * 64 + tid) * VEC + j;
-      gm[i * VEC + j] = gamma && c < D ? gamma[c] : 1.f;
-      ag[i * VEC + j] = ab[i * VEC + j] = 0.f;
-    }
+  for (int i = 0; i < E; ++i) ag[i] = ab[i] = 0.f;
   int turn = 0;
-  for (long row = (long)blockIdx.x * RPB + sub; row < rows; row += (long)gridDim.x * RPB, turn ^= 1) {
+  for (; row < rows; turn ^= 1) {
     float xv[E], gv[E];
-    load_row<T, NV, WPR>(x + row * D, D, tid, xv);
-    load_row<T, NV, WPR>(dy + row * D, D, tid, gv);
-    const float m = mean[row], r = rstd[row];
+    nx.get(D, tid, xv);
+    ng.get(D, tid, gv);
+    const float m = nm, r = nr;
+    const long here = row;
+    row += (long)gridDim.x * RPB;
+    if (row < rows) {
+      nx.load(x + row * D, D, tid);
+      ng.load(dy + row * D, D, tid);
+      nm = mean[row];
+      nr = rstd[row];
+    }
     float s1 = 0.f, s2 = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) {
-      // behind D, dy = 0 there: nothing is added
+      // behind D, dy = 0: nothing is added
       const float xh = (xv[i] - m) * r, w = gv[i] * gm[i];
       xv[i] = xh;
       s1 += w;
@@ -162,7 +228,6 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
       gv[i] = w;
     }
     if (dx) {
-      // two sets of slots in turn, so one barrier a row is enough
       s1 = sum64(s1);
       s2 = sum64(s2);
       if constexpr (WPR > 1) {
@@ -182,7 +247,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
       s2 /= (float)D;
 #pragma unroll
       for (int i = 0; i < E; ++i) gv[i] = r * (gv[i] - s1 - xv[i] * s2);
-      store_row<T, NV, WPR>(dx + row * D, D, tid, gv);
+      Part::store(dx + here * D, D, tid, gv);
     }
   }
   if (!part) return;
@@ -204,38 +269,43 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
         a[i] += (cols[i * 64 + tid] + cols[(E + i) * 64 + tid]) + cols[(2 * E + i) * 64 + tid];
     }
 #pragma unroll
-    for (int i = 0; i < NV; ++i)
+    for (int i = 0; i < NV; ++i) {
+      const int c = Part::at(i, tid);
+      float* o = (half ? pb : pg) + c;
+      if (c + VEC <= D) {
+        __builtin_memcpy(o, a + i * VEC, VEC * sizeof(float));
+      } else {
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) {
-        const int c = (i * WPR * 64 + tid) * VEC + j;
-        if (c < D) (half ? pb : pg)[c] = a[i * VEC + j];
+        for (int j = 0; j < VEC; ++j)
+          if (c + j < D) o[j] = a[i * VEC + j];
       }
+    }
   }
 }
 
 // dgamma[c] = sum_b part[0][b][c], dbeta[c] = sum_b part[1][b][c], always in the
-// same order.  Block: 64 columns; 16 waves share the partial rows.
+// same order.  Block: 32 columns (a line); 32 groups of lanes share the partial rows.
 __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restrict__ part, int nb,
                                                             int D, float* __restrict__ dgamma,
                                                             float* __restrict__ dbeta) {
-  __shared__ float red[16][64];
-  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
-  const int c = blockIdx.x * 64 + lane;
+  __shared__ float red[32][33];
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  const int c = blockIdx.x * 32 + lane;
   float* out = blockIdx.y ? dbeta : dgamma;
   if (!out) return;
   const float* p = part + (size_t)blockIdx.y * nb * D;
   float s = 0.f;
   if (c < D)
-#pragma unroll 4
-    for (int b = w; b < nb; b += 16) s += p[(size_t)b * D + c];
+#pragma unroll 8
+    for (int b = w; b < nb; b += 32) s += p[(size_t)b * D + c];
   red[w][lane] = s;
   __syncthreads();
-  if (w == 0 && c < D) {
-    float t = 0.f;
+  // group w adds up column w
+  float t = red[lane][w];
 #pragma unroll
-    for (int i = 0; i < 16; ++i) t += red[i][lane];
-    out[c] = t;
-  }
+  for (int off = 16; off >= 1; off >>= 1) t += __shfl_xor(t, off);
+  const int col = blockIdx.x * 32 + w;
+  if (lane == 0 && col < D) out[col] = t;
 }
 
 // ------------------------------------------------------- inner > 1: channels
@@ -424,18 +494,20 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
 
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
-// Vectors a lane holds and waves a row takes: one wave up to 2 vectors a lane
-// (forward 4), then 4 waves, then 16.
-template <typename T, int MAX1, typename F>
+// Vectors a lane holds and waves a row takes: one wave up to 2 vectors a lane, then
+// 4 waves, then 16.
+template <typename T, typename F>
 void row_shape(int D, F f) {
   const int vecs = (int)ceil_div(D, 64 * Vec<T>::N);
+  const bool whole = D % Vec<T>::N == 0;
   using std::integral_constant;
-#define S4_CASE(nv, wpr) f(integral_constant<int, nv>(), integral_constant<int, wpr>())
+  using Yes = std::true_type;
+  using No = std::false_type;
+#define S4_CASE(nv, wpr)                                                                 \
+  (whole ? f(integral_constant<int, nv>(), integral_constant<int, wpr>(), Yes())         \
+         : f(integral_constant<int, nv>(), integral_constant<int, wpr>(), No()))
   if (vecs <= 1) return S4_CASE(1, 1);
   if (vecs <= 2) return S4_CASE(2, 1);
-  if constexpr (MAX1 >= 4) {
-    if (vecs <= 4) return S4_CASE(4, 1);
-  }
   if (vecs <= 4) return S4_CASE(1, 4);
   if (vecs <= 8) return S4_CASE(2, 4);
   if (vecs <= 16) return S4_CASE(4, 4);
@@ -451,12 +523,14 @@ hipError_t fwd(const NormArgs& a, hipStream_t s) {
   T* y = (T*)a.y;
   const int D = (int)a.D;
   if (a.inner == 1) {
-    row_shape<T, 4>(D, [&](auto nv, auto wpr) {
+    row_shape<T>(D, [&](auto nv, auto wpr, auto whole) {
       constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
+      constexpr bool W = decltype(whole)::value;
       const long blocks = WPR == 1 ? ceil_div(a.outer, kRowThreads / 64) : a.outer;
-      norm_rows_kernel<T, NV, WPR><<<dim3((unsigned)blocks), WPR > 4 ? 64 * WPR : kRowThreads, 0,
-                                     s>>>(x, a.gamma, a.beta, y, a.mean, a.rstd, a.outer, D,
-                                          a.eps);
+      const long most = WPR > 4 ? kNormBlocks / 4 : kNormBlocks;
+      norm_rows_kernel<T, NV, WPR, W>
+          <<<dim3((unsigned)(blocks < most ? blocks : most)), WPR > 4 ? 64 * WPR : kRowThreads, 0,
+             s>>>(x, a.gamma, a.beta, y, a.mean, a.rstd, a.outer, D, a.eps);
     });
     return hipGetLastError();
   }
@@ -479,12 +553,14 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
   const int D = (int)a.D;
   const bool sums = a.dgamma || a.dbeta;
   float* part = sums ? a.part : nullptr;
-  const int nb = (int)norm_parts(a.outer, a.inner);
+  const int nb = (int)norm_parts(a.outer, a.D, a.inner);
   if (a.inner == 1) {
-    row_shape<T, 2>(D, [&](auto nv, auto wpr) {
+    row_shape<T>(D, [&](auto nv, auto wpr, auto whole) {
       constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
-      norm_rows_bwd_kernel<T, NV, WPR><<<dim3(nb), WPR > 4 ? 64 * WPR : kRowThreads, 0, s>>>(
-          x, a.gamma, a.mean, a.rstd, dy, dx, part, a.outer, D);
+      constexpr bool W = decltype(whole)::value;
+      norm_rows_bwd_kernel<T, NV, WPR, W>
+          <<<dim3(nb), WPR > 4 ? 64 * WPR : kRowThreads, 0, s>>>(x, a.gamma, a.mean, a.rstd, dy, dx,
+                                                                 part, a.outer, D);
     });
   } else {
 #define S4_GO(ept)                                                                   \
@@ -497,7 +573,7 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sums) return e;
-  norm_columns_kernel<<<dim3((unsigned)ceil_div(D, 64), 2), 1024, 0, s>>>(part, nb, D, a.dgamma,
+  norm_columns_kernel<<<dim3((unsigned)ceil_div(D, 32), 2), 1024, 0, s>>>(part, nb, D, a.dgamma,
                                                                          a.dbeta);
   return hipGetLastError();
 }

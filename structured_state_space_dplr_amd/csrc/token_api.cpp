@@ -60,7 +60,7 @@ s4dplr_status norm_shape(long outer, long D, long inner) {
 }
 
 size_t norm_part_bytes(long outer, long D, long inner) {
-  return align_up(sizeof(float) * 2 * (size_t)s4::norm_parts(outer, inner) * (size_t)D);
+  return align_up(sizeof(float) * 2 * (size_t)s4::norm_parts(outer, D, inner) * (size_t)D);
 }
 
 }  // namespace

@@ -55,12 +55,14 @@ __device__ __forceinline__ float sum16(float v) {
   return v;
 }
 
-// Sum over the 64 lanes, in every lane.
+// Sum over the 64 lanes, in every lane: rows 0 + 1 and 2 + 3, then the halves (the
+// swaps hand over the other row or half).
 __device__ __forceinline__ float sum64(float v) {
   v = sum16(v);
-  v += __shfl_xor(v, 16);
-  v += __shfl_xor(v, 32);
-  return v;
+  const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  v = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+  const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return __uint_as_float(b[0]) + __uint_as_float(b[1]);
 }
 
 }  // namespace s4
