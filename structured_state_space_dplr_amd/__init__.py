@@ -431,6 +431,9 @@ def _tensor(t, name, dtype, shape, device=None, optional=False):
     """Device pointer of a contiguous GPU tensor of that dtype and shape."""
     if t is None and optional:
         return None
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous() and t.is_cuda and (device is None or t.device == device):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -438,7 +441,7 @@ def _tensor(t, name, dtype, shape, device=None, optional=False):
     if t.dtype != dtype:
         raise TypeError(f"{name}: must be {dtype}, got {t.dtype}")
     if tuple(t.shape) != shape:
-        raise ValueError(f"{name}: expected shape {shape}, got {tuple(t.shape)}")
+        raise ValueError(f"{name}: expected shape {tuple(shape)}, got {tuple(t.shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{name}: must be contiguous")
     if device is not None and t.device != device:
@@ -449,6 +452,9 @@ def _tensor(t, name, dtype, shape, device=None, optional=False):
 def _rows(t, name, dtype, shape, device):
     """Device pointer and row pitch of a [rows, heads, d] tensor whose rows are
     contiguous (a column range of a wider matrix will do)."""
+    if type(t) is torch.Tensor and t.dtype is dtype and t.shape == shape and \
+            t.is_contiguous() and t.is_cuda and t.device == device:
+        return t.data_ptr(), shape[1] * shape[2]
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if not t.is_cuda:
@@ -467,15 +473,21 @@ def _rows(t, name, dtype, shape, device):
     return t.data_ptr(), sr if n > 1 else heads * d
 
 
-def _launch(device, stream, call):
-    """``call(stream)`` with ``device`` current."""
-    if device.index is None or device.index == torch.cuda.current_device():
-        return call(_stream(stream))
+def _launch(device, stream, fn, args):
+    """``fn(*args, stream)`` with ``device`` current."""
+    index = device.index
+    # the raw handle of the device's current stream, without a Stream object
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
+    if index == torch.cuda.current_device():
+        return fn(*args, raw)
     with torch.cuda.device(device):
-        return call(_stream(stream))
+        return fn(*args, raw)
 
 
 def _workspace(ws, name, need, device):
+    if type(ws) is torch.Tensor and ws.dtype is torch.uint8 and ws.device == device and \
+            ws.is_contiguous() and ws.numel() >= need:
+        return ws.data_ptr()
     if not isinstance(ws, torch.Tensor):
         raise TypeError(f"{name}: expected a torch.Tensor")
     if ws.device != device:
@@ -498,8 +510,10 @@ def _norm_dims(x, axis):
         raise TypeError("x: expected a torch.Tensor")
     if x.dtype not in _DTYPES:
         raise TypeError(f"x: must be float32, bfloat16 or float16, got {x.dtype}")
-    shape = tuple(x.shape)
+    shape = x.shape
     axis = axis + len(shape) if axis < 0 else axis
+    if axis == 1 and len(shape) == 2:
+        return shape[0], shape[1], 1, shape[:1]
     if not 0 <= axis < len(shape):
         raise ValueError(f"axis: out of range for {len(shape)} dimensions")
     outer = inner = 1
@@ -519,15 +533,16 @@ def layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, a
     ``layer_norm_bwd`` reads.  gamma, beta: [D] float32 or None (1 and 0)."""
     outer, D, inner, stat = _norm_dims(x, axis)
     dev = x.device
-    _validate("layer_norm_fwd", x=x, gamma=gamma, beta=beta)
+    if validation_enabled():
+        check_preconditions("layer_norm_fwd", x=x, gamma=gamma, beta=beta)
     f32 = torch.float32
-    args = (_tensor(x, "x", x.dtype, tuple(x.shape)),
+    args = (_tensor(x, "x", x.dtype, x.shape),
             _tensor(gamma, "gamma", f32, (D,), dev, True),
             _tensor(beta, "beta", f32, (D,), dev, True),
-            _tensor(y, "y", x.dtype, tuple(x.shape), dev),
+            _tensor(y, "y", x.dtype, x.shape, dev),
             _tensor(mean, "mean", f32, stat, dev, True),
             _tensor(rstd, "rstd", f32, stat, dev, True), outer, D, inner, eps, _DTYPES[x.dtype])
-    _check(_launch(dev, stream, lambda st: _lib.s4dplr_layer_norm_fwd(*args, st)),
+    _check(_launch(dev, stream, _lib.s4dplr_layer_norm_fwd, args),
            "layer_norm_fwd")
 
 
@@ -546,8 +561,9 @@ def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = 
     ``ws``: a 256-byte aligned GPU tensor of ``layer_norm_workspace_bytes``."""
     outer, D, inner, stat = _norm_dims(x, axis)
     dev = x.device
-    _validate("layer_norm_bwd", x=x, gamma=gamma, dy=dy)
-    f32, full = torch.float32, tuple(x.shape)
+    if validation_enabled():
+        check_preconditions("layer_norm_bwd", x=x, gamma=gamma, dy=dy)
+    f32, full = torch.float32, x.shape
     n = ctypes.c_size_t()
     _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)),
            "layer_norm_bwd")
@@ -557,7 +573,7 @@ def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = 
             _tensor(dgamma, "dgamma", f32, (D,), dev, True),
             _tensor(dbeta, "dbeta", f32, (D,), dev, True), outer, D, inner, _DTYPES[x.dtype],
             _workspace(ws, "ws", n.value, dev))
-    _check(_launch(dev, stream, lambda st: _lib.s4dplr_layer_norm_bwd(*args, st)),
+    _check(_launch(dev, stream, _lib.s4dplr_layer_norm_bwd, args),
            "layer_norm_bwd")
 
 
@@ -582,6 +598,9 @@ class DeltaPlan:
         _check(_lib.s4dplr_delta_plan_bytes(self.handle, ctypes.byref(a), ctypes.byref(b)),
                "delta_plan_bytes")
         self.workspace_bytes, self.saved_bytes = a.value, b.value
+        self._keys, self._vals = (tokens, Hk, dk), (tokens, Hv, dv)
+        self._heads, self._states = (tokens, Hv), (sequences, Hv, dk, dv)
+        self._scale = dk ** -0.5
         self.device = torch.device("cuda" if device is None else device)
         self._ws = None
 
@@ -623,15 +642,15 @@ def _delta_inputs(where, plan, q, k, v, g, beta, ws, scale, offsets):
         if bool(bad.any()):
             idx = tuple(int(i) for i in bad.nonzero()[0])
             raise S4DPLRPreconditionError(where, f"g must be <= 0, not so at index {idx}")
-    n, dev, dt, f32 = plan.tokens, v.device, plan.dtype, torch.float32
-    keys, heads = (n, plan.Hk, plan.dk), (n, plan.Hv)
+    dev, dt, f32 = v.device, plan.dtype, torch.float32
+    keys, heads = plan._keys, plan._heads
     off = None
     if offsets is not None:
         off = _tensor(offsets, "offsets", torch.int32, (plan.sequences + 1,), dev)
     return dev, (plan.handle, *_rows(q, "q", dt, keys, dev), *_rows(k, "k", dt, keys, dev),
-                 *_rows(v, "v", dt, (n, plan.Hv, plan.dv), dev),
+                 *_rows(v, "v", dt, plan._vals, dev),
                  _tensor(g, "g", f32, heads, dev), _tensor(beta, "beta", f32, heads, dev), off,
-                 plan.dk ** -0.5 if scale is None else float(scale)), \
+                 plan._scale if scale is None else float(scale)), \
         _workspace(ws, "ws", plan.workspace_bytes, dev)
 
 
@@ -646,13 +665,12 @@ def delta_fwd(plan: "DeltaPlan", q, k, v, g, beta, state, o, state_out, ws, save
     lengths.  scale: None is dk ** -0.5.  saved: ``plan.saved()`` for a later
     ``delta_bwd``."""
     dev, args, w = _delta_inputs("delta_fwd", plan, q, k, v, g, beta, ws, scale, offsets)
-    st = (plan.sequences, plan.Hv, plan.dk, plan.dv)
-    f32 = torch.float32
+    st, f32 = plan._states, torch.float32
     args += (_tensor(state, "state", f32, st, dev, True),
-             _tensor(o, "o", plan.dtype, (plan.tokens, plan.Hv, plan.dv), dev),
+             _tensor(o, "o", plan.dtype, plan._vals, dev),
              _tensor(state_out, "state_out", f32, st, dev, True),
              None if saved is None else _workspace(saved, "saved", plan.saved_bytes, dev), w)
-    _check(_launch(dev, stream, lambda s: _lib.s4dplr_delta_fwd(*args, s)), "delta_fwd")
+    _check(_launch(dev, stream, _lib.s4dplr_delta_fwd, args), "delta_fwd")
 
 
 def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, dk, dv, dg, dbeta,
@@ -661,9 +679,8 @@ def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, 
     it filled, from ``dout`` and ``dstate_out`` (None: zeros); any of dq, dk, dv,
     dg, dbeta, dstate may be None."""
     dev, args, w = _delta_inputs("delta_bwd", plan, q, k, v, g, beta, ws, scale, offsets)
-    n, dt, f32 = plan.tokens, plan.dtype, torch.float32
-    st = (plan.sequences, plan.Hv, plan.dk, plan.dv)
-    keys, vals, heads = (n, plan.Hk, plan.dk), (n, plan.Hv, plan.dv), (n, plan.Hv)
+    dt, f32 = plan.dtype, torch.float32
+    st, keys, vals, heads = plan._states, plan._keys, plan._vals, plan._heads
     args += (_workspace(saved, "saved", plan.saved_bytes, dev),
              _tensor(dout, "dout", dt, vals, dev),
              _tensor(dstate_out, "dstate_out", f32, st, dev, True),
@@ -671,4 +688,4 @@ def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, 
              _tensor(dv, "dv", dt, vals, dev, True), _tensor(dg, "dg", f32, heads, dev, True),
              _tensor(dbeta, "dbeta", f32, heads, dev, True),
              _tensor(dstate, "dstate", f32, st, dev, True), w)
-    _check(_launch(dev, stream, lambda s: _lib.s4dplr_delta_bwd(*args, s)), "delta_bwd")
+    _check(_launch(dev, stream, _lib.s4dplr_delta_bwd, args), "delta_bwd")
