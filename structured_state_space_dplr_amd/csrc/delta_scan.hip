@@ -1,5 +1,6 @@
 // Gated delta rule, chunked form, stage 2: the chunks of a sequence one after
-// another.  A block carries DS columns of one head's dk x dv state S through them:
+// another.  A block carries DS = 16 or 32 columns of one head's dk x dv state S through
+// them:
 //   R = V - e . (K S),  N = X R,  U = beta . N,
 //   O = scale e . (Q S) + (scale P) U,  S <- e_last S + K^T (d . U).
 //
@@ -21,7 +22,6 @@ namespace s4 {
 
 namespace {
 
-constexpr int DS = 16;
 constexpr int kLdT = kChunk + 8;   // bf16 from column to column of a chunk-long operand
 constexpr int kLdF = kChunk + 4;   // fp32 likewise
 
@@ -40,11 +40,12 @@ struct Own {
 
 // What both scans start from.
 struct Place {
-  int sh, h, hk, nc, slice, slices, col0, col, ccol, lr, lg;
-  bool colon;
+  __device__ __forceinline__ int col(int u) const { return col0 + 16 * u + lr; }
+  int sh, h, hk, nc, slice, slices, col0, lr, lg;
   Rows r;
   long slot0;
 };
+template <int DS>
 __device__ __forceinline__ bool place_of(const s4dplr_delta_plan& p, const DeltaArgs& a, int lane,
                                          Place* o) {
   o->slices = (p.dv + DS - 1) / DS;
@@ -58,16 +59,13 @@ __device__ __forceinline__ bool place_of(const s4dplr_delta_plan& p, const Delta
   o->lr = lane & 15;
   o->lg = lane >> 4;
   o->col0 = o->slice * DS;
-  o->col = o->col0 + o->lr;
-  o->colon = o->col < p.dv;
-  o->ccol = o->colon ? o->col : 0;
   return true;
 }
 
 // The wave's rows of a state [dk][dv] in fp32: tile t of k step k, accumulator entry e,
 // is row 32 k + 8 lg + 4 t + e.
 template <int KW>
-__device__ __forceinline__ void load_state(v4f (&S)[KW][2], const float* state, int k0,
+__device__ __forceinline__ void load_state(v4f (&S)[KW][2], const float* state, int k0, int col,
                                            const s4dplr_delta_plan& p, const Place& at) {
 #pragma unroll
   for (int i = 0; i < KW; ++i)
@@ -76,14 +74,14 @@ __device__ __forceinline__ void load_state(v4f (&S)[KW][2], const float* state, 
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int d = 32 * (k0 + i) + 8 * at.lg + 4 * t + e;
-        S[i][t][e] = state && at.colon && d < p.dk
-                         ? state[((size_t)at.sh * p.dk + d) * p.dv + at.col] : 0.f;
+        S[i][t][e] = state && col < p.dv && d < p.dk
+                         ? state[((size_t)at.sh * p.dk + d) * p.dv + col] : 0.f;
       }
 }
 template <int KW>
-__device__ __forceinline__ void store_state(const v4f (&S)[KW][2], float* state, int k0,
+__device__ __forceinline__ void store_state(const v4f (&S)[KW][2], float* state, int k0, int col,
                                             const s4dplr_delta_plan& p, const Place& at) {
-  if (!state || !at.colon) return;
+  if (!state || col >= p.dv) return;
 #pragma unroll
   for (int i = 0; i < KW; ++i)
 #pragma unroll
@@ -91,7 +89,7 @@ __device__ __forceinline__ void store_state(const v4f (&S)[KW][2], float* state,
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int d = 32 * (k0 + i) + 8 * at.lg + 4 * t + e;
-        if (d < p.dk) state[((size_t)at.sh * p.dk + d) * p.dv + at.col] = S[i][t][e];
+        if (d < p.dk) state[((size_t)at.sh * p.dk + d) * p.dv + col] = S[i][t][e];
       }
 }
 // The rows of a k step as an operand of three parts.
@@ -105,14 +103,14 @@ __device__ __forceinline__ void state_operand(const v4f (&S)[2], v8bf (&out)[3])
   split8<3>(x, out);
 }
 
-template <int N>
+template <int N, int DS>
 __device__ __forceinline__ void put4(__bf16 (*to)[DS][kLdT], v4f x, int lr, int i0) {
   v4bf t[N];
   split4<N>(x, t);
 #pragma unroll
   for (int q = 0; q < N; ++q) *reinterpret_cast<v4bf*>(&to[q][lr][i0]) = t[q];
 }
-template <int N>
+template <int N, int DS>
 __device__ __forceinline__ void get8(const __bf16 (*from)[DS][kLdT], v8bf (&x)[N], int lr, int k) {
 #pragma unroll
   for (int q = 0; q < N; ++q) x[q] = *reinterpret_cast<const v8bf*>(&from[q][lr][k]);
@@ -120,8 +118,8 @@ __device__ __forceinline__ void get8(const __bf16 (*from)[DS][kLdT], v8bf (&x)[N
 
 // The storing waves: j = 0, 1.  A matrix [DS][LD] in LDS to [dv][n] in memory (`to`:
 // the slice's first column), rows of n floats.
-template <int LD>
-__device__ __forceinline__ void store_columns(float* to, const float (*m)[LD], int n, int cols,
+template <int LD, int DS>
+__device__ __forceinline__ void store_columns(float* to, const float (&m)[DS][LD], int n, int cols,
                                               int j, int lane) {
   constexpr int G = (LD - 4) / 4;   // groups of 4 a column
 #pragma unroll
@@ -140,7 +138,7 @@ __device__ __forceinline__ void store_columns(float* to, const float (*m)[LD], i
   }
 }
 // The state's columns from its three parts in LDS (their sum is exact) to [dv][dk].
-template <int DKP>
+template <int DKP, int DS>
 __device__ __forceinline__ void store_parts(float* to, const __bf16 (*m)[DS][DKP + 8], int dk,
                                             int cols, int j, int lane) {
 #pragma unroll
@@ -156,21 +154,25 @@ __device__ __forceinline__ void store_parts(float* to, const __bf16 (*m)[DS][DKP
   }
 }
 // A chunk's rows from LDS [column][row] to memory: 8 columns of one row a lane.
-template <typename T>
-__device__ __forceinline__ void store_rows(T* to, unsigned ld, const float (*m)[kLdF], int cols,
+template <typename T, int DS>
+__device__ __forceinline__ void store_rows(T* to, unsigned ld, const float (&m)[DS][kLdF], int cols,
                                            int n, int j, int lane) {
-  const int row = j * 32 + (lane >> 1), c = (lane & 1) * 8;
-  T t[8];
+  constexpr int G = DS / 8;   // lanes a row
 #pragma unroll
-  for (int q = 0; q < 8; ++q) t[q] = from_f32<T>(m[c + q][row]);
-  if (row >= n) return;
-  T* o = to + (unsigned)(row * ld + c);
-  if (c + 8 <= cols) {
-    __builtin_memcpy(o, t, sizeof(t));
-  } else {
+  for (int i = 0; i < DS / 16; ++i) {
+    const int at = (i * 2 + j) * 64 + lane, row = at / G, c = at % G * 8;
+    T t[8];
 #pragma unroll
-    for (int q = 0; q < 8; ++q)
-      if (c + q < cols) o[q] = t[q];
+    for (int q = 0; q < 8; ++q) t[q] = from_f32<T>(m[c + q][row]);
+    if (row >= n) continue;
+    T* o = to + (unsigned)(row * ld + c);
+    if (c + 8 <= cols) {
+      __builtin_memcpy(o, t, sizeof(t));
+    } else {
+#pragma unroll
+      for (int q = 0; q < 8; ++q)
+        if (c + q < cols) o[q] = t[q];
+    }
   }
 }
 
@@ -247,11 +249,11 @@ struct Ahead {
 
 }  // namespace
 
-template <typename T, int PARTS, int OUTS, int DKP, bool SAVE>
+template <typename T, int PARTS, int OUTS, int DKP, bool SAVE, int DS>
 __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan p,
                                                          const DeltaArgs a) {
   using O = Own<DKP>;
-  constexpr int KS = O::KS, KW = O::KW, RT = O::RT;
+  constexpr int KS = O::KS, KW = O::KW, RT = O::RT, NT = DS / 16;   // NT: column tiles
   __shared__ __attribute__((aligned(16))) float pk[O::WAVES][DS][kLdF];   // K S, by owner
   __shared__ __attribute__((aligned(16))) float os[DS][kLdF];             // O
   __shared__ __attribute__((aligned(16))) float ns[SAVE ? DS : 1][kLdF];  // N
@@ -261,7 +263,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
   __shared__ __attribute__((aligned(16))) __bf16 du[3][DS][kLdT];         // d . U
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place at;
-  if (!place_of(p, a, lane, &at) || at.r.len <= a.step_tokens) return;
+  if (!place_of<DS>(p, a, lane, &at) || at.r.len <= a.step_tokens) return;
   const int lr = at.lr, lg = at.lg, nc = at.nc;
   constexpr size_t kbytes = (size_t)PARTS * 4 * KS * kFrag;
   const size_t k0 = ((size_t)at.slot0 * p.Hk + at.hk) * kbytes;
@@ -274,22 +276,26 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
   if (wave < 4) {
     __builtin_amdgcn_s_setprio(1);
     const int w = wave, i0 = 16 * w + 4 * lg, kw = O::kw(w) * KW, rt0 = O::rt(w);
-    v4f S[KW][2];
-    load_state<KW>(S, a.state, kw, p, at);
+    v4f S[NT][KW][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) load_state<KW>(S[u], a.state, kw, at.col(u), p, at);
 
     // Operands of one chunk, each set loaded right after its last use.
     v8bf ka[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS];
     v4f ev, dv, bv;
     float el;
-    T vv[4];
+    T vv[NT][4];
     const unsigned char* kp = a.ws + p.off_k + k0 + (size_t)(rt0 * KS + kw) * kFrag;
     const unsigned char* tp = a.ws + p.off_kt + k0 + (size_t)kw * 4 * kFrag;
     const unsigned char* xp = a.ws + p.off_x + v0 * (3 * 8 * kFrag) + (size_t)w * 2 * kFrag;
     const T* vp = (const T*)a.v + at.r.start * a.ldv + (size_t)at.h * p.dv;
     const unsigned ldv = (unsigned)a.ldv;
-    unsigned voff[4];
+    // columns behind dv read column 0: nothing of theirs is stored
+    unsigned voff[4], vcol[NT];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) voff[e] = (unsigned)(i0 + e) * ldv + at.ccol;
+    for (int e = 0; e < 4; ++e) voff[e] = (unsigned)(i0 + e) * ldv;
+#pragma unroll
+    for (int u = 0; u < NT; ++u) vcol[u] = at.col(u) < p.dv ? at.col(u) : 0;
     auto load_k = [&] {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
@@ -322,11 +328,15 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
     auto load_v = [&](int n) {
       if (n >= kChunk) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) vv[e] = vp[voff[e]];
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) vv[u][e] = vp[voff[e] + vcol[u]];
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          vv[e] = vp[(unsigned)(i0 + e < n ? i0 + e : n - 1) * ldv + at.ccol];
+        for (int u = 0; u < NT; ++u)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            vv[u][e] = vp[(unsigned)(i0 + e < n ? i0 + e : n - 1) * ldv + vcol[u]];
       }
     };
     auto load_d = [&] {
@@ -352,77 +362,83 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
         dp += p.Hv;
         vp += (size_t)kChunk * ldv;
       }
-      {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
         v4f x[RT];
 #pragma unroll
         for (int t = 0; t < RT; ++t) x[t] = zero;
 #pragma unroll
         for (int i = 0; i < KW; ++i) {
           v8bf sb[3];
-          state_operand(S[i], sb);
+          state_operand(S[u][i], sb);
 #pragma unroll
           for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(ka[i][t], sb, x[t]);
           if (O::first(w))
 #pragma unroll
             for (int q = 0; q < 3; ++q)
-              *reinterpret_cast<v8bf*>(&st[q][lr][32 * (kw + i) + 8 * lg]) = sb[q];
+              *reinterpret_cast<v8bf*>(&st[q][16 * u + lr][32 * (kw + i) + 8 * lg]) = sb[q];
         }
 #pragma unroll
         for (int t = 0; t < RT; ++t)
-          *reinterpret_cast<v4f*>(&pk[O::kw(w)][lr][16 * (rt0 + t) + 4 * lg]) = x[t];
+          *reinterpret_cast<v4f*>(&pk[O::kw(w)][16 * u + lr][16 * (rt0 + t) + 4 * lg]) = x[t];
       }
       __syncthreads();
-      {
-        v4f ks[O::WAVES];
+      load_k();
 #pragma unroll
-        for (int i = 0; i < O::WAVES; ++i) ks[i] = *reinterpret_cast<const v4f*>(&pk[i][lr][i0]);
-        load_k();
+      for (int u = 0; u < NT; ++u) {
+        v4f sum = *reinterpret_cast<const v4f*>(&pk[0][16 * u + lr][i0]);
+#pragma unroll
+        for (int i = 1; i < O::WAVES; ++i)
+          sum += *reinterpret_cast<const v4f*>(&pk[i][16 * u + lr][i0]);
         v4f R;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) R[e] = to_f32(vv[e]);
-        v4f sum = ks[0] + ks[1];
-        if constexpr (O::WAVES == 4) sum += ks[2] + ks[3];
-        put4<3>(rt, R - ev * sum, lr, i0);
+        for (int e = 0; e < 4; ++e) R[e] = to_f32(vv[u][e]);
+        put4<3>(rt, R - ev * sum, 16 * u + lr, i0);
       }
       load_v(n);
       __syncthreads();
-      v4f N = zero, n1 = zero;
-      {
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        v4f N = zero, n1 = zero;
         v8bf rb[3], rc[3];
-        get8<3>(rt, rb, lr, lg * 8);
+        get8<3>(rt, rb, 16 * u + lr, lg * 8);
         if (w >= 2) {
-          get8<3>(rt, rc, lr, 32 + lg * 8);
+          get8<3>(rt, rc, 16 * u + lr, 32 + lg * 8);
           n1 = mfma_parts<3>(xa[1], rc, n1);
         }
         N = mfma_parts<3>(xa[0], rb, N);
         N += n1;
-      }
-      {
         const v4f U = bv * N;
-        put4<3>(du, dv * U, lr, i0);
-        put4<OUTS>(ut, U, lr, i0);
-        if constexpr (SAVE) *reinterpret_cast<v4f*>(&ns[lr][i0]) = N;
+        put4<3>(du, dv * U, 16 * u + lr, i0);
+        put4<OUTS>(ut, U, 16 * u + lr, i0);
+        if constexpr (SAVE) *reinterpret_cast<v4f*>(&ns[16 * u + lr][i0]) = N;
       }
       load_x();
       __syncthreads();
-      v8bf ub[2][3];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) get8<3>(du, ub[ks], lr, ks * 32 + lg * 8);
+      for (int u = 0; u < NT; ++u) {
+        v8bf ub[2][3];
 #pragma unroll
-      for (int i = 0; i < KW; ++i)
-#pragma unroll
-        for (int t = 0; t < 2; ++t) S[i][t] *= el;
-#pragma unroll
-      for (int ks = 0; ks < 2; ++ks)
+        for (int ks = 0; ks < 2; ++ks) get8<3>(du, ub[ks], 16 * u + lr, ks * 32 + lg * 8);
 #pragma unroll
         for (int i = 0; i < KW; ++i)
 #pragma unroll
-          for (int t = 0; t < 2; ++t) S[i][t] = mfma_parts<3>(ta[i][t][ks], ub[ks], S[i][t]);
+          for (int t = 0; t < 2; ++t) S[u][i][t] *= el;
+#pragma unroll
+        for (int ks = 0; ks < 2; ++ks)
+#pragma unroll
+          for (int i = 0; i < KW; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              S[u][i][t] = mfma_parts<3>(ta[i][t][ks], ub[ks], S[u][i][t]);
+      }
       load_d();
       load_t();
     }
     __syncthreads();
-    if (O::first(w)) store_state<KW>(S, a.state_out, kw, p, at);
+    if (O::first(w))
+#pragma unroll
+      for (int u = 0; u < NT; ++u) store_state<KW>(S[u], a.state_out, kw, at.col(u), p, at);
   } else if (wave < 6) {
     // row tiles j and 3 - j of O: one of them reaches over both k steps of P
     const int j = wave - 4;
@@ -460,29 +476,36 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
         dp += p.Hv;
       }
       __syncthreads();
-      v4f o[2] = {zero, zero};
+      v4f o[NT][2];
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        v8bf sb[3];
+      for (int u = 0; u < NT; ++u) {
+        o[u][0] = o[u][1] = zero;
 #pragma unroll
-        for (int q = 0; q < 3; ++q)
-          sb[q] = *reinterpret_cast<const v8bf*>(&st[q][lr][32 * ks + 8 * lg]);
-        o[0] = mfma_parts<3>(qa[0][ks], sb, o[0]);
-        o[1] = mfma_parts<3>(qa[1][ks], sb, o[1]);
+        for (int ks = 0; ks < KS; ++ks) {
+          v8bf sb[3];
+#pragma unroll
+          for (int q = 0; q < 3; ++q)
+            sb[q] = *reinterpret_cast<const v8bf*>(&st[q][16 * u + lr][32 * ks + 8 * lg]);
+          o[u][0] = mfma_parts<3>(qa[0][ks], sb, o[u][0]);
+          o[u][1] = mfma_parts<3>(qa[1][ks], sb, o[u][1]);
+        }
+        o[u][0] *= ev[0] * a.scale;
+        o[u][1] *= ev[1] * a.scale;
       }
-      o[0] *= ev[0] * a.scale;
-      o[1] *= ev[1] * a.scale;
       load_q();
       __syncthreads();
       __syncthreads();
-      v8bf ub[2][OUTS];
-      get8<OUTS>(ut, ub[0], lr, lg * 8);
-      get8<OUTS>(ut, ub[1], lr, 32 + lg * 8);
-      o[0] = mfma_parts<OUTS>(p0, ub[0], o[0]);
-      o[1] = mfma_parts<OUTS>(p1[0], ub[0], o[1]);
-      o[1] = mfma_parts<OUTS>(p1[1], ub[1], o[1]);
-      *reinterpret_cast<v4f*>(&os[lr][16 * j + 4 * lg]) = o[0];
-      *reinterpret_cast<v4f*>(&os[lr][16 * (3 - j) + 4 * lg]) = o[1];
+#pragma unroll
+      for (int u = 0; u < NT; ++u) {
+        v8bf ub[2][OUTS];
+        get8<OUTS>(ut, ub[0], 16 * u + lr, lg * 8);
+        get8<OUTS>(ut, ub[1], 16 * u + lr, 32 + lg * 8);
+        o[u][0] = mfma_parts<OUTS>(p0, ub[0], o[u][0]);
+        o[u][1] = mfma_parts<OUTS>(p1[0], ub[0], o[u][1]);
+        o[u][1] = mfma_parts<OUTS>(p1[1], ub[1], o[u][1]);
+        *reinterpret_cast<v4f*>(&os[16 * u + lr][16 * j + 4 * lg]) = o[u][0];
+        *reinterpret_cast<v4f*>(&os[16 * u + lr][16 * (3 - j) + 4 * lg]) = o[u][1];
+      }
       load_p();
     }
     __syncthreads();
@@ -511,27 +534,27 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       for (int u = 0; u < A::kSets; ++u) {
         const int c = c4 + u;
         if (c < nc) {
-        A::settle(held[(u + 3) % A::kSets]);
-        touch(c + 3, held[(u + 3) % A::kSets]);
-        __syncthreads();
-        if constexpr (SAVE) {
-          store_parts<DKP>(sp, st, p.dk, cols, j, lane);
-          sp += (size_t)p.Hv * p.dk * p.dv;
-        }
-        if (c > 0) {
-          store_rows<T>(op, ldo, os, cols, kChunk, j, lane);
-          op += (size_t)kChunk * ldo;
-        }
-        __syncthreads();
-        __syncthreads();
-        if constexpr (SAVE) {
-          store_columns<kLdF>(np, ns, kChunk, cols, j, lane);
-          np += (size_t)p.Hv * kChunk * p.dv;
-        }
+          A::settle(held[(u + 3) % A::kSets]);
+          touch(c + 3, held[(u + 3) % A::kSets]);
+          __syncthreads();
+          if constexpr (SAVE) {
+            store_parts<DKP>(sp, st, p.dk, cols, j, lane);
+            sp += (size_t)p.Hv * p.dk * p.dv;
+          }
+          if (c > 0) {
+            store_rows(op, ldo, os, cols, kChunk, j, lane);
+            op += (size_t)kChunk * ldo;
+          }
+          __syncthreads();
+          __syncthreads();
+          if constexpr (SAVE) {
+            store_columns(np, ns, kChunk, cols, j, lane);
+            np += (size_t)p.Hv * kChunk * p.dv;
+          }
         }
       }
     __syncthreads();
-    if (nc > 0) store_rows<T>(op, ldo, os, cols, (int)(at.r.len - (long)(nc - 1) * kChunk), j, lane);
+    if (nc > 0) store_rows(op, ldo, os, cols, (int)(at.r.len - (long)(nc - 1) * kChunk), j, lane);
   }
 }
 
@@ -542,11 +565,11 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
 // Waves 0 - 3 walk this chain, 4 and 5 prepare the products with dO a chunk ahead, 6
 // and 7 store dV (the gradient of v, and fp32 [dv][64] for stage 3) and Z before its
 // update ([dv][dk], for stage 3).
-template <typename T, int PARTS, int OUTS, int DKP>
+template <typename T, int PARTS, int OUTS, int DKP, int DS>
 __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_plan p,
                                                              const DeltaArgs a) {
   using O = Own<DKP>;
-  constexpr int KS = O::KS, KW = O::KW, RT = O::RT;
+  constexpr int KS = O::KS, KW = O::KW, RT = O::RT, NT = DS / 16;   // NT: column tiles
   __shared__ __attribute__((aligned(16))) float pk[O::WAVES][DS][kLdF];   // K Z, by owner
   __shared__ __attribute__((aligned(16))) float d1[2][DS][kLdF];          // (scale P)^T dO
   __shared__ __attribute__((aligned(16))) float vs[DS][kLdF];             // dV
@@ -558,7 +581,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
   __shared__ __attribute__((aligned(16))) __bf16 vt[3][DS][kLdT];         // -e . dV
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place at;
-  if (!place_of(p, a, lane, &at)) return;
+  if (!place_of<DS>(p, a, lane, &at)) return;
   const int lr = at.lr, lg = at.lg, nc = at.nc;
   constexpr size_t kbytes = (size_t)PARTS * 4 * KS * kFrag;
   const long slot1 = at.slot0 + nc - 1;   // the last chunk
@@ -575,8 +598,9 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
   if (wave < 4) {
     __builtin_amdgcn_s_setprio(1);
     const int w = wave, i0 = 16 * w + 4 * lg, kw = O::kw(w) * KW, rt0 = O::rt(w);
-    v4f Z[KW][2];
-    load_state<KW>(Z, a.dstate_out, kw, p, at);
+    v4f Z[NT][KW][2];
+#pragma unroll
+    for (int u = 0; u < NT; ++u) load_state<KW>(Z[u], a.dstate_out, kw, at.col(u), p, at);
     if (nc > 0) {
       v8bf ka[KW][RT][PARTS], xa[2][3], ta[KW][2][2][PARTS];
       v4f ev, dv, bv;
@@ -630,14 +654,15 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
           dp -= p.Hv;
         }
         const int b = c & 1;
-        {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
           v4f x[RT];
 #pragma unroll
           for (int t = 0; t < RT; ++t) x[t] = zero;
 #pragma unroll
           for (int i = 0; i < KW; ++i) {
             v8bf sb[3];
-            state_operand(Z[i], sb);
+            state_operand(Z[u][i], sb);
 #pragma unroll
             for (int t = 0; t < RT; ++t) x[t] = mfma_parts<3>(ka[i][t], sb, x[t]);
           }
@@ -646,87 +671,105 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
             for (int i = 0; i < KW; ++i)
 #pragma unroll
               for (int t = 0; t < 2; ++t)
-                *reinterpret_cast<v4f*>(&ss[lr][32 * (kw + i) + 8 * lg + 4 * t]) = Z[i][t];
+                *reinterpret_cast<v4f*>(&ss[16 * u + lr][32 * (kw + i) + 8 * lg + 4 * t]) = Z[u][i][t];
 #pragma unroll
           for (int t = 0; t < RT; ++t)
-            *reinterpret_cast<v4f*>(&pk[O::kw(w)][lr][16 * (rt0 + t) + 4 * lg]) = x[t];
+            *reinterpret_cast<v4f*>(&pk[O::kw(w)][16 * u + lr][16 * (rt0 + t) + 4 * lg]) = x[t];
         }
         load_k();
         __syncthreads();
-        {
-          v4f kz = *reinterpret_cast<const v4f*>(&pk[0][lr][i0]);
 #pragma unroll
-          for (int i = 1; i < O::WAVES; ++i) kz += *reinterpret_cast<const v4f*>(&pk[i][lr][i0]);
-          const v4f g = *reinterpret_cast<const v4f*>(&d1[b][lr][i0]);
-          put4<3>(ut, bv * (g + dv * kz), lr, i0);
+        for (int u = 0; u < NT; ++u) {
+          v4f kz = *reinterpret_cast<const v4f*>(&pk[0][16 * u + lr][i0]);
+#pragma unroll
+          for (int i = 1; i < O::WAVES; ++i)
+            kz += *reinterpret_cast<const v4f*>(&pk[i][16 * u + lr][i0]);
+          const v4f g = *reinterpret_cast<const v4f*>(&d1[b][16 * u + lr][i0]);
+          put4<3>(ut, bv * (g + dv * kz), 16 * u + lr, i0);
         }
 #pragma unroll
-        for (int i = 0; i < KW; ++i)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int t = 0; t < 2; ++t)
-            Z[i][t] = Z[i][t] * el +
-                      *reinterpret_cast<const v4f*>(&eq[b][lr][32 * (kw + i) + 8 * lg + 4 * t]);
+          for (int i = 0; i < KW; ++i)
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+              Z[u][i][t] = Z[u][i][t] * el +
+                           *reinterpret_cast<const v4f*>(
+                               &eq[b][16 * u + lr][32 * (kw + i) + 8 * lg + 4 * t]);
         __syncthreads();
-        v4f dV = zero, dV1 = zero;
-        {
+#pragma unroll
+        for (int u = 0; u < NT; ++u) {
+          v4f dV = zero, dV1 = zero;
           v8bf ub[3], uc[3];
-          get8<3>(ut, ub, lr, 32 + lg * 8);
+          get8<3>(ut, ub, 16 * u + lr, 32 + lg * 8);
           if (w < 2) {
-            get8<3>(ut, uc, lr, lg * 8);
+            get8<3>(ut, uc, 16 * u + lr, lg * 8);
             dV1 = mfma_parts<3>(xa[0], uc, dV1);
           }
           dV = mfma_parts<3>(xa[1], ub, dV);
           dV += dV1;
+          put4<3>(vt, -(ev * dV), 16 * u + lr, i0);
+          *reinterpret_cast<v4f*>(&vs[16 * u + lr][i0]) = dV;
         }
-        put4<3>(vt, -(ev * dV), lr, i0);
-        *reinterpret_cast<v4f*>(&vs[lr][i0]) = dV;
         load_x();
         load_d();
         __syncthreads();
 #pragma unroll
-        for (int ks = 0; ks < 2; ++ks) {
-          v8bf vb[3];
-          get8<3>(vt, vb, lr, ks * 32 + lg * 8);
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int i = 0; i < KW; ++i)
+          for (int ks = 0; ks < 2; ++ks) {
+            v8bf vb[3];
+            get8<3>(vt, vb, 16 * u + lr, ks * 32 + lg * 8);
 #pragma unroll
-            for (int t = 0; t < 2; ++t) Z[i][t] = mfma_parts<3>(ta[i][t][ks], vb, Z[i][t]);
-        }
+            for (int i = 0; i < KW; ++i)
+#pragma unroll
+              for (int t = 0; t < 2; ++t)
+                Z[u][i][t] = mfma_parts<3>(ta[i][t][ks], vb, Z[u][i][t]);
+          }
         load_t();
       }
     }
-    if (O::first(w)) store_state<KW>(Z, a.dstate, kw, p, at);
+    if (O::first(w))
+#pragma unroll
+      for (int u = 0; u < NT; ++u) store_state<KW>(Z[u], a.dstate, kw, at.col(u), p, at);
   } else if (nc > 0 && wave < 6) {
     // row tiles j and 3 - j: one of them reaches over both k steps of P^T
     const int j = wave - 4, ra = 16 * j + 4 * lg, rb = 16 * (3 - j) + 4 * lg;
     constexpr int QT = DKP / 32;   // tiles of Q^T a wave
     v8bf p0[2][OUTS], p1[OUTS], qa[QT][2][PARTS];
     v4f ev[2];
-    T go[2][4];
+    T go[NT][2][4];
     const unsigned char* qp = a.ws + p.off_qt + k0 + (size_t)j * QT * 2 * kFrag;
     const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag);
     const T* gp = (const T*)a.dout + row1 * ldo + (size_t)at.h * p.dv;
-    unsigned ooff[2][4];
+    unsigned ooff[2][4], ocol[NT];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      ooff[0][e] = (unsigned)(ra + e) * ldo + at.ccol;
-      ooff[1][e] = (unsigned)(rb + e) * ldo + at.ccol;
+      ooff[0][e] = (unsigned)(ra + e) * ldo;
+      ooff[1][e] = (unsigned)(rb + e) * ldo;
     }
+#pragma unroll
+    for (int u = 0; u < NT; ++u) ocol[u] = at.col(u) < p.dv ? at.col(u) : 0;
     auto load = [&](bool whole) {   // by the moving pointers
       ev[0] = *reinterpret_cast<const v4f*>(dp->e + ra);
       ev[1] = *reinterpret_cast<const v4f*>(dp->e + rb);
       if (whole) {
 #pragma unroll
-        for (int t = 0; t < 2; ++t)
+        for (int u = 0; u < NT; ++u)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) go[t][e] = ((const GLOBAL T*)gp)[ooff[t][e]];
+          for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              go[u][t][e] = ((const GLOBAL T*)gp)[ooff[t][e] + ocol[u]];
       } else {   // rows behind the end: Q and P are zero there
 #pragma unroll
         for (int t = 0; t < 2; ++t)
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const int i = (t ? rb : ra) + e;
-            go[t][e] = ((const GLOBAL T*)gp)[(unsigned)(i < last ? i : last - 1) * ldo + at.ccol];
+            const unsigned o = (unsigned)(i < last ? i : last - 1) * ldo;
+#pragma unroll
+            for (int u = 0; u < NT; ++u) go[u][t][e] = ((const GLOBAL T*)gp)[o + ocol[u]];
           }
       }
 #pragma unroll
@@ -745,38 +788,44 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
     };
     auto put = [&] {
 #pragma unroll
-      for (int t = 0; t < 2; ++t) {
-        v4f g;
+      for (int u = 0; u < NT; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) g[e] = to_f32(go[t][e]);
-        put4<PARTS>(ot, g, lr, t ? rb : ra);
-        put4<3>(et, g * (ev[t] * a.scale), lr, t ? rb : ra);
-      }
+        for (int t = 0; t < 2; ++t) {
+          v4f g;
+#pragma unroll
+          for (int e = 0; e < 4; ++e) g[e] = to_f32(go[u][t][e]);
+          put4<PARTS>(ot, g, 16 * u + lr, t ? rb : ra);
+          put4<3>(et, g * (ev[t] * a.scale), 16 * u + lr, t ? rb : ra);
+        }
     };
     auto product = [&](int b) {
-      v4f g0 = zero, g1 = zero;
-      v8bf oa[PARTS], ob[PARTS];
-      get8<PARTS>(ot, oa, lr, lg * 8);
-      get8<PARTS>(ot, ob, lr, 32 + lg * 8);
-      g0 = mfma_parts<3>(p0[0], oa, g0);
-      g1 = mfma_parts<3>(p1, ob, g1);
-      g0 = mfma_parts<3>(p0[1], ob, g0);
-      *reinterpret_cast<v4f*>(&d1[b][lr][ra]) = g0;
-      *reinterpret_cast<v4f*>(&d1[b][lr][rb]) = g1;
-      v4f x[QT];
 #pragma unroll
-      for (int t = 0; t < QT; ++t) x[t] = zero;
+      for (int u = 0; u < NT; ++u) {
+        const int col = 16 * u + lr;
+        v4f g0 = zero, g1 = zero;
+        v8bf oa[PARTS], ob[PARTS];
+        get8<PARTS>(ot, oa, col, lg * 8);
+        get8<PARTS>(ot, ob, col, 32 + lg * 8);
+        g0 = mfma_parts<3>(p0[0], oa, g0);
+        g1 = mfma_parts<3>(p1, ob, g1);
+        g0 = mfma_parts<3>(p0[1], ob, g0);
+        *reinterpret_cast<v4f*>(&d1[b][col][ra]) = g0;
+        *reinterpret_cast<v4f*>(&d1[b][col][rb]) = g1;
+        v4f x[QT];
 #pragma unroll
-      for (int ks = 0; ks < 2; ++ks) {
-        v8bf eb[3];
-        get8<3>(et, eb, lr, ks * 32 + lg * 8);
+        for (int t = 0; t < QT; ++t) x[t] = zero;
 #pragma unroll
-        for (int t = 0; t < QT; ++t) x[t] = mfma_parts<3>(qa[t][ks], eb, x[t]);
-      }
+        for (int ks = 0; ks < 2; ++ks) {
+          v8bf eb[3];
+          get8<3>(et, eb, col, ks * 32 + lg * 8);
 #pragma unroll
-      for (int t = 0; t < QT; ++t) {
-        const int rt = j * QT + t;
-        *reinterpret_cast<v4f*>(&eq[b][lr][32 * (rt >> 1) + 8 * lg + 4 * (rt & 1)]) = x[t];
+          for (int t = 0; t < QT; ++t) x[t] = mfma_parts<3>(qa[t][ks], eb, x[t]);
+        }
+#pragma unroll
+        for (int t = 0; t < QT; ++t) {
+          const int rt = j * QT + t;
+          *reinterpret_cast<v4f*>(&eq[b][col][32 * (rt >> 1) + 8 * lg + 4 * (rt & 1)]) = x[t];
+        }
       }
     };
     auto back = [&](int c) {   // chunk c's operands are used up: the next
@@ -824,19 +873,19 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
       for (int u = 0; u < A::kSets; ++u) {
         const int c = c4 - u;
         if (c >= 0) {
-        A::settle(held[(u + 3) % A::kSets]);
-        touch(c - 3, held[(u + 3) % A::kSets]);
-        __syncthreads();
-        store_columns<DKP + 4>(zp, ss, p.dk, cols, j, lane);
-        zp -= (size_t)p.Hv * p.dk * p.dv;
-        __syncthreads();
-        __syncthreads();
-        store_columns<kLdF>(fp, vs, kChunk, cols, j, lane);
-        fp -= (size_t)p.Hv * kChunk * p.dv;
-        if (op) {
-          store_rows<T>(op, ldo, vs, cols, c == nc - 1 ? last : kChunk, j, lane);
-          op -= (size_t)kChunk * ldo;
-        }
+          A::settle(held[(u + 3) % A::kSets]);
+          touch(c - 3, held[(u + 3) % A::kSets]);
+          __syncthreads();
+          store_columns(zp, ss, p.dk, cols, j, lane);
+          zp -= (size_t)p.Hv * p.dk * p.dv;
+          __syncthreads();
+          __syncthreads();
+          store_columns(fp, vs, kChunk, cols, j, lane);
+          fp -= (size_t)p.Hv * kChunk * p.dv;
+          if (op) {
+            store_rows(op, ldo, vs, cols, c == nc - 1 ? last : kChunk, j, lane);
+            op -= (size_t)kChunk * ldo;
+          }
         }
       }
   }
@@ -844,25 +893,34 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
 
 namespace {
 
-unsigned slice_blocks(const s4dplr_delta_plan* p) {
+template <typename T, int PARTS, int OUTS, int DKP, int DS>
+void go(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
   const unsigned heads = (unsigned)(p->sequences * p->Hv);
-  return (heads + 7) / 8 * 8 * ((p->dv + DS - 1) / DS);
+  const unsigned grid = (heads + 7) / 8 * 8 * ((p->dv + DS - 1) / DS);
+  if (bwd) delta_scan_bwd_kernel<T, PARTS, OUTS, DKP, DS><<<grid, 512, 0, s>>>(*p, a);
+  else if (a.saved) delta_scan_kernel<T, PARTS, OUTS, DKP, true, DS><<<grid, 512, 0, s>>>(*p, a);
+  else delta_scan_kernel<T, PARTS, OUTS, DKP, false, DS><<<grid, 512, 0, s>>>(*p, a);
 }
 
+// bf16 at 64 < dk <= 128: while blocks of 16 columns are no more than the 256 CUs, more
+// of them at once is what counts; beyond, blocks of 32 columns share the loads of a
+// chunk's operands, which bound the step (4 sequences of 4096 tokens, 16 heads of 128
+// x 128, 512 blocks of 16: forward with saving 340 -> 300 us, backward 318 -> 286 us).  At
+// dk <= 64 two blocks of 16 columns share a CU and are the faster ones (5003 tokens in
+// 13 sequences, 8 heads of 64 x 128: 42 us, 48 with 32).  Operands of two and three
+// parts, and dk > 128, leave no room for 32 columns.
 template <typename T, int PARTS, int OUTS>
 hipError_t scan(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
-  const unsigned grid = slice_blocks(p);
-#define S4_GO(dkp)                                                                     \
-  if (bwd)                                                                             \
-    delta_scan_bwd_kernel<T, PARTS, OUTS, dkp><<<grid, 512, 0, s>>>(*p, a);            \
-  else if (a.saved)                                                                    \
-    delta_scan_kernel<T, PARTS, OUTS, dkp, true><<<grid, 512, 0, s>>>(*p, a);          \
-  else                                                                                 \
-    delta_scan_kernel<T, PARTS, OUTS, dkp, false><<<grid, 512, 0, s>>>(*p, a)
-  if (p->dkp == 64) { S4_GO(64); }
-  else if (p->dkp == 128) { S4_GO(128); }
-  else { S4_GO(256); }
-#undef S4_GO
+  const long blocks = (long)p->sequences * p->Hv * ((p->dv + 15) / 16);
+  if constexpr (PARTS == 1) {
+    if (p->dkp == 128 && p->dv > 16 && blocks > 256) {
+      go<T, PARTS, OUTS, 128, 32>(p, a, bwd, s);
+      return hipGetLastError();
+    }
+  }
+  if (p->dkp == 64) go<T, PARTS, OUTS, 64, 16>(p, a, bwd, s);
+  else if (p->dkp == 128) go<T, PARTS, OUTS, 128, 16>(p, a, bwd, s);
+  else go<T, PARTS, OUTS, 256, 16>(p, a, bwd, s);
   return hipGetLastError();
 }
 

@@ -145,6 +145,21 @@ def test_packed_sequences(s4, offsets, dtype, state):
     check_forward(s4, inputs(9, 200, 5, 1, 2, 32, 24, dtype, state=state), 5, offsets)
 
 
+@pytest.mark.parametrize("dk,dv", [(128, 128), (100, 120), (65, 33), (128, 17)])
+def test_many_heads(s4, dk, dv):
+    # more slices of 16 columns than the GPU has CUs: the blocks take 32
+    x = inputs(dk + dv, 5 * 130, 5, 6, 18, dk, dv, BF)
+    check_forward(s4, x, 5)
+    check_backward(s4, x, 5)
+
+
+def test_many_heads_packed(s4):
+    x = inputs(77, 300, 6, 16, 16, 128, 48, BF)
+    offsets = [2, 2, 3, 131, 200, 264, 290]
+    check_forward(s4, x, 6, offsets)
+    check_backward(s4, x, 6, offsets)
+
+
 def test_many_sequences(s4):
     # more sequences than a wave has lanes
     gen = torch.Generator().manual_seed(0)
