@@ -368,7 +368,7 @@ typedef enum s4dplr_dtype { S4DPLR_F32 = 0, S4DPLR_BF16 = 1, S4DPLR_F16 = 2 } s4
  *   mean, rstd : [outer][inner] float32, the m and r that s4dplr_layer_norm_bwd
  *                reads; each may be NULL (not written).
  * outer = 0 is a no-op.  Limits: outer >= 0, 1 <= D <= 32768, inner >= 1,
- * outer * inner < 2^31, eps >= 0 (ERR_SHAPE).
+ * outer * inner < 2^31 (inner > 1: 2^28), eps >= 0 and finite (ERR_SHAPE).
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS (an output overlaps an
  * input or another output), ERR_UNSUPPORTED (dtype), ERR_HIP.
  */
@@ -421,9 +421,9 @@ typedef struct s4dplr_delta_plan s4dplr_delta_plan;
 
 /*
  * Plan for `sequences` sequences of together `tokens` rows.  Host-only.
- * Limits: sequences >= 1, 0 <= tokens < 2^31, 1 <= dk, dv <= 256, Hk >= 1, Hv a
- * multiple of Hk up to 65535, sequences * Hv <= 2^24 (ERR_SHAPE).  Errors:
- * ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED (dtype, flags).  A plan is immutable
+ * Limits: sequences >= 1, tokens >= 0, 1 <= dk, dv <= 256, Hk >= 1, Hv a multiple of
+ * Hk up to 65535, sequences * Hv <= 2^18, tokens * Hv < 2^31, tokens / 64 + sequences
+ * < 2^22 - 8 (ERR_SHAPE).  Errors: ERR_NULL, ERR_SHAPE, ERR_UNSUPPORTED (dtype, flags).  A plan is immutable
  * and may be used from several threads and streams, each with its own workspace.
  */
 s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, long tokens,
@@ -442,8 +442,9 @@ s4dplr_status s4dplr_delta_plan_bytes(const s4dplr_delta_plan* plan, size_t* wor
  * first rows, NULL for zeros; state_out: the states after the last rows, may be
  * NULL (not written) or `state` itself.  saved: NULL, or (plans with
  * S4DPLR_DELTA_TRAINING) the buffer for s4dplr_delta_bwd, 256-byte aligned.
- * Short sequences are taken token by token in one launch, longer ones by chunks
- * of 64 tokens on the matrix cores; with `saved`, all of them by chunks.  Both
+ * Sequences of up to 8 or 16 tokens are taken token by token in one launch, longer
+ * ones by chunks of 64 tokens on the matrix cores (packed batches that are long in
+ * the mean, and all calls with `saved`: all of them by chunks).  Both
  * compute the same recurrence.  tokens = 0 passes the states on.
  * Errors: ERR_NULL, ERR_SHAPE (a row pitch; without offsets, tokens not a
  * multiple of sequences), ERR_ALIGN, ERR_ALIAS (an output overlaps an input,

@@ -67,8 +67,15 @@ struct DeltaArgs {
   int step_tokens;            // sequences of at most so many tokens go token by token
 };
 
-// Longest sequence that is taken token by token.
-constexpr int kStepTokens = 16;
+// Longest sequence that is taken token by token.  A token costs 1.4 us (128 sequences,
+// 16 heads of 128 x 128: 14 us), a chunk with its preparation what 9 to 16 tokens do:
+// one sequence, 16 heads of 128 x 128: 8 tokens 15.5 us against 18.7, 16 tokens 27.3
+// against 17.4; 16 sequences: 16 tokens 43.1 against 44.3, 24 tokens 59.8 against 44.9;
+// 128 sequences: 249 against 259, 357 against 264.  The line is drawn where the chunked
+// form's blocks (16 columns each) fill the 256 CUs.
+inline int step_limit(const s4dplr_delta_plan* p) {
+  return (long)p->sequences * p->Hv * ((p->dv + 15) / 16) > 256 ? 16 : 8;
+}
 
 hipError_t launch_delta_steps(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd,

@@ -54,8 +54,8 @@ s4dplr_status done(hipError_t e) { return e == hipSuccess ? S4DPLR_OK : s4::hip_
 
 s4dplr_status norm_shape(long outer, long D, long inner) {
   if (outer < 0 || D < 1 || D > s4::kNormMaxD || inner < 1) return S4DPLR_ERR_SHAPE;
-  if (inner >= (1L << 31) || outer >= (1L << 31) || outer * inner >= (1L << 31))
-    return S4DPLR_ERR_SHAPE;
+  const long most = inner == 1 ? 1L << 31 : 1L << 28;   // 512 threads per 64 vectors
+  if (inner >= most || outer >= most || outer * inner >= most) return S4DPLR_ERR_SHAPE;
   return S4DPLR_OK;
 }
 
@@ -142,7 +142,10 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
   if (sequences < 1 || tokens < 0 || tokens >= (1L << 31)) return S4DPLR_ERR_SHAPE;
   if (dk < 1 || dk > 256 || dv < 1 || dv > 256) return S4DPLR_ERR_SHAPE;
   if (Hk < 1 || Hv < 1 || Hv > 65535 || Hv % Hk) return S4DPLR_ERR_SHAPE;
-  if ((long)sequences * Hv > (1L << 24)) return S4DPLR_ERR_SHAPE;
+  // a launch counts its threads in 32 bits: slices of a head x 512, chunks x 4 x 256
+  if ((long)sequences * Hv > (1L << 18) || tokens * Hv >= (1L << 31) ||
+      tokens / s4::kChunk + sequences >= (1L << 22) - 8)
+    return S4DPLR_ERR_SHAPE;
   s4dplr_delta_plan* p = new (std::nothrow) s4dplr_delta_plan();
   if (!p) return S4DPLR_ERR_SHAPE;
   p->sequences = sequences;
@@ -263,14 +266,15 @@ s4dplr_status s4dplr_delta_fwd(const s4dplr_delta_plan* p, const void* q, long l
   a.o = o;
   a.state_out = state_out;
   a.saved = static_cast<unsigned char*>(saved);
-  // The step form carries any length; the chunked one pays from kStepTokens on.
-  // A packed batch may hold both kinds: then both forms run, each on its own.
+  // The lengths of a packed batch are known to the device only.  Where its sequences
+  // are short in the mean, both forms run, each on its own sequences; else all go by
+  // chunks, which one more launch for the few short ones would not make faster.
   bool steps = false, chunks = true;
   if (!saved) {
-    const long longest = offsets ? p->tokens : p->tokens / p->sequences;
-    chunks = longest > s4::kStepTokens;
-    steps = !chunks || offsets;
-    if (steps) a.step_tokens = s4::kStepTokens;
+    const long limit = s4::step_limit(p);
+    chunks = (offsets ? p->tokens : p->each) > limit;
+    steps = !chunks || (offsets && p->tokens <= limit * p->sequences);
+    if (steps) a.step_tokens = (int)limit;
   }
   hipError_t e = hipSuccess;
   if (chunks) {

@@ -160,6 +160,14 @@ def test_many_heads_packed(s4):
     check_backward(s4, x, 6, offsets)
 
 
+@pytest.mark.parametrize("offsets", [[0, 1, 2, 2, 5, 12], [0, 1, 41, 41, 42, 45], [0, 3, 6, 8, 9, 9]])
+def test_packed_short_sequences(s4, offsets):
+    # token by token, token by token beside chunks, token by token with an empty one
+    check_forward(s4, inputs(19, offsets[-1], 5, 1, 2, 32, 24, BF), 5, offsets)
+    x = inputs(20, offsets[-1], 5, 8, 8, 32, 112, F32)
+    check_forward(s4, x, 5, offsets)
+
+
 def test_many_sequences(s4):
     # more sequences than a wave has lanes
     gen = torch.Generator().manual_seed(0)

@@ -38,7 +38,8 @@ def norm_bwd(lib, **kw):
 
 def test_norm_sizes(lib):
     for bad in (dict(outer=-1), dict(D=0), dict(D=32769), dict(inner=0), dict(inner=1 << 31),
-                dict(outer=1 << 31), dict(outer=1 << 20, inner=1 << 11)):
+                dict(outer=1 << 31), dict(outer=1 << 20, inner=1 << 11),
+                dict(outer=1 << 18, inner=1 << 10)):
         assert norm_fwd(lib, **bad) == SHAPE, bad
         assert norm_bwd(lib, **bad) == SHAPE, bad
     for eps in (-1e-9, float("nan"), float("inf")):
@@ -92,7 +93,8 @@ def plan(lib, S=3, tokens=30, Hk=2, Hv=4, dk=16, dv=8, dtype=1, flags=0):
     (dict(S=0), SHAPE), (dict(tokens=-1), SHAPE), (dict(tokens=1 << 31), SHAPE),
     (dict(dk=0), SHAPE), (dict(dk=257), SHAPE), (dict(dv=0), SHAPE), (dict(dv=257), SHAPE),
     (dict(Hk=0), SHAPE), (dict(Hv=0), SHAPE), (dict(Hk=3), SHAPE), (dict(Hv=65536), SHAPE),
-    (dict(S=1 << 23), SHAPE), (dict(dtype=3), UNSUPPORTED), (dict(flags=2), UNSUPPORTED)])
+    (dict(S=1 << 23), SHAPE), (dict(S=(1 << 16) + 1), SHAPE), (dict(tokens=1 << 29), SHAPE),
+    (dict(tokens=1 << 28, Hk=1, Hv=1), SHAPE), (dict(dtype=3), UNSUPPORTED), (dict(flags=2), UNSUPPORTED)])
 def test_delta_plan(lib, kw, expect):
     st, h = plan(lib, **kw)
     assert st == expect
