@@ -123,7 +123,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
     __bf16 v[3][32][kLdS], n[3][32][kLdS], s[3][32][kLdS];
   };
   struct Pairs {
-    float ym[64][kLd], bm[64][kLd], xm[64][kLd];
+    float ym[64][kLd], bm[64][kLd];
   };
   union Mem {
     Stage st;
@@ -131,6 +131,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
   };
   __shared__ __attribute__((aligned(16))) Mem mem;
   __shared__ float colsum[4][64];                    // dbeta's pair sums by row tile
+  __shared__ float cross[4][64];                     // dg's, of the pairs i >= t > j
   __shared__ float qg[64], kfv[64], sz[4], xs[64];
   const int nb = (p.dk + kCols - 1) / kCols;
   // the column blocks of a chunk, which share N and dV, on one XCD
@@ -314,10 +315,12 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
     double Gi[4];
 #pragma unroll
     for (int e = 0; e < 4; ++e) Gi[e] = vec->G[i0 + e];
+    // sum_{j < t} x_ij of the lane's rows up to the tile at hand
+    float run[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const int j = 16 * i + lr;
-      float cs = 0.f;
+      float cs = 0.f, cr = 0.f;
       if (i <= w) {
         const float bj = vec->beta[j];
         const double Gj = vec->G[j];
@@ -332,16 +335,28 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
           cs += t;
           mem.pr.ym[q][j] = bj * gy;
           mem.pr.bm[q][j] = bj * gw;
-          mem.pr.xm[q][j] = low ? bj * t : 0.f;
+          // sums over the columns up to each, by the 16 lanes of a row of the tile
+          float x = low ? bj * t : 0.f;
+          x += dpp<0x111>(x);   // row_shr 1, 2, 4, 8
+          x += dpp<0x112>(x);
+          x += dpp<0x114>(x);
+          x += dpp<0x118>(x);
+          const float before = run[e] + dpp<0x111>(x);   // columns below j = t
+          cr += diag ? before : 0.f;
+          run[e] += dpp<0x15F>(x);                       // row_newbcast 15: the tile's sum
         }
         cs += __shfl_xor(cs, 16);
+        cr += __shfl_xor(cr, 16);
         cs += __shfl_xor(cs, 32);
+        cr += __shfl_xor(cr, 32);
       } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          mem.pr.ym[i0 + e][j] = mem.pr.bm[i0 + e][j] = mem.pr.xm[i0 + e][j] = 0.f;
+        for (int e = 0; e < 4; ++e) mem.pr.ym[i0 + e][j] = mem.pr.bm[i0 + e][j] = 0.f;
       }
-      if (lg == 0) colsum[w][j] = cs;
+      if (lg == 0) {
+        colsum[w][j] = cs;
+        cross[w][j] = cr;
+      }
     }
     __syncthreads();
     // dQ += A K, dK += A^T Q - (B + B^T) K
@@ -367,46 +382,30 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
         dk[i] = mfma_parts<3>(kc[ks][i], ba, dk[i]);
       }
     }
-    // dbeta, dg
-    if (tid < 64 && cb == 0) {
-      // xm[i][t] becomes sum_{j < t} x_ij
-      float run = 0.f;
-#pragma unroll
-      for (int j = 0; j < 64; j += 16) {
-        float t[16];
-#pragma unroll
-        for (int q = 0; q < 16; q += 4)
-          *reinterpret_cast<v4f*>(t + q) = *reinterpret_cast<const v4f*>(&mem.pr.xm[tid][j + q]);
-#pragma unroll
-        for (int q = 0; q < 16; ++q) {
-          const float x = t[q];
-          t[q] = run;
-          run += x;
-        }
-#pragma unroll
-        for (int q = 0; q < 16; q += 4)
-          *reinterpret_cast<v4f*>(&mem.pr.xm[tid][j + q]) = *reinterpret_cast<const v4f*>(t + q);
-      }
-    }
-    __syncthreads();
-    if (tid < n) {
+    // dbeta, dg: token t = lane
+    if (w == 0) {
       const int t = tid;
-      float u = 0.f, cs = 0.f;
+      float after = qg[t], before = xs[t];   // sums over i >= t and, then, j < t
+#pragma unroll
+      for (int off = 1; off < 64; off <<= 1) {
+        const float x = __shfl_down(after, off), z = __shfl_up(before, off);
+        if (t + off < 64) after += x;
+        if (t >= off) before += z;
+      }
+      before = __shfl_up(before, 1);
+      float u = after + (t > 0 ? before : 0.f);
+      float cs = 0.f;
       if (cb == 0) {
-#pragma unroll 16
-        for (int i = 63; i >= 0; --i) u += i >= t ? mem.pr.xm[i][t] + qg[i] : xs[i];
+        u += (cross[0][t] + cross[1][t]) + (cross[2][t] + cross[3][t]);
         cs = (colsum[0][t] + colsum[1][t]) + (colsum[2][t] + colsum[3][t]);
-      } else {
-#pragma unroll 16
-        for (int i = 63; i >= 0; --i) u += i >= t ? qg[i] : xs[i];
       }
       const float ss = (sz[0] + sz[1]) + (sz[2] + sz[3]);
       const size_t at = (size_t)(t0 + t) * p.Hv + h;
       const size_t all = (size_t)p.tokens * p.Hv;
       float* dg = nb == 1 ? a.dg : reinterpret_cast<float*>(a.ws + p.off_gates) + 2 * cb * all;
       float* db = nb == 1 ? a.dbeta : dg + all;
-      if (dg) dg[at] = u + vec->e[kChunk - 1] * ss;
-      if (db) db[at] = cs + kfv[t];
+      if (dg && t < n) dg[at] = u + vec->e[kChunk - 1] * ss;
+      if (db && t < n) db[at] = cs + kfv[t];
     }
     __syncthreads();
   }
