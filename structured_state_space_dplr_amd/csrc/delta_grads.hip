@@ -15,9 +15,9 @@
 // heads of the group, so shared heads are summed in a fixed order.  dg and dbeta are
 // linear in the columns: each block writes its part, and delta_gates_kernel adds the
 // parts (dk <= 64: there is one, and it is the result).  Blocks of 64 columns keep a
-// wave under 256 registers and a block under 64 KB of LDS: two or three share a CU
-// and one computes while another loads (one block for all 128 columns took 790 us
-// where this takes 330, at 4096 chunks and heads of 128 x 128).
+// wave under 256 registers and a block under 50 KB of LDS: two or three share a CU
+// and one computes while another loads.  (At 4096 chunks and heads of 128 x 128: 428 us,
+// 1.1 GB read; a block for all 128 columns, one to a CU, took 790.)
 //
 // N, S, dV and Z are [dv][..] in memory, 32 of dv a step, and go through LDS as bf16
 // parts; the products' k index is dv, so operands come out of LDS with the
@@ -115,10 +115,19 @@ __device__ __forceinline__ void store4(T* p, int n, v4f x) {
 
 }  // namespace
 
-template <typename T, int PARTS, int OUTS, int DKP>
-__global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_plan p,
+// Three blocks a CU where 168 registers a lane do: bf16, one value head a key head (no
+// sums over heads are held), and each step's tiles loaded when it begins, since the
+// other blocks compute meanwhile (485 -> 428 us at 4096 chunks and heads of 128 x
+// 128).  Elsewhere two blocks, with the next step's tiles on their way.
+constexpr bool three_blocks(int parts, int dkp, bool grouped) {
+  return parts == 1 && dkp <= 128 && !grouped;
+}
+
+template <typename T, int PARTS, int OUTS, int DKP, bool GROUPED>
+__global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) void delta_grads_kernel(const s4dplr_delta_plan p,
                                                              const DeltaArgs a) {
   constexpr int CT = kCols / 16, KS = DKP / 32;
+  constexpr bool kThree = three_blocks(PARTS, DKP, GROUPED);
   struct Stage {
     __bf16 v[3][32][kLdS], n[3][32][kLdS], s[3][32][kLdS];
   };
@@ -137,7 +146,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
   // the column blocks of a chunk, which share N and dV, on one XCD
   const int slot = (int)(blockIdx.x / (8 * nb)) * 8 + (blockIdx.x & 7), cb = blockIdx.x / 8 % nb;
   if (slot >= p.slots) return;
-  const int hk = blockIdx.y, group = p.Hv / p.Hk;
+  const int hk = blockIdx.y, group = GROUPED ? p.Hv / p.Hk : 1;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int s = sequence_of(p, a.offsets, slot);
   const Rows r = rows_of(p, a.offsets, s);
@@ -193,8 +202,9 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
       tz.load(Z + (size_t)k0 * p.dk, p.dk, p.dv - k0, dcols, tid);
       load8(go + k0 + 8 * lg, row < n ? p.dv - k0 - 8 * lg : 0, ox);
     };
-    load(0);
+    if constexpr (!kThree) load(0);
     for (int k0 = 0; k0 < p.dv; k0 += 32) {
+      if constexpr (kThree) load(k0);
       __syncthreads();
       tv.put(mem.st.v, tid);
       tn.put(mem.st.n, tid);
@@ -207,7 +217,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
         for (int e = 0; e < 4; ++e) dot = fmaf(ts.x[i][e], tz.x[i][e], dot);
       const Tile zn = tz;
       __syncthreads();
-      if (k0 + 32 < p.dv) load(k0 + 32);
+      if (!kThree && k0 + 32 < p.dv) load(k0 + 32);
       get_tr<3>(mem.st.v, 16 * w, lr, lg, va);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
@@ -266,8 +276,9 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
             }
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        dq[i] += g1[i] * (er * a.scale);
-        dk[i] += f[i] * dbr - g2[i] * er;
+        const v4f x = g1[i] * (er * a.scale), z = f[i] * dbr - g2[i] * er;
+        dq[i] = GROUPED ? dq[i] + x : x;
+        dk[i] = GROUPED ? dk[i] + z : z;
       }
       a1 = er * (a.scale * a1 - a2);
       a1 += __shfl_xor(a1, 16);
@@ -296,7 +307,7 @@ __global__ __launch_bounds__(256, 2) void delta_grads_kernel(const s4dplr_delta_
           hh[i] = mfma_parts<3>(ka[ks], kb, hh[i]);
         }
     // the last products' operands, ahead of what they wait for
-    constexpr bool kAhead = PARTS == 1;
+    constexpr bool kAhead = PARTS == 1 && !kThree;
     v8bf kc[2][CT][PARTS], qc[2][CT][PARTS];
     auto load_kq = [&](int ks) {
 #pragma unroll
@@ -445,9 +456,13 @@ template <typename T, int PARTS, int OUTS>
 hipError_t grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) {
   const int nb = (p->dk + kCols - 1) / kCols;
   const dim3 grid((unsigned)((p->slots + 7) / 8 * 8 * nb), (unsigned)p->Hk);
-  if (p->dkp == 64) delta_grads_kernel<T, PARTS, OUTS, 64><<<grid, 256, 0, s>>>(*p, a);
-  else if (p->dkp == 128) delta_grads_kernel<T, PARTS, OUTS, 128><<<grid, 256, 0, s>>>(*p, a);
-  else delta_grads_kernel<T, PARTS, OUTS, 256><<<grid, 256, 0, s>>>(*p, a);
+#define S4_GO(dkp)                                                                           \
+  (p->Hv > p->Hk ? delta_grads_kernel<T, PARTS, OUTS, dkp, true><<<grid, 256, 0, s>>>(*p, a) \
+                 : delta_grads_kernel<T, PARTS, OUTS, dkp, false><<<grid, 256, 0, s>>>(*p, a))
+  if (p->dkp == 64) S4_GO(64);
+  else if (p->dkp == 128) S4_GO(128);
+  else S4_GO(256);
+#undef S4_GO
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || nb == 1 || p->tokens == 0 || (!a.dg && !a.dbeta)) return e;
   const size_t n = (size_t)p->tokens * p->Hv;
