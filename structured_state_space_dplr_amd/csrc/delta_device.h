@@ -129,6 +129,29 @@ __device__ __forceinline__ v8bf load_frag(const unsigned char* base, int frag, u
   return *reinterpret_cast<const v8bf*>(base + (size_t)(frag & ~3) * kFrag + (off + (frag & 3) * kFrag));
 }
 
+// Operand of 16 columns (the fast index of m [part][ROWS][LD] in LDS) by 32 k (its rows r0
+// ..): lane (lr, lg) gets its column, rows r0 + 8 lg .. + 8.  In the transposing read 16
+// lanes fetch 4 rows of 4 groups of 4 columns, and lane i receives column i of the
+// 16.  The groups are STEP columns apart: 4, or 8 for tiles of dk in the order of K^T's
+// rows.
+template <int P, int STEP, int ROWS, int LD>
+__device__ __forceinline__ void get_tr(const __bf16 (*m)[ROWS][LD], int r0, int c0, int lr, int lg,
+                                       v8bf (&out)[P]) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds4;
+#pragma unroll
+  for (int q = 0; q < P; ++q) {
+    const __bf16* a = &m[q][r0 + 8 * lg + (lr >> 2)][c0 + STEP * (lr & 3)];
+    union {
+      v4s h[2];
+      v8bf v;
+    } u;
+    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)a);
+    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(a + 4 * LD));
+    out[q] = u.v;
+  }
+}
+
 // 2^x for a difference x held in 64 bits, at fp32 accuracy for any size of it: the
 // hardware's 2^f for |f| <= 1 / 2, scaled by the whole part.
 __device__ __forceinline__ float exp_diff(double x) {

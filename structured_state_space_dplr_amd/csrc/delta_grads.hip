@@ -32,29 +32,6 @@ constexpr int kLd = 68;
 constexpr int kLdS = 64 + 16;   // bf16 from row to row of a staged tile: 8 banks
 constexpr int kCols = 64;       // columns of dk of a block
 
-// Operand of 16 columns (the fast index of m [32][LD]) by 32 k (its rows): lane
-// (lr, lg) gets its column, rows 8 lg .. + 8.  In the transposing read 16 lanes
-// fetch 4 rows of 4 groups of 4 columns, and lane i receives column i of the 16.  The
-// groups are STEP columns apart: 4, or 8 for the tiles of dk, which come in the order of
-// K^T's rows.
-template <int P, int STEP = 4>
-__device__ __forceinline__ void get_tr(const __bf16 (*m)[32][kLdS], int c0, int lr, int lg,
-                                       v8bf (&out)[P]) {
-  typedef short v4s __attribute__((ext_vector_type(4)));
-  typedef __attribute__((address_space(3))) v4s lds4;
-#pragma unroll
-  for (int q = 0; q < P; ++q) {
-    const __bf16* a = &m[q][8 * lg + (lr >> 2)][c0 + STEP * (lr & 3)];
-    union {
-      v4s h[2];
-      v8bf v;
-    } u;
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)a);
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)(a + 4 * kLdS));
-    out[q] = u.v;
-  }
-}
-
 // A tile of 32 rows (of dv) by 64 columns of an fp32 matrix, by 256 threads: 4 columns
 // at a time, rows thread / 16 and + 16.
 struct Tile {
@@ -218,18 +195,18 @@ __global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) voi
       const Tile zn = tz;
       __syncthreads();
       if (!kThree && k0 + 32 < p.dv) load(k0 + 32);
-      get_tr<3>(mem.st.v, 16 * w, lr, lg, va);
+      get_tr<3, 4>(mem.st.v, 0, 16 * w, lr, lg, va);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        get_tr<3, 8>(mem.st.s, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
+        get_tr<3, 8>(mem.st.s, 0, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
         g1[i] = mfma_parts<3>(b, oa, g1[i]);
         g2[i] = mfma_parts<3>(b, va, g2[i]);
       }
-      get_tr<3>(mem.st.n, 16 * w, lr, lg, na);
+      get_tr<3, 4>(mem.st.n, 0, 16 * w, lr, lg, na);
 #pragma unroll
       for (int i = 0; i < 4; ++i)
         if (i <= w) {
-          get_tr<3>(mem.st.n, 16 * i, lr, lg, b);
+          get_tr<3, 4>(mem.st.n, 0, 16 * i, lr, lg, b);
           y[i] = mfma_parts<3>(oa, b, y[i]);
           wv[i] = mfma_parts<3>(va, b, wv[i]);
         }
@@ -238,7 +215,7 @@ __global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) voi
       __syncthreads();
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
-        get_tr<3, 8>(mem.st.s, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
+        get_tr<3, 8>(mem.st.s, 0, 32 * (i >> 1) + 4 * (i & 1), lr, lg, b);
         f[i] = mfma_parts<3>(b, na, f[i]);
       }
     }

@@ -24,7 +24,7 @@ template <typename T, int PARTS, int OUTS, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan p,
                                                          const DeltaArgs a) {
   constexpr int KS = DKP / 32;
-  __shared__ v8bf kf[PARTS][4][KS][64];
+  __shared__ __attribute__((aligned(16))) __bf16 km[PARTS][64][DKP + 8];   // K, then Q, by rows
   __shared__ float am[64][kLd], pm[64][kLd];
   __shared__ double G[64];
   __shared__ float bt[64];
@@ -41,6 +41,11 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   const size_t kslot = (size_t)slot * p.Hk + hk, vslot = (size_t)slot * p.Hv + h;
   constexpr size_t kbytes = (size_t)PARTS * 4 * KS * kFrag;
 
+  float g0 = 0.f, b0 = 0.f;   // on their way while K and Q are split
+  if (w == 0 && lane < n) {
+    g0 = a.g[(size_t)(t0 + lane) * p.Hv + h];
+    b0 = a.beta[(size_t)(t0 + lane) * p.Hv + h];
+  }
   // K and Q of the wave's 16 rows
   const int row = 16 * w + (lane & 15);
   v8bf qr[KS][PARTS];
@@ -61,7 +66,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
       split8<PARTS>(x, qr[ks]);
 #pragma unroll
       for (int i = 0; i < PARTS; ++i) {
-        kf[i][w][ks][lane] = kk[i];
+        *reinterpret_cast<v8bf*>(&km[i][row][col]) = kk[i];
         if (own_k) {
           const size_t f = ((size_t)(i * 4 + w) * KS + ks) * kFrag + lane * 16;
           *reinterpret_cast<v8bf*>(ko + f) = kk[i];
@@ -74,10 +79,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   // large negative g (a reset); below -200 the decay is 0 in fp32 either way
   if (w == 0) {
     DeltaVec* vec = reinterpret_cast<DeltaVec*>(a.ws + p.off_vec) + vslot;
-    const bool on = lane < n;
-    const float g = on ? a.g[(size_t)(t0 + lane) * p.Hv + h] : 0.f;
-    const float b = on ? a.beta[(size_t)(t0 + lane) * p.Hv + h] : 0.f;
-    double x = (g < -200.f ? -200.0 : (double)g) * 1.4426950408889634;   // powers of 2
+    double x = (g0 < -200.f ? -200.0 : (double)g0) * 1.4426950408889634;   // powers of 2
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double y = __shfl_up(x, off);
@@ -85,10 +87,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
     }
     const double last = __shfl(x, 63);
     G[lane] = x;
-    bt[lane] = b;
+    bt[lane] = b0;
     vec->e[lane] = exp_diff(x);
     vec->d[lane] = exp_diff(last - x);
-    vec->beta[lane] = b;
+    vec->beta[lane] = b0;
     vec->G[lane] = x;
   }
   __syncthreads();
@@ -103,8 +105,8 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
         v8bf ka[PARTS], kb[PARTS];
 #pragma unroll
         for (int i = 0; i < PARTS; ++i) {
-          ka[i] = kf[i][w][ks][lane];
-          kb[i] = kf[i][ct][ks][lane];
+          ka[i] = *reinterpret_cast<const v8bf*>(&km[i][row][ks * 32 + (lane >> 4) * 8]);
+          kb[i] = *reinterpret_cast<const v8bf*>(&km[i][16 * ct + (lane & 15)][ks * 32 + (lane >> 4) * 8]);
         }
         hh = mfma_parts<3>(ka, kb, hh);
         pp = mfma_parts<3>(qr[ks], kb, pp);
@@ -204,8 +206,7 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   }
   // K^T (then, through the same memory, Q^T).  Row 4 g + e of tile t of a k step of dk is
   // column 8 g + 4 t + e of the step, so that the two tiles' accumulators hold 8
-  // neighbouring rows of the state a lane.  Element (column d, k = i) is lane
-  // (i % 16) + 16 ((d % 32) / 8), entry d % 8 of K's operand [i / 16][d / 32].
+  // neighbouring rows of the state a lane.
   if (!own_k) return;
 #pragma unroll
   for (int pass = 0; pass < (BWD ? 2 : 1); ++pass) {
@@ -215,19 +216,18 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
-        for (int i = 0; i < PARTS; ++i) kf[i][w][ks][lane] = qr[ks][i];
+        for (int i = 0; i < PARTS; ++i)
+          *reinterpret_cast<v8bf*>(&km[i][row][ks * 32 + (lane >> 4) * 8]) = qr[ks][i];
       __syncthreads();
     }
-    for (int f = w; f < PARTS * (DKP / 16) * 2; f += 4) {
-      const int ks = f & 1, rt = (f >> 1) % (DKP / 16), part = f / (DKP / 8);
-      const int d = (rt >> 1) * 32 + 8 * ((lane & 15) >> 2) + 4 * (rt & 1) + (lane & 3);
-      v8bf t;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int i = ks * 32 + (lane >> 4) * 8 + e;
-        t[e] = kf[part][i >> 4][d >> 5][(i & 15) + 16 * ((d & 31) >> 3)][d & 7];
-      }
-      *reinterpret_cast<v8bf*>(to + (size_t)f * kFrag + lane * 16) = t;
+    for (int f = 0; f < DKP / 32; ++f) {   // tiles w, w + 4, ... of DKP / 16, both k steps
+      const int at = w + 4 * f, rt = at >> 1, ks = at & 1;
+      v8bf t[PARTS];
+      get_tr<PARTS, 8>(km, 32 * ks, 32 * (rt >> 1) + 4 * (rt & 1), lane & 15, lane >> 4, t);
+#pragma unroll
+      for (int q = 0; q < PARTS; ++q)
+        *reinterpret_cast<v8bf*>(to + (size_t)((q * (DKP / 16) + rt) * 2 + ks) * kFrag + lane * 16) = t[q];
     }
   }
 }
