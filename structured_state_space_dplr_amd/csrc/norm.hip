@@ -478,7 +478,10 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
       }
     }
   }
-  if constexpr (EPT > 0) {
+  if constexpr (EPT == 0) {
+    if (part && first)   // no positions at all
+      for (int d = threadIdx.x; d < D; d += 64 * kChWaves) pg[d] = pb[d] = 0.f;
+  } else {
     if (!part) return;
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {

@@ -124,6 +124,18 @@ def test_channels(s4, D, outer, inner, dtype):
     check(s4, (outer, D, inner), 1, dtype, seed=D + inner)
 
 
+@pytest.mark.parametrize("D", [64, 256, 300])
+def test_channels_of_no_batch(s4, D):
+    x, gamma, _, _ = make((0, D, 5), D, F32, 1)
+    x, gamma = x.cuda(), gamma.cuda()
+    st = torch.empty(0, 5, device="cuda")
+    dg, db = torch.full((D,), 7.0, device="cuda"), torch.full((D,), 7.0, device="cuda")
+    ws = torch.full((s4.layer_norm_workspace_bytes(x, 1),), 77, dtype=torch.uint8, device="cuda")
+    s4.layer_norm_fwd(x, gamma, None, torch.empty_like(x), st, st, axis=1)
+    s4.layer_norm_bwd(x, gamma, st, st, x, torch.empty_like(x), dg, db, ws, axis=1)
+    assert bool((dg == 0).all()) and bool((db == 0).all())
+
+
 def test_channels_half(s4):
     check(s4, (4, 33, 129), 1, F16)
 
