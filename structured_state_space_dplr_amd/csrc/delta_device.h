@@ -83,26 +83,18 @@ __device__ __forceinline__ void split4(v4f x, v4bf (&out)[P]) {
   }
 }
 
-// N elements of one row, zero behind the first n.
-template <int N, typename T>
-__device__ __forceinline__ void load_n(const T* p, int n, float* out) {
-  if (n >= N) {
-    T t[N];
-    __builtin_memcpy(t, p, sizeof(t));
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = to_f32(t[i]);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) out[i] = i < n ? to_f32(p[i]) : 0.f;
-  }
-}
+// Eight elements of one row, zero behind the first n.
 template <typename T>
 __device__ __forceinline__ void load8(const T* p, int n, float* out) {
-  load_n<8>(p, n, out);
-}
-template <typename T>
-__device__ __forceinline__ void load4(const T* p, int n, float* out) {
-  load_n<4>(p, n, out);
+  if (n >= 8) {
+    T t[8];
+    __builtin_memcpy(t, p, sizeof(t));
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = to_f32(t[i]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) out[i] = i < n ? to_f32(p[i]) : 0.f;
+  }
 }
 
 // Eight floats, the first n of them.
@@ -193,20 +185,23 @@ __device__ __forceinline__ bool slice_of(int heads, int slices, int* head, int* 
   return *head < heads;
 }
 
-// The sequence whose chunks include `slot`, by all lanes of a wave together:
-// sequences with first(s) <= slot are counted.
+// The sequence whose chunks include `slot`, by all lanes of a wave together: the last
+// with first(s) <= slot, 64 sequences probed at a time (first(s) rises with s; for
+// offsets out of order some sequence is returned, and the caller's bounds hold).
 __device__ __forceinline__ int sequence_of(const s4dplr_delta_plan& p, const int* offsets,
                                            long slot) {
   const int lane = threadIdx.x & 63;
-  int n = 0;
-  for (int s0 = 0; s0 < p.sequences; s0 += 64) {
-    const int s = s0 + lane;
-    const bool le = s < p.sequences && rows_of(p, offsets, s).first(s) <= slot;
+  int s = 0;
+  for (int n = p.sequences;;) {   // sequences s .. s + n are left
+    const int step = (n + 63) / 64, at = lane * step;
+    const bool le = at < n && rows_of(p, offsets, s + at).first(s + at) <= slot;
     const int c = __popcll(__ballot(le));
-    n += c;
-    if (c < 64) break;
+    if (c == 0) return s;
+    s += (c - 1) * step;
+    n -= (c - 1) * step;
+    if (step == 1) return s;
+    n = n < step ? n : step;
   }
-  return n > 0 ? n - 1 : 0;
 }
 
 }  // namespace s4

@@ -176,6 +176,18 @@ def test_many_sequences(s4):
     check_forward(s4, inputs(1, offsets[-1] + 3, 150, 1, 1, 16, 16, BF), 150, offsets)
 
 
+@pytest.mark.parametrize("S", [65, 4097])
+def test_thousands_of_packed_sequences(s4, S):
+    # three of them are longer than a chunk, a third is empty
+    gen = torch.Generator().manual_seed(S)
+    lengths = torch.randint(0, 3, (S,), generator=gen)
+    lengths[torch.tensor([0, S // 2, S - 1])] = torch.tensor([70, 130, 65])
+    offsets = [0] + torch.cumsum(lengths, 0).tolist()
+    x = inputs(S, offsets[-1], S, 1, 1, 8, 8, F32)
+    check_forward(s4, x, S, offsets)
+    check_backward(s4, x, S, offsets)
+
+
 @pytest.mark.parametrize("T", [8, 130])
 @pytest.mark.parametrize("reset", [-math.inf, torch.finfo(torch.float32).min, -1e4, -150.0, -60.0])
 def test_resets(s4, reset, T):
