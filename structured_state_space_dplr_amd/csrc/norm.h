@@ -8,7 +8,9 @@
 namespace s4 {
 
 constexpr long kNormMaxD = 32768;      // a row of 16 waves, 32 values a lane
-constexpr long kNormBlocks = 2048;     // blocks of the forward pass over rows: eight a CU
+// Blocks of the forward pass over rows: eight a CU (16: 8192 x 8192 bf16 45.1 -> 50.5 us,
+// and no row gains over 5 %); two of 16 waves.
+constexpr long kNormBlocks = 2048;
 
 struct NormArgs {
   const void* x;
@@ -23,11 +25,14 @@ struct NormArgs {
 };
 
 // Blocks of the backward pass, the rows of its partial sums [2][parts][D]: one
-// per tile of work (a row, 4 rows up to 1024 values, or 64 positions) up to four a CU,
-// one where a row takes 16 waves.
+// per tile of work (a row, 4 rows up to 512 values, or 64 positions) up to four a CU, two
+// with 8 waves each, one where a row takes 4 waves of 32 values a lane or 16 waves
+// (twice as many blocks each: 16384 x 2048 bf16 40.4 -> 50.5 us, 8192 x 8192 bf16 81.4 ->
+// 87.5, for the partial sums' traffic).  Above 16384 values the columns' sums have
+// their own kernel, whose blocks take a strip of columns each.
 inline long norm_parts(long outer, long D, long inner) {
   const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;
-  const long most = inner > 1 ? 512 : D > 4096 ? 256 : 1024;
+  const long most = inner > 1 ? 512 : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
   return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 

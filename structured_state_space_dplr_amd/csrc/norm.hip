@@ -82,6 +82,17 @@ struct RowPart {
   }
 };
 
+// Rows of 32 values a lane: 16 waves have 128 registers a lane, and gamma and beta are
+// read where they are used.
+constexpr bool wide_rows(int values, int waves) { return waves > 4 && values > 16; }
+
+// The same value, unknown to the compiler: a load at it is not taken out of the loop, where
+// its result would be kept in registers and spilled.
+__device__ __forceinline__ int opaque(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 // Forward over rows.  WPR waves share a row (blocks of 256 threads hold 4 rows at WPR =
 // 1), and a block walks over rows blockIdx, blockIdx + gridDim, ..., the next row on its
 // way while one is computed: gamma and beta are read once.  A wave takes mean and
@@ -102,9 +113,12 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
   if (row >= rows) return;   // WPR > 1: the whole block
   Part next;
   next.load(x + row * D, D, tid);
-  float gm[E], bt[E];
-  Part::columns(gamma, D, tid, 1.f, gm);
-  Part::columns(beta, D, tid, 0.f, bt);
+  constexpr bool kWide = wide_rows(E, WPR);
+  float gm[kWide ? 1 : E], bt[kWide ? 1 : E];
+  if constexpr (!kWide) {
+    Part::columns(gamma, D, tid, 1.f, gm);
+    Part::columns(beta, D, tid, 0.f, bt);
+  }
   // elements of the wave's part
   float n = (float)D;
   if constexpr (WPR > 1) {
@@ -163,12 +177,46 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
       }
     }
     const float r = 1.f / sqrtf(q / (float)D + eps);
+    if constexpr (kWide) {
+      using One = RowPart<T, 1, WPR, WHOLE>;
+      const int t0 = opaque(tid);
 #pragma unroll
-    for (int i = 0; i < E; ++i) v[i] = fmaf((v[i] - m) * r, gm[i], bt[i]);
-    Part::store(y + here * D, D, tid, v);
+      for (int i = 0; i < NV; ++i) {
+        float g[VEC], b[VEC], *u = v + i * VEC;
+        One::columns(gamma, D, t0 + i * WPR * 64, 1.f, g);
+        One::columns(beta, D, t0 + i * WPR * 64, 0.f, b);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) u[j] = fmaf((u[j] - m) * r, g[j], b[j]);
+        One::store(y + here * D, D, t0 + i * WPR * 64, u);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < E; ++i) v[i] = fmaf((v[i] - m) * r, gm[i], bt[i]);
+      Part::store(y + here * D, D, tid, v);
+    }
     if (tid == 0) {
       if (mean) mean[here] = m;
       if (rstd) rstd[here] = r;
+    }
+  }
+}
+
+// Both sums over the waves of a row, in every lane; `red` is used in turn.
+template <int WPR>
+__device__ __forceinline__ void block_sums(float& s1, float& s2, float (&red)[2][WPR]) {
+  s1 = sum64(s1);
+  s2 = sum64(s2);
+  if constexpr (WPR > 1) {
+    if ((threadIdx.x & 63) == 0) {
+      red[0][threadIdx.x >> 6] = s1;
+      red[1][threadIdx.x >> 6] = s2;
+    }
+    __syncthreads();
+    s1 = s2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < WPR; ++i) {
+      s1 += red[0][i];
+      s2 += red[1][i];
     }
   }
 }
@@ -228,21 +276,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
       gv[i] = w;
     }
     if (dx) {
-      s1 = sum64(s1);
-      s2 = sum64(s2);
-      if constexpr (WPR > 1) {
-        if ((threadIdx.x & 63) == 0) {
-          red[turn][0][threadIdx.x >> 6] = s1;
-          red[turn][1][threadIdx.x >> 6] = s2;
-        }
-        __syncthreads();
-        s1 = s2 = 0.f;
-#pragma unroll
-        for (int i = 0; i < WPR; ++i) {
-          s1 += red[turn][0][i];
-          s2 += red[turn][1][i];
-        }
-      }
+      block_sums<WPR>(s1, s2, red[turn]);
       s1 /= (float)D;
       s2 /= (float)D;
 #pragma unroll
@@ -280,6 +314,108 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
           if (c + j < D) o[j] = a[i * VEC + j];
       }
     }
+  }
+}
+
+// Backward over wide rows, in two kernels, since a row's columns leave no registers for
+// their sums: dx by rows (x and dy are read again behind the row's sums, from the
+// caches), and the columns' sums.
+template <typename T, int WPR, bool WHOLE>
+__global__ __launch_bounds__(64 * WPR) void norm_wide_dx_kernel(
+    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx, long rows,
+    int D) {
+  using One = RowPart<T, 1, WPR, WHOLE>;
+  constexpr int VEC = One::VEC, STEP = 64 * WPR;
+  __shared__ float red[2][2][WPR];
+  const int tid = threadIdx.x;
+  int turn = 0;
+  for (long row = blockIdx.x; row < rows; row += gridDim.x, turn ^= 1) {
+    const T *xr = x + row * D, *gr = dy + row * D;
+    T* dr = dx + row * D;
+    const float m = mean[row], r = rstd[row];
+    auto vectors = [&](auto f) {   // f(at, xh, dy gamma); a whole step is inside or partly
+      One xo, go;
+      float xv[VEC], gv[VEC], g[VEC];
+#pragma unroll 2
+      for (int at = tid; at * VEC < D; at += STEP) {
+        xo.load(xr, D, at);
+        go.load(gr, D, at);
+        One::columns(gamma, D, at, 1.f, g);
+        xo.get(D, at, xv);
+        go.get(D, at, gv);
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) {
+          xv[j] = (xv[j] - m) * r;
+          gv[j] *= g[j];
+        }
+        f(at, xv, gv);
+      }
+    };
+    float s1 = 0.f, s2 = 0.f;
+    vectors([&](int, const float* xh, const float* w) {
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {   // behind D, w = 0: nothing is added
+        s1 += w[j];
+        s2 = fmaf(w[j], xh[j], s2);
+      }
+    });
+    block_sums<WPR>(s1, s2, red[turn]);
+    s1 /= (float)D;
+    s2 /= (float)D;
+    vectors([&](int at, const float* xh, const float* w) {
+      float o[VEC];
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) o[j] = r * (w[j] - s1 - xh[j] * s2);
+      One::store(dr, D, at, o);
+    });
+  }
+}
+
+// Block: 64 vectors of columns, the rows blockIdx.y 4 + wave and on by gridDim.y 4.
+template <typename T, bool WHOLE>
+__global__ __launch_bounds__(256) void norm_wide_sums_kernel(
+    const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const T* __restrict__ dy, float* __restrict__ part, long rows, int D) {
+  using One = RowPart<T, 1, 1, WHOLE>;
+  constexpr int VEC = One::VEC;
+  __shared__ float red[3][2][VEC][64];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int at = blockIdx.x * 64 + lane;
+  float ag[VEC], ab[VEC];
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) ag[j] = ab[j] = 0.f;
+#pragma unroll 4
+  for (long row = blockIdx.y * 4 + w; row < rows; row += gridDim.y * 4) {
+    One xo, go;
+    float xv[VEC], gv[VEC];
+    xo.load(x + row * D, D, at);
+    go.load(dy + row * D, D, at);
+    const float m = mean[row], r = rstd[row];
+    xo.get(D, at, xv);
+    go.get(D, at, gv);
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      ag[j] = fmaf(gv[j], (xv[j] - m) * r, ag[j]);
+      ab[j] += gv[j];
+    }
+  }
+  if (w > 0)
+#pragma unroll
+    for (int j = 0; j < VEC; ++j) {
+      red[w - 1][0][j][lane] = ag[j];
+      red[w - 1][1][j][lane] = ab[j];
+    }
+  __syncthreads();
+  if (w > 0) return;
+  float* pg = part + (size_t)blockIdx.y * D;
+  float* pb = part + ((size_t)gridDim.y + blockIdx.y) * D;
+#pragma unroll
+  for (int j = 0; j < VEC; ++j) {
+    const int c = at * VEC + j;
+    if (c >= D) continue;
+    pg[c] = ag[j] + ((red[0][0][j][lane] + red[1][0][j][lane]) + red[2][0][j][lane]);
+    pb[c] = ab[j] + ((red[0][1][j][lane] + red[1][1][j][lane]) + red[2][1][j][lane]);
   }
 }
 
@@ -561,9 +697,20 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
     row_shape<T>(D, [&](auto nv, auto wpr, auto whole) {
       constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
       constexpr bool W = decltype(whole)::value;
-      norm_rows_bwd_kernel<T, NV, WPR, W>
-          <<<dim3(nb), WPR > 4 ? 64 * WPR : kRowThreads, 0, s>>>(x, a.gamma, a.mean, a.rstd, dy, dx,
-                                                                 part, a.outer, D);
+      if constexpr (wide_rows(NV * Vec<T>::N, WPR)) {
+        if (dx && a.outer > 0)
+          norm_wide_dx_kernel<T, WPR, W>
+              <<<dim3((unsigned)(a.outer < 512 ? a.outer : 512)), 64 * WPR, 0, s>>>(
+                  x, a.gamma, a.mean, a.rstd, dy, dx, a.outer, D);
+        if (part)
+          norm_wide_sums_kernel<T, W>
+              <<<dim3((unsigned)ceil_div(D, 64 * Vec<T>::N), nb), 256, 0, s>>>(
+                  x, a.mean, a.rstd, dy, part, a.outer, D);
+      } else {
+        norm_rows_bwd_kernel<T, NV, WPR, W>
+            <<<dim3(nb), WPR > 4 ? 64 * WPR : kRowThreads, 0, s>>>(x, a.gamma, a.mean, a.rstd, dy,
+                                                                   dx, part, a.outer, D);
+      }
     });
   } else {
 #define S4_GO(ept)                                                                   \

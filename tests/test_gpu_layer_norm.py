@@ -111,6 +111,31 @@ def test_row_counts(s4, rows):
     check(s4, (rows, 2049), -1, BF, seed=rows)
 
 
+@pytest.mark.parametrize("D", [16392, 32765])
+@pytest.mark.parametrize("dtype", [F32, BF])
+def test_wide_rows_left_out(s4, D, dtype):
+    x, gamma, beta, dy = make((517, D), D, dtype, 3)
+    full = run(s4, x, gamma, beta, dy, -1)[3]
+    for skip in (("dx",), ("dgamma",), ("dgamma", "dbeta")):
+        part = run(s4, x, gamma, beta, dy, -1, skip=skip)[3]
+        assert all(part[n] is None or torch.equal(part[n], full[n]) for n in full)
+    X, g = x[500:].double(), dy.double()
+    r = ((X - X.mean(1, keepdim=True)).square().mean(1, keepdim=True) + 1e-5).rsqrt()
+    xh = (X - X.mean(1, keepdim=True)) * r
+    w = g[500:] * gamma.double()
+    ref = r * (w - w.mean(1, keepdim=True) - xh * (w * xh).mean(1, keepdim=True))
+    spread = xh.abs().amax(1, keepdim=True)
+    close(full["dx"][500:], ref, "dx", r * w.abs().amax(1, keepdim=True) * spread * spread)
+    a = g.abs().sum(0)
+    close(full["dbeta"], g.sum(0), "dbeta", a)
+
+
+def test_wide_rows_of_no_batch(s4):
+    x, gamma, beta, dy = make((0, 20000), 20000, BF, 3)
+    g = run(s4, x, gamma, beta, dy, -1)[3]
+    assert bool((g["dgamma"] == 0).all()) and bool((g["dbeta"] == 0).all())
+
+
 def test_leading_dimensions(s4):
     check(s4, (3, 5, 2, 96), 3, BF)
     check(s4, (2, 3, 48, 7), 2, F32)
