@@ -12,6 +12,8 @@ constexpr long kNormMaxD = 32768;      // a row of 16 waves, 32 values a lane
 // and no row gains over 5 %); two of 16 waves.
 constexpr long kNormBlocks = 2048;
 
+constexpr long kNormChannels = 256;    // fp32 channels whose sums stay in registers
+
 struct NormArgs {
   const void* x;
   const float *gamma, *beta;
@@ -29,10 +31,11 @@ struct NormArgs {
 // with 8 waves each, one where a row takes 4 waves of 32 values a lane or 16 waves
 // (twice as many blocks each: 16384 x 2048 bf16 40.4 -> 50.5 us, 8192 x 8192 bf16 81.4 ->
 // 87.5, for the partial sums' traffic).  Above 16384 values the columns' sums have
-// their own kernel, whose blocks take a strip of columns each.
+// their own kernel, whose blocks take a strip of columns each, and so have those of
+// channels above kNormChannels (16-bit elements: above 64, which use 64 parts of them).
 inline long norm_parts(long outer, long D, long inner) {
   const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;
-  const long most = inner > 1 ? 512 : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
+  const long most = inner > 1 ? (D > kNormChannels ? 64 : 512) : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
   return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 

@@ -9,7 +9,10 @@
 // registers), so a large common offset costs no digits.
 //
 // Both directions are bound by HBM: forward reads x and writes y, backward reads
-// x and dy and writes dx.
+// x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 46 us (5.8 TB/s,
+// part of it from the last-level cache), backward of 16384 x 2048 41 us with the columns'
+// sums (4.9 TB/s); fp32 channels 32 x 256 x 1024: 15.7 us (4.3 TB/s) and 34.6 us (2.9
+// TB/s, where each wave's loads are one line a channel).
 #include "norm.h"
 
 #include "vec.h"
@@ -82,8 +85,8 @@ struct RowPart {
   }
 };
 
-// Rows of 32 values a lane: 16 waves have 128 registers a lane, and gamma and beta are
-// read where they are used.
+// Rows of 32 values a lane over 16 waves: those have 128 registers a lane, so gamma and beta
+// are read where they are used (2048 x 32768 bf16 108 -> 72 us).
 constexpr bool wide_rows(int values, int waves) { return waves > 4 && values > 16; }
 
 // The same value, unknown to the compiler: a load at it is not taken out of the loop, where
@@ -319,7 +322,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
 
 // Backward over wide rows, in two kernels, since a row's columns leave no registers for
 // their sums: dx by rows (x and dy are read again behind the row's sums, from the
-// caches), and the columns' sums.
+// caches), and the columns' sums.  2048 x 32768 bf16 160 us (in one kernel, which spilled,
+// 639), 512 x 32768 fp32 80 (314).
 template <typename T, int WPR, bool WHOLE>
 __global__ __launch_bounds__(64 * WPR) void norm_wide_dx_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
@@ -446,187 +450,332 @@ __global__ __launch_bounds__(1024) void norm_columns_kernel(const float* __restr
 
 // ------------------------------------------------------- inner > 1: channels
 
-// Lanes take 64 neighbouring positions (o, i) of the flattened outer x inner
-// axis, so a wave reads a line of one channel; the block's 8 waves take the
-// channels d = w, w + 8, ...  EPT > 0 (D <= 8 EPT): the values stay in
-// registers; EPT = 0: they are read again, from the caches where they fit.
-constexpr int kChWaves = 8;
+// Lanes take neighbouring positions (o, i) of the flattened outer x inner axis, so a wave
+// reads a line of one channel; the block's W waves take the channels d = w, w + W, ....
+// VP positions a lane: two of 16 bits where inner is even, so that they lie side by
+// side.  EPT > 0 (D <= W EPT): a lane's elements stay in its registers as they came;
+// EPT = 0: they are read again, from the caches where they fit.
+template <typename T, int VP>
+struct Pack {
+  T v[VP];
+};
+template <typename T, int VP>
+__device__ __forceinline__ Pack<T, VP> load_pack(const T* p) {
+  Pack<T, VP> r;
+  __builtin_memcpy(&r, p, sizeof(r));
+  return r;
+}
+// Channel d of D at a lane's positions.  Elements of 16 bits are read without a branch, a
+// missing one from channel 0 (a load into half a register is waited for at a branch: 59
+// us instead of 30 for the gradients of 32 x 256 x 1024 bf16); of 32 bits, under the
+// condition (33.0 us against 35.4 in fp32).  What a missing one holds is not used.
+template <typename T, int VP>
+__device__ __forceinline__ Pack<T, VP> load_channel(const T* p, int d, int D, unsigned inner,
+                                                    bool on) {
+  if constexpr (sizeof(T) == 2) return load_pack<T, VP>(p + (long)(d < D ? d : 0) * inner);
+  Pack<T, VP> r = {};
+  if (on && d < D) r = load_pack<T, VP>(p + (long)d * inner);
+  return r;
+}
+// Two floats of a converted pair are not worth keeping for the next pass.
+template <typename T, int VP>
+__device__ __forceinline__ void forget(Pack<T, VP>& x) {
+  if constexpr (sizeof(x) == 4) {
+    int t;
+    __builtin_memcpy(&t, &x, 4);
+    t = opaque(t);
+    __builtin_memcpy(&x, &t, 4);
+  }
+}
 
-template <int NS>
-__device__ __forceinline__ void wave_sums(float (&s)[NS], float (*red)[kChWaves][64], int w,
+// s[k] summed over the block's waves, position by position.
+template <int NS, int W, int VP>
+__device__ __forceinline__ void wave_sums(float (&s)[NS][VP], float (*red)[W][64 * VP], int w,
                                           int lane) {
 #pragma unroll
-  for (int k = 0; k < NS; ++k) red[k][w][lane] = s[k];
+  for (int k = 0; k < NS; ++k)
+#pragma unroll
+    for (int q = 0; q < VP; ++q) red[k][w][lane * VP + q] = s[k][q];
   __syncthreads();
 #pragma unroll
-  for (int k = 0; k < NS; ++k) {
-    float t = 0.f;
+  for (int k = 0; k < NS; ++k)
 #pragma unroll
-    for (int i = 0; i < kChWaves; ++i) t += red[k][i][lane];
-    s[k] = t;
-  }
+    for (int q = 0; q < VP; ++q) {
+      float t = 0.f;
+#pragma unroll
+      for (int i = 0; i < W; ++i) t += red[k][i][lane * VP + q];
+      s[k][q] = t;
+    }
 }
 
-template <typename T, int EPT>
-__global__ __launch_bounds__(64 * kChWaves) void norm_channels_kernel(
+// Where a lane's positions lie.
+template <int VP>
+struct Positions {
+  bool on;
+  unsigned pos;
+  long at;   // element of channel 0
+  __device__ __forceinline__ Positions(unsigned tile, int lane, unsigned positions, int D,
+                                       unsigned inner) {
+    pos = (tile * 64 + lane) * VP;
+    on = pos < positions;
+    const unsigned o = on ? pos / inner : 0;
+    at = (long)o * D * inner + (on ? pos - o * inner : 0);
+  }
+};
+
+template <typename T, int EPT, int W, int VP>
+__global__ __launch_bounds__(64 * W) void norm_channels_kernel(
     const T* x, const float* __restrict__ gamma, const float* __restrict__ beta, T* y,
-    float* __restrict__ mean, float* __restrict__ rstd, long outer, int D, long inner, float eps) {
-  __shared__ float red[2][1][kChWaves][64];
+    float* __restrict__ mean, float* __restrict__ rstd, unsigned positions, int D, unsigned inner,
+    float eps) {
+  using P = Pack<T, VP>;
+  __shared__ float red[2][1][W][64 * VP];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long pos = (long)blockIdx.x * 64 + lane;
-  const bool on = pos < outer * inner;
-  const long o = on ? pos / inner : 0, i0 = on ? pos - o * inner : 0;
-  const T* xp = x + o * D * inner + i0;
-  float v[EPT > 0 ? EPT : 1];
-  float s[1] = {0.f};
-  if constexpr (EPT > 0) {
+  const unsigned tiles = (positions + 64 * VP - 1) / (64 * VP);
+  for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const Positions<VP> ps(tile, lane, positions, D, inner);
+    const bool on = ps.on;
+    const T* xp = x + ps.at;
+    P v[EPT > 0 ? EPT : 1];
+    // every channel of the wave: f(k, d)
+    auto channels = [&](auto f) {
+      if constexpr (EPT > 0) {
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int d = w + kChWaves * k;
-      v[k] = on && d < D ? to_f32(xp[d * inner]) : 0.f;
-      s[0] += v[k];
-    }
-  } else if (on) {
+        for (int k = 0; k < EPT; ++k) f(k, w + W * k);
+      } else {
 #pragma unroll 8
-    for (int d = w; d < D; d += kChWaves) s[0] += to_f32(xp[d * inner]);
-  }
-  wave_sums(s, red[0], w, lane);
-  const float m = s[0] / (float)D;
-  s[0] = 0.f;
-  if constexpr (EPT > 0) {
+        for (int d = w; d < D; d += W) {
+          v[0] = load_channel<T, VP>(xp, d, D, inner, on);
+          f(0, d);
+        }
+      }
+    };
+    if constexpr (EPT > 0)
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      v[k] -= m;
-      s[0] += w + kChWaves * k < D ? v[k] * v[k] : 0.f;
-    }
-  } else if (on) {
-#pragma unroll 8
-    for (int d = w; d < D; d += kChWaves) {
-      const float t = to_f32(xp[d * inner]) - m;
-      s[0] = fmaf(t, t, s[0]);
-    }
-  }
-  wave_sums(s, red[1], w, lane);
-  const float r = 1.f / sqrtf(s[0] / (float)D + eps);
-  if (!on) return;
-  T* yp = y + o * D * inner + i0;
-  if constexpr (EPT > 0) {
+      for (int k = 0; k < EPT; ++k) v[k] = load_channel<T, VP>(xp, w + W * k, D, inner, on);
+    float s[1][VP], m[VP], r[VP];
 #pragma unroll
-    for (int k = 0; k < EPT; ++k) {
-      const int d = w + kChWaves * k;
-      if (d < D)
-        yp[d * inner] = from_f32<T>(
-            fmaf(v[k] * r, gamma ? gamma[d] : 1.f, beta ? beta[d] : 0.f));
+    for (int q = 0; q < VP; ++q) s[0][q] = 0.f;
+    channels([&](int k, int d) {
+#pragma unroll
+      for (int q = 0; q < VP; ++q) s[0][q] += d < D ? to_f32(v[k].v[q]) : 0.f;
+      if constexpr (EPT > 0) forget(v[k]);
+    });
+    wave_sums<1, W, VP>(s, red[0], w, lane);
+#pragma unroll
+    for (int q = 0; q < VP; ++q) {
+      m[q] = s[0][q] / (float)D;
+      s[0][q] = 0.f;
     }
-  } else {
-#pragma unroll 8
-    for (int d = w; d < D; d += kChWaves)
-      yp[d * inner] = from_f32<T>(fmaf((to_f32(xp[d * inner]) - m) * r, gamma ? gamma[d] : 1.f,
-                                       beta ? beta[d] : 0.f));
-  }
-  if (w == 0) {
-    if (mean) mean[pos] = m;
-    if (rstd) rstd[pos] = r;
+    channels([&](int k, int d) {
+#pragma unroll
+      for (int q = 0; q < VP; ++q) {
+        const float t = to_f32(v[k].v[q]) - m[q];
+        s[0][q] = d < D ? fmaf(t, t, s[0][q]) : s[0][q];
+      }
+      if constexpr (EPT > 0) forget(v[k]);
+    });
+    wave_sums<1, W, VP>(s, red[1], w, lane);
+#pragma unroll
+    for (int q = 0; q < VP; ++q) r[q] = 1.f / sqrtf(s[0][q] / (float)D + eps);
+    if (!on) continue;   // red[0] is free: every wave has passed the second barrier
+    T* yp = y + ps.at;
+    channels([&](int k, int d) {
+      if (d >= D) return;
+      const float g = gamma ? gamma[d] : 1.f, b = beta ? beta[d] : 0.f;
+      P t;
+#pragma unroll
+      for (int q = 0; q < VP; ++q)
+        t.v[q] = from_f32<T>(fmaf((to_f32(v[k].v[q]) - m[q]) * r[q], g, b));
+      __builtin_memcpy(yp + (long)d * inner, &t, sizeof(t));
+    });
+    if (w == 0)
+#pragma unroll
+      for (int q = 0; q < VP; ++q) {
+        if (mean) mean[ps.pos + q] = m[q];
+        if (rstd) rstd[ps.pos + q] = r[q];
+      }
   }
 }
 
-// Backward: a block walks over tiles of 64 positions.  EPT > 0: dgamma and dbeta
-// of the thread's channels are summed in registers over the tiles and over the
-// lanes at the end; EPT = 0: over the lanes in every tile, into the block's own
-// row of part (no other block touches it).
+// dx alone, for more channels than the fused kernel holds sums of: 256 in fp32 (32 x 256 x
+// 1024: fused 34.6 us, apart 45.4), 64 of 16 bits, whose loads carry two positions here
+// (32 x 256 x 1024 bf16 24.5 us against 30.6, 8 x 256 x 256 16.2 against 14.7, 128 x 256 x
+// 1024 73.0 against 67.4).  x and dy are read again for dx, from the caches (kept in
+// registers, up to 512 channels: 58.3 us instead of 40.5 with the sums for 32 x 512 x 1024
+// bf16, 77.5 instead of 72.7 in fp32).
+template <typename T, int W, int VP>
+__global__ __launch_bounds__(64 * W) void norm_channels_dx_kernel(
+    const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
+    const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
+    unsigned positions, int D, unsigned inner) {
+  using P = Pack<T, VP>;
+  __shared__ float red[2][2][W][64 * VP];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const unsigned tiles = (positions + 64 * VP - 1) / (64 * VP);
+  int turn = 0;
+  for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    const Positions<VP> ps(tile, lane, positions, D, inner);
+    const bool on = ps.on;
+    float m[VP], r[VP];
+#pragma unroll
+    for (int q = 0; q < VP; ++q) {
+      m[q] = on ? mean[ps.pos + q] : 0.f;
+      r[q] = on ? rstd[ps.pos + q] : 0.f;
+    }
+    auto channels = [&](auto f) {   // f(d, xh, dy gamma)
+#pragma unroll 4
+      for (int d = w; d < D; d += W) {
+        const P v = load_channel<T, VP>(x + ps.at, d, D, inner, on);
+        const P g = load_channel<T, VP>(dy + ps.at, d, D, inner, on);
+        const float gm = gamma ? gamma[d] : 1.f;
+        float xh[VP], wg[VP];
+#pragma unroll
+        for (int q = 0; q < VP; ++q) {
+          xh[q] = (to_f32(v.v[q]) - m[q]) * r[q];
+          wg[q] = to_f32(g.v[q]) * gm;
+        }
+        f(d, xh, wg);
+      }
+    };
+    float s[2][VP];
+#pragma unroll
+    for (int q = 0; q < VP; ++q) s[0][q] = s[1][q] = 0.f;
+    channels([&](int, const float* xh, const float* wg) {
+#pragma unroll
+      for (int q = 0; q < VP; ++q) {
+        s[0][q] += wg[q];
+        s[1][q] = fmaf(wg[q], xh[q], s[1][q]);
+      }
+    });
+    wave_sums<2, W, VP>(s, red[turn], w, lane);
+#pragma unroll
+    for (int q = 0; q < VP; ++q) {
+      s[0][q] /= (float)D;
+      s[1][q] /= (float)D;
+    }
+    if (!on) continue;   // no barrier behind this
+    channels([&](int d, const float* xh, const float* wg) {
+      P t;
+#pragma unroll
+      for (int q = 0; q < VP; ++q) t.v[q] = from_f32<T>(r[q] * (wg[q] - s[0][q] - xh[q] * s[1][q]));
+      __builtin_memcpy(dx + ps.at + (long)d * inner, &t, sizeof(t));
+    });
+  }
+}
+
+// The columns' sums for the same: a wave takes kSums channels, its lanes V positions
+// each (16 bytes where inner is a multiple of them, else one), and the block's row of
+// part the tiles blockIdx.y, blockIdx.y + gridDim.y, ....
+constexpr int kSums = 4;
+
+template <typename T, int V>
+__global__ __launch_bounds__(256) void norm_channels_sums_kernel(
+    const T* __restrict__ x, const float* __restrict__ mean, const float* __restrict__ rstd,
+    const T* __restrict__ dy, float* __restrict__ part, unsigned positions, int D,
+    unsigned inner) {
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int d0 = (blockIdx.x * 4 + w) * kSums;
+  if (d0 >= D) return;
+  const unsigned tiles = (positions + 64 * V - 1) / (64 * V);
+  float ag[kSums], ab[kSums];
+#pragma unroll
+  for (int c = 0; c < kSums; ++c) ag[c] = ab[c] = 0.f;
+  for (unsigned tile = blockIdx.y; tile < tiles; tile += gridDim.y) {
+    const Positions<V> ps(tile, lane, positions, D, inner);
+    if (!ps.on) continue;
+    float m[V], r[V];
+    __builtin_memcpy(m, mean + ps.pos, sizeof(m));
+    __builtin_memcpy(r, rstd + ps.pos, sizeof(r));
+    Pack<T, V> v[kSums], g[kSums];
+#pragma unroll
+    for (int c = 0; c < kSums; ++c) {   // channels behind D: the last one, not written
+      const long at = ps.at + (long)(d0 + c < D ? d0 + c : D - 1) * inner;
+      v[c] = load_pack<T, V>(x + at);
+      g[c] = load_pack<T, V>(dy + at);
+    }
+#pragma unroll
+    for (int c = 0; c < kSums; ++c)
+#pragma unroll
+      for (int q = 0; q < V; ++q) {
+        const float t = to_f32(g[c].v[q]);
+        ag[c] = fmaf(t, (to_f32(v[c].v[q]) - m[q]) * r[q], ag[c]);
+        ab[c] += t;
+      }
+  }
+#pragma unroll
+  for (int c = 0; c < kSums; ++c) {
+    const float tg = sum64(ag[c]), tb = sum64(ab[c]);
+    if (lane == 0 && d0 + c < D) {
+      part[(size_t)blockIdx.y * D + d0 + c] = tg;
+      part[((size_t)gridDim.y + blockIdx.y) * D + d0 + c] = tb;
+    }
+  }
+}
+
+// Backward, up to 8 EPT channels: a block walks over tiles of 64 positions; dgamma and
+// dbeta of the thread's channels are summed in registers over the tiles and over the
+// lanes at the end.
+constexpr int kChWaves = 8;
+
 template <typename T, int EPT>
 __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
     const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
-    float* __restrict__ part, long outer, int D, long inner) {
+    float* __restrict__ part, unsigned positions, int D, unsigned inner) {
   __shared__ float red[2][2][kChWaves][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const long positions = outer * inner, tiles = (positions + 63) / 64;
-  float* pg = part ? part + (size_t)blockIdx.x * D : nullptr;
-  float* pb = part ? part + ((size_t)gridDim.x + blockIdx.x) * D : nullptr;
-  constexpr int E = EPT > 0 ? EPT : 1;
-  float ag[E], ab[E];
+  const unsigned tiles = (positions + 63) / 64;
+  float ag[EPT], ab[EPT];
 #pragma unroll
-  for (int k = 0; k < E; ++k) ag[k] = ab[k] = 0.f;
+  for (int k = 0; k < EPT; ++k) ag[k] = ab[k] = 0.f;
   int turn = 0;
-  bool first = true;
-  for (long tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1, first = false) {
-    const long pos = tile * 64 + lane;
-    const bool on = pos < positions;
-    const long o = on ? pos / inner : 0, i0 = on ? pos - o * inner : 0;
-    const T* xp = x + o * D * inner + i0;
-    const T* gp = dy + o * D * inner + i0;
-    T* dp = dx ? dx + o * D * inner + i0 : nullptr;
-    const float m = on ? mean[pos] : 0.f, r = on ? rstd[pos] : 0.f;
-    float s[2] = {0.f, 0.f};
-    float xh[E], wv[E];
-    if constexpr (EPT > 0) {
+  for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x, turn ^= 1) {
+    const Positions<1> ps(tile, lane, positions, D, inner);
+    const bool on = ps.on;
+    const T *xp = x + ps.at, *gp = dy + ps.at;
+    const float m = on ? mean[ps.pos] : 0.f, r = on ? rstd[ps.pos] : 0.f;
+    float s[2][1] = {{0.f}, {0.f}};
+    float xh[EPT], wv[EPT];
+    Pack<T, 1> xr[EPT], gr[EPT];
 #pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int d = w + kChWaves * k;
-        const bool in = on && d < D;
-        xh[k] = in ? to_f32(xp[d * inner]) : 0.f;
-        wv[k] = in ? to_f32(gp[d * inner]) : 0.f;
-      }
-#pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int d = w + kChWaves * k;
-        const float g = wv[k];
-        xh[k] = (xh[k] - m) * r;
-        ag[k] = fmaf(g, xh[k], ag[k]);
-        ab[k] += g;
-        wv[k] = g * (gamma && d < D ? gamma[d] : 1.f);
-        s[0] += wv[k];
-        s[1] = fmaf(wv[k], xh[k], s[1]);
-      }
-    } else {
-      for (int d = w; d < D; d += kChWaves) {
-        const float g = on ? to_f32(gp[d * inner]) : 0.f;
-        const float h = on ? (to_f32(xp[d * inner]) - m) * r : 0.f;
-        const float wg = g * (gamma ? gamma[d] : 1.f);
-        s[0] += wg;
-        s[1] = fmaf(wg, h, s[1]);
-        if (part) {
-          const float tg = sum64(g * h), tb = sum64(g);
-          if (lane == 0) {
-            pg[d] = first ? tg : pg[d] + tg;
-            pb[d] = first ? tb : pb[d] + tb;
-          }
-        }
-      }
+    for (int k = 0; k < EPT; ++k) {
+      xr[k] = load_channel<T, 1>(xp, w + kChWaves * k, D, inner, on);
+      gr[k] = load_channel<T, 1>(gp, w + kChWaves * k, D, inner, on);
     }
-    if (!dx) continue;
-    wave_sums(s, red[turn], w, lane);
-    const float a = s[0] / (float)D, b = s[1] / (float)D;
-    if (!on) continue;   // no barrier behind this
-    if constexpr (EPT > 0) {
-#pragma unroll
-      for (int k = 0; k < EPT; ++k) {
-        const int d = w + kChWaves * k;
-        if (d < D) dp[d * inner] = from_f32<T>(r * (wv[k] - a - xh[k] * b));
-      }
-    } else {
-#pragma unroll 4
-      for (int d = w; d < D; d += kChWaves) {
-        const float h = (to_f32(xp[d * inner]) - m) * r;
-        const float wg = to_f32(gp[d * inner]) * (gamma ? gamma[d] : 1.f);
-        dp[d * inner] = from_f32<T>(r * (wg - a - h * b));
-      }
-    }
-  }
-  if constexpr (EPT == 0) {
-    if (part && first)   // no positions at all
-      for (int d = threadIdx.x; d < D; d += 64 * kChWaves) pg[d] = pb[d] = 0.f;
-  } else {
-    if (!part) return;
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
       const int d = w + kChWaves * k;
-      const float tg = sum64(ag[k]), tb = sum64(ab[k]);
-      if (lane == 0 && d < D) {
-        pg[d] = tg;
-        pb[d] = tb;
-      }
+      const bool in = on && d < D;
+      const float g = in ? to_f32(gr[k].v[0]) : 0.f;
+      xh[k] = in ? (to_f32(xr[k].v[0]) - m) * r : 0.f;
+      ag[k] = fmaf(g, xh[k], ag[k]);
+      ab[k] += g;
+      wv[k] = g * (gamma && d < D ? gamma[d] : 1.f);
+      s[0][0] += wv[k];
+      s[1][0] = fmaf(wv[k], xh[k], s[1][0]);
+    }
+    if (!dx) continue;
+    wave_sums<2, kChWaves, 1>(s, red[turn], w, lane);
+    const float a = s[0][0] / (float)D, b = s[1][0] / (float)D;
+    if (!on) continue;   // no barrier behind this
+    T* dp = dx + ps.at;
+#pragma unroll
+    for (int k = 0; k < EPT; ++k) {
+      const int d = w + kChWaves * k;
+      if (d < D) dp[(long)d * inner] = from_f32<T>(r * (wv[k] - a - xh[k] * b));
+    }
+  }
+  if (!part) return;
+  float* pg = part + (size_t)blockIdx.x * D;
+  float* pb = part + ((size_t)gridDim.x + blockIdx.x) * D;
+#pragma unroll
+  for (int k = 0; k < EPT; ++k) {
+    const int d = w + kChWaves * k;
+    const float tg = sum64(ag[k]), tb = sum64(ab[k]);
+    if (lane == 0 && d < D) {
+      pg[d] = tg;
+      pb[d] = tb;
     }
   }
 }
@@ -634,7 +783,10 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
 long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 // Vectors a lane holds and waves a row takes: one wave up to 2 vectors a lane, then
-// 4 waves, then 16.
+// 4 waves, then 16.  On either side: one wave with 4 vectors, 16384 x 2048 bf16 backward
+// 54.6 us instead of 40.8 (forward 26.1 and 26.8); 4 waves from 2 vectors on, 65536 x 512
+// fp32 forward 63.3 us instead of 42.9; 16 waves from 16 vectors on, 8192 x 8192 bf16
+// forward 64.5 us instead of 46.3.
 template <typename T, typename F>
 void row_shape(int D, F f) {
   const int vecs = (int)ceil_div(D, 64 * Vec<T>::N);
@@ -656,6 +808,19 @@ void row_shape(int D, F f) {
 #undef S4_CASE
 }
 
+// Two positions a lane for 16-bit elements of an even inner axis, if the blocks still
+// fill the 256 CUs (32 x 512 x 1024 bf16 forward 21.7 us against 26.2, gradients 40.6
+// against 46.1).
+template <typename T, typename F>
+void by_positions(const NormArgs& a, F f) {
+  if constexpr (sizeof(T) == 2)
+    if (a.inner % 2 == 0 && a.outer * a.inner >= 256 * 128)
+      return f(std::integral_constant<int, 2>());
+  f(std::integral_constant<int, 1>());
+}
+
+constexpr unsigned kChBlocks = 1u << 16;   // a launch counts its threads in 32 bits
+
 template <typename T>
 hipError_t fwd(const NormArgs& a, hipStream_t s) {
   const T* x = (const T*)a.x;
@@ -673,15 +838,26 @@ hipError_t fwd(const NormArgs& a, hipStream_t s) {
     });
     return hipGetLastError();
   }
-  const dim3 grid((unsigned)ceil_div(a.outer * a.inner, 64));
-#define S4_GO(ept)                                                                            \
-  norm_channels_kernel<T, ept><<<grid, 64 * kChWaves, 0, s>>>(x, a.gamma, a.beta, y, a.mean,  \
-                                                              a.rstd, a.outer, D, a.inner, a.eps)
-  if (D <= 8 * kChWaves) S4_GO(8);
-  else if (D <= 32 * kChWaves) S4_GO(32);
-  else if (D <= 64 * kChWaves) S4_GO(64);
-  else S4_GO(0);
+  // 16 waves of few channels each for 16-bit elements, 8 for fp32, whose lines fill the
+  // loads (32 x 512 x 1024 with 16 against 8: bf16 21.7 against 24.9 us, fp32 33.7 against
+  // 28.3; 8 x 512 x 256 bf16 10.3 against 16.3).  Above 512 channels they are
+  // read again (16 x 1024 x 1024 bf16 31.2 us against 35.3 in registers; fp32 44.5
+  // against 40.8).
+  const unsigned n = (unsigned)(a.outer * a.inner), inner = (unsigned)a.inner;
+  by_positions<T>(a, [&](auto vp) {
+    constexpr int VP = decltype(vp)::value;
+    const unsigned tiles = (unsigned)ceil_div(n, 64 * VP);
+    const unsigned grid = tiles < kChBlocks ? tiles : kChBlocks;
+#define S4_GO(ept, waves)                                                                   \
+  norm_channels_kernel<T, ept, waves, VP><<<grid, 64 * waves, 0, s>>>(                      \
+      x, a.gamma, a.beta, y, a.mean, a.rstd, n, D, inner, a.eps)
+    constexpr int kWaves = sizeof(T) == 2 ? 16 : 8;
+    if (D <= 64) S4_GO(8, 8);
+    else if (D <= 256) S4_GO(256 / kWaves, kWaves);
+    else if (D <= 512) S4_GO(512 / kWaves, kWaves);
+    else S4_GO(0, 16);
 #undef S4_GO
+  });
   return hipGetLastError();
 }
 
@@ -692,7 +868,7 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
   const int D = (int)a.D;
   const bool sums = a.dgamma || a.dbeta;
   float* part = sums ? a.part : nullptr;
-  const int nb = (int)norm_parts(a.outer, a.D, a.inner);
+  int nb = (int)norm_parts(a.outer, a.D, a.inner);
   if (a.inner == 1) {
     row_shape<T>(D, [&](auto nv, auto wpr, auto whole) {
       constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
@@ -713,13 +889,33 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
       }
     });
   } else {
-#define S4_GO(ept)                                                                   \
-  norm_channels_bwd_kernel<T, ept><<<dim3(nb), 64 * kChWaves, 0, s>>>(               \
-      x, a.gamma, a.mean, a.rstd, dy, dx, part, a.outer, D, a.inner)
-    if (D <= 8 * kChWaves) S4_GO(8);
-    else if (D <= 32 * kChWaves) S4_GO(32);
-    else S4_GO(0);
-#undef S4_GO
+    const unsigned n = (unsigned)(a.outer * a.inner), inner = (unsigned)a.inner;
+    const bool few = D <= 64, fused = sizeof(T) == 4 && D <= kNormChannels;
+    if (few) {
+      norm_channels_bwd_kernel<T, 8><<<dim3(nb), 64 * kChWaves, 0, s>>>(
+          x, a.gamma, a.mean, a.rstd, dy, dx, part, n, D, inner);
+    } else if (fused) {
+      if constexpr (sizeof(T) == 4)
+        norm_channels_bwd_kernel<T, kNormChannels / kChWaves><<<dim3(nb), 64 * kChWaves, 0, s>>>(
+            x, a.gamma, a.mean, a.rstd, dy, dx, part, n, D, inner);
+    } else {
+      if (dx && n > 0)
+        by_positions<T>(a, [&](auto vp) {
+          constexpr int VP = decltype(vp)::value;
+          const unsigned tiles = (unsigned)ceil_div(n, 64 * VP);
+          const unsigned grid = tiles < kChBlocks ? tiles : kChBlocks;
+          norm_channels_dx_kernel<T, 16, VP><<<grid, 1024, 0, s>>>(x, a.gamma, a.mean, a.rstd, dy,
+                                                                   dx, n, D, inner);
+        });
+      nb = nb < 64 ? nb : 64;
+      const dim3 grid((unsigned)ceil_div(D, 4 * kSums), nb);
+      if (part && a.inner % Vec<T>::N == 0)
+        norm_channels_sums_kernel<T, Vec<T>::N><<<grid, 256, 0, s>>>(
+            x, a.mean, a.rstd, dy, part, n, D, inner);
+      else if (part)
+        norm_channels_sums_kernel<T, 1><<<grid, 256, 0, s>>>(x, a.mean, a.rstd, dy, part, n, D,
+                                                             inner);
+    }
   }
   hipError_t e = hipGetLastError();
   if (e != hipSuccess || !sums) return e;

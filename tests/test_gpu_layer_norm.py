@@ -149,6 +149,26 @@ def test_channels(s4, D, outer, inner, dtype):
     check(s4, (outer, D, inner), 1, dtype, seed=D + inner)
 
 
+@pytest.mark.parametrize("D", [5, 70, 256, 300, 515])
+@pytest.mark.parametrize("dtype,inner", [(BF, 1024), (F16, 1026), (BF, 1023), (F32, 1028)])
+def test_channels_of_many_positions(s4, D, dtype, inner):
+    check(s4, (33, D, inner), 1, dtype, seed=D)
+
+
+@pytest.mark.parametrize("D,dtype,affine", [(65, BF, True), (3, F32, False)])
+def test_channels_of_more_tiles_than_blocks(s4, D, dtype, affine):
+    # 84 copies of a batch that the other tests' sizes cover
+    x, gamma, beta, dy = make((100, D, 1000), D, dtype, 5)
+    y, mean, rstd, g = run(s4, x, gamma, beta, dy, 1, affine=affine)
+    Y, M, R, G = run(s4, x.cuda().repeat(84, 1, 1), gamma, beta, dy.cuda().repeat(84, 1, 1), 1,
+                     affine=affine)
+    for one, all_ in ((y, Y), (mean, M), (rstd, R), (g["dx"], G["dx"])):
+        assert bool((all_.unflatten(0, (84, 100)) == one).all())
+    # sums of 8.4e6 terms: within the same part of the sum of magnitudes
+    for n, a in (("dbeta", dy.double().abs().sum((0, 2))),):
+        close(G[n], 84 * dy.double().sum((0, 2)), n, 84 * a)
+
+
 @pytest.mark.parametrize("D", [64, 256, 300])
 def test_channels_of_no_batch(s4, D):
     x, gamma, _, _ = make((0, D, 5), D, F32, 1)
