@@ -7,6 +7,11 @@
 // sequential stage reads them with whole-line loads and no bounds.  The backward
 // pass takes X^T, P^T and Q^T instead of X and P.
 //
+// It is bound by what it reads and writes beside short dependent products (256 chunks of 16
+// value heads and 8 key heads of 128 in bf16: 94 us; of 16 key heads, 128 us in the mean of
+// forward and backward); 256 threads and 53 KB of LDS let three blocks share a CU, so that
+// one writes while another computes.
+//
 // The inverse is exact fp32: each 16 x 16 diagonal block by forward
 // substitution, the blocks below by X_rc = -X_rr sum_m A_rm X_mc with the fp32
 // matrix instruction, one wave per block column.

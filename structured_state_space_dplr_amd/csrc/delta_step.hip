@@ -3,8 +3,9 @@
 //   n = v - a p,  o = scale (a z + (q . k) beta n),  S <- a S + k (beta n)^T,
 // so one pass over the state and one sum across its rows give a token.  A block
 // of 256 threads holds kCols columns of one head's state in registers (8 lanes x
-// 4 columns, 32 groups of rows); for one token the state's read and write bound
-// it.
+// 4 columns, 32 groups of rows), so a head is spread over dv / 32 blocks and a row of 32
+// columns is a whole line; for one token the state's read and write bound it (128
+// sequences of 16 heads of 128 x 128: 52 us, 5.2 TB/s).
 #include "delta_device.h"
 
 namespace s4 {

@@ -12,7 +12,7 @@ constexpr long kNormMaxD = 32768;      // a row of 16 waves, 32 values a lane
 // and no row gains over 5 %); two of 16 waves.
 constexpr long kNormBlocks = 2048;
 
-constexpr long kNormChannels = 256;    // fp32 channels whose sums stay in registers
+constexpr long kNormChannels = 256;    // channels whose sums stay in registers
 
 struct NormArgs {
   const void* x;
@@ -28,14 +28,14 @@ struct NormArgs {
 
 // Blocks of the backward pass, the rows of its partial sums [2][parts][D]: one
 // per tile of work (a row, 4 rows up to 512 values, or 64 positions) up to four a CU, two
-// with 8 waves each, one where a row takes 4 waves of 32 values a lane or 16 waves
-// (twice as many blocks each: 16384 x 2048 bf16 40.4 -> 50.5 us, 8192 x 8192 bf16 81.4 ->
-// 87.5, for the partial sums' traffic).  Above 16384 values the columns' sums have
-// their own kernel, whose blocks take a strip of columns each, and so have those of
-// channels above kNormChannels (16-bit elements: above 64, which use 64 parts of them).
+// with 8 waves each, one where a row takes 4 waves of 32 values a lane, or 16 waves
+// (twice as many each, for the partial sums' traffic: 16384 x 2048 bf16 40.4 -> 50.5 us,
+// 8192 x 8192 bf16 81.4 -> 87.5, channels of 32 x 256 x 1024 fp32 25.9 -> 30.2).  Above 16384
+// values or kNormChannels channels the columns' sums have their own kernel, whose blocks
+// take some columns each.
 inline long norm_parts(long outer, long D, long inner) {
   const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;
-  const long most = inner > 1 ? (D > kNormChannels ? 64 : 512) : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
+  const long most = inner > 1 ? (D > kNormChannels ? 64 : D > 64 ? 256 : 512) : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
   return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 

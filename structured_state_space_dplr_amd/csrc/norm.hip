@@ -11,8 +11,8 @@
 // Both directions are bound by HBM: forward reads x and writes y, backward reads
 // x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 46 us (5.8 TB/s,
 // part of it from the last-level cache), backward of 16384 x 2048 41 us with the columns'
-// sums (4.9 TB/s); fp32 channels 32 x 256 x 1024: 15.7 us (4.3 TB/s) and 34.6 us (2.9
-// TB/s, where each wave's loads are one line a channel).
+// sums (4.9 TB/s); fp32 channels 32 x 256 x 1024: 15.7 us (4.3 TB/s) and 25.9 us (3.9
+// TB/s).
 #include "norm.h"
 
 #include "vec.h"
@@ -467,8 +467,8 @@ __device__ __forceinline__ Pack<T, VP> load_pack(const T* p) {
 }
 // Channel d of D at a lane's positions.  Elements of 16 bits are read without a branch, a
 // missing one from channel 0 (a load into half a register is waited for at a branch: 59
-// us instead of 30 for the gradients of 32 x 256 x 1024 bf16); of 32 bits, under the
-// condition (33.0 us against 35.4 in fp32).  What a missing one holds is not used.
+// us instead of 30 for the gradients of 32 x 256 x 1024 bf16, with 8 waves); of 32 bits,
+// under the condition (33.0 us against 35.4 in fp32).  What a missing one holds is not used.
 template <typename T, int VP>
 __device__ __forceinline__ Pack<T, VP> load_channel(const T* p, int d, int D, unsigned inner,
                                                     bool on) {
@@ -598,12 +598,10 @@ __global__ __launch_bounds__(64 * W) void norm_channels_kernel(
   }
 }
 
-// dx alone, for more channels than the fused kernel holds sums of: 256 in fp32 (32 x 256 x
-// 1024: fused 34.6 us, apart 45.4), 64 of 16 bits, whose loads carry two positions here
-// (32 x 256 x 1024 bf16 24.5 us against 30.6, 8 x 256 x 256 16.2 against 14.7, 128 x 256 x
-// 1024 73.0 against 67.4).  x and dy are read again for dx, from the caches (kept in
-// registers, up to 512 channels: 58.3 us instead of 40.5 with the sums for 32 x 512 x 1024
-// bf16, 77.5 instead of 72.7 in fp32).
+// dx alone, for more channels than the fused kernel holds sums of (32 x 256 x 1024: fused
+// 25.9 us in fp32 and 20.2 in bf16, apart 45.4 and 24.5).  x and dy are read again for dx,
+// from the caches (kept in registers, up to 512 channels: 58.3 us instead of 40.5 with the
+// sums for 32 x 512 x 1024 bf16, 77.5 instead of 72.7 in fp32).
 template <typename T, int W, int VP>
 __global__ __launch_bounds__(64 * W) void norm_channels_dx_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
@@ -713,17 +711,16 @@ __global__ __launch_bounds__(256) void norm_channels_sums_kernel(
   }
 }
 
-// Backward, up to 8 EPT channels: a block walks over tiles of 64 positions; dgamma and
+// Backward, up to W EPT channels: a block walks over tiles of 64 positions; dgamma and
 // dbeta of the thread's channels are summed in registers over the tiles and over the
-// lanes at the end.
-constexpr int kChWaves = 8;
-
-template <typename T, int EPT>
-__global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
+// lanes at the end.  Above 64 channels 16 waves of 16 channels at one block a CU (32 x 256 x
+// 1024 fp32 25.9 us; 8 waves of 32 channels, two blocks a CU launched, took 34.6).
+template <typename T, int EPT, int W>
+__global__ __launch_bounds__(64 * W) void norm_channels_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
     const float* __restrict__ rstd, const T* __restrict__ dy, T* __restrict__ dx,
     float* __restrict__ part, unsigned positions, int D, unsigned inner) {
-  __shared__ float red[2][2][kChWaves][64];
+  __shared__ float red[2][2][W][64];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned tiles = (positions + 63) / 64;
   float ag[EPT], ab[EPT];
@@ -740,12 +737,12 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
     Pack<T, 1> xr[EPT], gr[EPT];
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
-      xr[k] = load_channel<T, 1>(xp, w + kChWaves * k, D, inner, on);
-      gr[k] = load_channel<T, 1>(gp, w + kChWaves * k, D, inner, on);
+      xr[k] = load_channel<T, 1>(xp, w + W * k, D, inner, on);
+      gr[k] = load_channel<T, 1>(gp, w + W * k, D, inner, on);
     }
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
-      const int d = w + kChWaves * k;
+      const int d = w + W * k;
       const bool in = on && d < D;
       const float g = in ? to_f32(gr[k].v[0]) : 0.f;
       xh[k] = in ? (to_f32(xr[k].v[0]) - m) * r : 0.f;
@@ -756,13 +753,13 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
       s[1][0] = fmaf(wv[k], xh[k], s[1][0]);
     }
     if (!dx) continue;
-    wave_sums<2, kChWaves, 1>(s, red[turn], w, lane);
+    wave_sums<2, W, 1>(s, red[turn], w, lane);
     const float a = s[0][0] / (float)D, b = s[1][0] / (float)D;
     if (!on) continue;   // no barrier behind this
     T* dp = dx + ps.at;
 #pragma unroll
     for (int k = 0; k < EPT; ++k) {
-      const int d = w + kChWaves * k;
+      const int d = w + W * k;
       if (d < D) dp[(long)d * inner] = from_f32<T>(r * (wv[k] - a - xh[k] * b));
     }
   }
@@ -771,7 +768,7 @@ __global__ __launch_bounds__(64 * kChWaves) void norm_channels_bwd_kernel(
   float* pb = part + ((size_t)gridDim.x + blockIdx.x) * D;
 #pragma unroll
   for (int k = 0; k < EPT; ++k) {
-    const int d = w + kChWaves * k;
+    const int d = w + W * k;
     const float tg = sum64(ag[k]), tb = sum64(ab[k]);
     if (lane == 0 && d < D) {
       pg[d] = tg;
@@ -868,7 +865,7 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
   const int D = (int)a.D;
   const bool sums = a.dgamma || a.dbeta;
   float* part = sums ? a.part : nullptr;
-  int nb = (int)norm_parts(a.outer, a.D, a.inner);
+  const int nb = (int)norm_parts(a.outer, a.D, a.inner);
   if (a.inner == 1) {
     row_shape<T>(D, [&](auto nv, auto wpr, auto whole) {
       constexpr int NV = decltype(nv)::value, WPR = decltype(wpr)::value;
@@ -890,14 +887,12 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
     });
   } else {
     const unsigned n = (unsigned)(a.outer * a.inner), inner = (unsigned)a.inner;
-    const bool few = D <= 64, fused = sizeof(T) == 4 && D <= kNormChannels;
-    if (few) {
-      norm_channels_bwd_kernel<T, 8><<<dim3(nb), 64 * kChWaves, 0, s>>>(
+    if (D <= 64) {
+      norm_channels_bwd_kernel<T, 8, 8><<<dim3(nb), 512, 0, s>>>(
           x, a.gamma, a.mean, a.rstd, dy, dx, part, n, D, inner);
-    } else if (fused) {
-      if constexpr (sizeof(T) == 4)
-        norm_channels_bwd_kernel<T, kNormChannels / kChWaves><<<dim3(nb), 64 * kChWaves, 0, s>>>(
-            x, a.gamma, a.mean, a.rstd, dy, dx, part, n, D, inner);
+    } else if (D <= kNormChannels) {
+      norm_channels_bwd_kernel<T, kNormChannels / 16, 16><<<dim3(nb), 1024, 0, s>>>(
+          x, a.gamma, a.mean, a.rstd, dy, dx, part, n, D, inner);
     } else {
       if (dx && n > 0)
         by_positions<T>(a, [&](auto vp) {
@@ -907,7 +902,6 @@ hipError_t bwd(const NormArgs& a, hipStream_t s) {
           norm_channels_dx_kernel<T, 16, VP><<<grid, 1024, 0, s>>>(x, a.gamma, a.mean, a.rstd, dy,
                                                                    dx, n, D, inner);
         });
-      nb = nb < 64 ? nb : 64;
       const dim3 grid((unsigned)ceil_div(D, 4 * kSums), nb);
       if (part && a.inner % Vec<T>::N == 0)
         norm_channels_sums_kernel<T, Vec<T>::N><<<grid, 256, 0, s>>>(
