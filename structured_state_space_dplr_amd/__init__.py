@@ -589,6 +589,8 @@ class DeltaPlan:
         self.handle = 0
         self.sequences, self.tokens, self.Hk, self.Hv = sequences, tokens, Hk, Hv
         self.dk, self.dv, self.dtype, self.training = dk, dv, dtype, training
+        if not all(abs(n) < 1 << 31 for n in (sequences, tokens, Hk, Hv, dk, dv)):
+            raise S4DPLRError(2, "delta_plan_create")      # ctypes would wrap them
         h = _p()
         _check(_lib.s4dplr_delta_plan_create(
             ctypes.byref(h), sequences, tokens, Hk, Hv, dk, dv, _DTYPES[dtype],

@@ -182,3 +182,14 @@ def test_header_names_every_entry(lib):
     for n in ("layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes", "delta_plan_create",
               "delta_plan_bytes", "delta_plan_destroy", "delta_fwd", "delta_bwd"):
         assert f"s4dplr_{n}(" in text and hasattr(lib, f"s4dplr_{n}")
+
+
+@pytest.mark.parametrize("at", range(6))
+@pytest.mark.parametrize("size", [1 << 32, (1 << 32) + 1, -(1 << 32) + 1])
+def test_plan_sizes_of_more_than_32_bits(lib, at, size):
+    import structured_state_space_dplr_amd as s4
+    sizes = [1, 64, 1, 1, 16, 16]
+    sizes[at] = size
+    with pytest.raises(s4.S4DPLRError) as e:
+        s4.DeltaPlan(*sizes)
+    assert e.value.status == SHAPE
