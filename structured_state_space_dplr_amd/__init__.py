@@ -26,6 +26,7 @@ their inputs are checked to be finite and the log decays g to be <= 0.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import torch  # loads the HIP runtime that libs4dplr then shares
@@ -546,13 +547,17 @@ def layer_norm_fwd(x, gamma, beta, y, mean=None, rstd=None, eps: float = 1e-5, a
            "layer_norm_fwd")
 
 
+@functools.lru_cache(maxsize=1024)      # a call through ctypes takes longer than this
+def _norm_workspace(outer, D, inner, where):
+    n = ctypes.c_size_t()
+    _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)), where)
+    return n.value
+
+
 def layer_norm_workspace_bytes(x, axis: int = -1) -> int:
     """Bytes of workspace of ``layer_norm_bwd`` for this ``x``."""
     outer, D, inner, _ = _norm_dims(x, axis)
-    n = ctypes.c_size_t()
-    _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)),
-           "layer_norm_workspace_bytes")
-    return n.value
+    return _norm_workspace(outer, D, inner, "layer_norm_workspace_bytes")
 
 
 def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = -1,
@@ -564,15 +569,13 @@ def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = 
     if validation_enabled():
         check_preconditions("layer_norm_bwd", x=x, gamma=gamma, dy=dy)
     f32, full = torch.float32, x.shape
-    n = ctypes.c_size_t()
-    _check(_lib.s4dplr_layer_norm_workspace_bytes(outer, D, inner, ctypes.byref(n)),
-           "layer_norm_bwd")
+    need = _norm_workspace(outer, D, inner, "layer_norm_bwd")
     args = (_tensor(x, "x", x.dtype, full), _tensor(gamma, "gamma", f32, (D,), dev, True),
             _tensor(mean, "mean", f32, stat, dev), _tensor(rstd, "rstd", f32, stat, dev),
             _tensor(dy, "dy", x.dtype, full, dev), _tensor(dx, "dx", x.dtype, full, dev, True),
             _tensor(dgamma, "dgamma", f32, (D,), dev, True),
             _tensor(dbeta, "dbeta", f32, (D,), dev, True), outer, D, inner, _DTYPES[x.dtype],
-            _workspace(ws, "ws", n.value, dev))
+            _workspace(ws, "ws", need, dev))
     _check(_launch(dev, stream, _lib.s4dplr_layer_norm_bwd, args),
            "layer_norm_bwd")
 
