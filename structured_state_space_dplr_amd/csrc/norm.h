@@ -27,15 +27,16 @@ struct NormArgs {
 };
 
 // Blocks of the backward pass, the rows of its partial sums [2][parts][D]: one
-// per tile of work (a row, 4 rows up to 512 values, or 64 positions) up to four a CU, two
-// with 8 waves each, one where a row takes 4 waves of 32 values a lane, or 16 waves
-// (twice as many each, for the partial sums' traffic: 16384 x 2048 bf16 40.4 -> 50.5 us,
-// 8192 x 8192 bf16 81.4 -> 87.5, channels of 32 x 256 x 1024 fp32 25.9 -> 30.2).  Above 16384
-// values or kNormChannels channels the columns' sums have their own kernel, whose blocks
-// take some columns each.
+// per tile of work (a row, 4 rows up to 512 values, or 64 positions) up to two a CU, one for
+// rows above 2048 values and for channels above 64, whose blocks keep more loads on
+// their way.  More blocks cost more traffic of partial sums, fewer leave the memory
+// idle: 16384 x 2048 bf16 50.5 us with eight a CU, 42.0 with four, 42.6 with two, 51.6 with one;
+// 16384 x 4096 95.1 with four, 79.4 with two, 77.4 with one; channels of 32 x 256 x 1024
+// fp32 30.2 with two, 25.9 with one.  Above 16384 values or kNormChannels channels the
+// columns' sums have their own kernel, whose blocks take some columns each.
 inline long norm_parts(long outer, long D, long inner) {
   const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;
-  const long most = inner > 1 ? (D > kNormChannels ? 64 : D > 64 ? 256 : 512) : D > 16384 ? 32 : D > 4096 ? 256 : 1024;
+  const long most = inner > 1 ? (D > kNormChannels ? 64 : D > 64 ? 256 : 512) : D > 16384 ? 32 : D > 2048 ? 256 : 512;
   return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 

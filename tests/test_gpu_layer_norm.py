@@ -5,8 +5,9 @@ Tolerances: an output of b bits is rounded once (eps / 2 of the value).  Before
 that: a mean of D values is a tree of at most 32 serial additions a lane and
 about 10 across lanes, so off by at most 42 * 2^-24 of the mean magnitude; y, dx
 and rstd follow with a few roundings more: 64 * 2^-24 of the largest value in the
-row.  dgamma and dbeta are sums over the rows by at most rows / 512 + 32 serial
-additions, off by the same part of the sum of magnitudes."""
+row.  dgamma and dbeta are sums over the rows by at most a few hundred serial
+additions a lane, whose independent errors add up as the square root of their
+number: off by the same part of the sum of magnitudes."""
 import pytest
 import torch
 
@@ -164,7 +165,8 @@ def test_channels_of_more_tiles_than_blocks(s4, D, dtype, affine):
                      affine=affine)
     for one, all_ in ((y, Y), (mean, M), (rstd, R), (g["dx"], G["dx"])):
         assert bool((all_.unflatten(0, (84, 100)) == one).all())
-    # sums of 8.4e6 terms: within the same part of the sum of magnitudes
+    # 8.4e6 terms, 512 of them (131 250 tiles, 256 blocks) after one another a lane: errors
+    # of 2^-24 each add up to sqrt(512) < 64 of them
     for n, a in (("dbeta", dy.double().abs().sum((0, 2))),):
         close(G[n], 84 * dy.double().sum((0, 2)), n, 84 * a)
 
