@@ -21,7 +21,6 @@ struct s4dplr_delta_plan {
   bool training;
   int dkp;      // dk rounded up to 64, 128 or 256
   int parts;    // bf16 parts an input element is the exact sum of: 1 (bf16), 2 (fp16), 3 (fp32)
-  int outs;     // parts kept of an operand that only reaches an output of the input's type
   long slots;   // chunks of all sequences, at most
   // Workspace, byte offsets.  "frags" are operands in the register order of the
   // 16x16x32 bf16 matrix instruction, [part][row tile][k step] of kFrag bytes.

@@ -2,11 +2,10 @@
 //
 // The matrix products run on the bf16 matrix cores.  An operand enters as a sum
 // of bf16 parts (hi, mid, lo: 8 significant bits each), so a bf16 input is one
-// part, fp16 two, fp32 three; values computed on the way (states, the inverse,
-// corrections) take three parts wherever they reach the carried state or an
-// fp32 output, which keeps those at fp32 accuracy (the dropped cross products are
-// below 2^-24 relative), and two (2^-16) where the only reader is an output of
-// 16 bits.  Three parts of products cost 6 matrix instructions where the fp32
+// part, fp16 two, fp32 three; values computed on the way (states, the inverse, the
+// pairs' products, corrections) take three, which keeps fp32 accuracy (the dropped cross
+// products are below 2^-24 relative).  Backward, the pairs' products of 16-bit tensors
+// take two.  Three parts of products cost 6 matrix instructions where the fp32
 // instruction would take 16 times the bf16 one's time.
 #pragma once
 

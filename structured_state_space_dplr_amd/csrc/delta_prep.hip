@@ -25,6 +25,7 @@ constexpr int kLd = 68;   // floats from row to row of a 64 x 64 matrix in LDS
 
 }  // namespace
 
+// OUTS: parts of P backward.
 template <typename T, int PARTS, int OUTS, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan p,
                                                          const DeltaArgs a) {
@@ -246,7 +247,7 @@ hipError_t prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStr
   if (bwd)                                                                             \
     delta_prep_kernel<T, PARTS, OUTS, dkp, true><<<grid, 256, 0, s>>>(*p, a);          \
   else                                                                                 \
-    delta_prep_kernel<T, PARTS, OUTS, dkp, false><<<grid, 256, 0, s>>>(*p, a)
+    delta_prep_kernel<T, PARTS, 3, dkp, false><<<grid, 256, 0, s>>>(*p, a)
   if (p->dkp == 64) { S4_GO(64); }
   else if (p->dkp == 128) { S4_GO(128); }
   else { S4_GO(256); }

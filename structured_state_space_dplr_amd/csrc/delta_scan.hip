@@ -251,7 +251,7 @@ struct Ahead {
 
 }  // namespace
 
-template <typename T, int PARTS, int OUTS, int DKP, bool SAVE, int DS>
+template <typename T, int PARTS, int DKP, bool SAVE, int DS>
 __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan p,
                                                          const DeltaArgs a) {
   using O = Own<DKP>;
@@ -261,7 +261,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
   __shared__ __attribute__((aligned(16))) float ns[SAVE ? DS : 1][kLdF];  // N
   __shared__ __attribute__((aligned(16))) __bf16 st[3][DS][DKP + 8];      // S
   __shared__ __attribute__((aligned(16))) __bf16 rt[3][DS][kLdT];         // R
-  __shared__ __attribute__((aligned(16))) __bf16 ut[OUTS][DS][kLdT];      // U
+  __shared__ __attribute__((aligned(16))) __bf16 ut[3][DS][kLdT];      // U
   __shared__ __attribute__((aligned(16))) __bf16 du[3][DS][kLdT];         // d . U
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   Place at;
@@ -412,7 +412,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
         N += n1;
         const v4f U = bv * N;
         put4<3>(du, dv * U, 16 * u + lr, i0);
-        put4<OUTS>(ut, U, 16 * u + lr, i0);
+        put4<3>(ut, U, 16 * u + lr, i0);
         if constexpr (SAVE) *reinterpret_cast<v4f*>(&ns[16 * u + lr][i0]) = N;
       }
       load_x();
@@ -444,10 +444,10 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
   } else if (wave < 6) {
     // row tiles j and 3 - j of O: one of them reaches over both k steps of P
     const int j = wave - 4;
-    v8bf p0[OUTS], p1[2][OUTS], qa[2][KS][PARTS];
+    v8bf p0[3], p1[2][3], qa[2][KS][PARTS];
     v4f ev[2];
     const unsigned char* qp = a.ws + p.off_q + k0;
-    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag);
+    const unsigned char* pp = a.ws + p.off_p + v0 * (3 * 8 * kFrag);
     auto load_q = [&] {
 #pragma unroll
       for (int q = 0; q < PARTS; ++q)
@@ -461,7 +461,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
     };
     auto load_p = [&] {
 #pragma unroll
-      for (int q = 0; q < OUTS; ++q) {
+      for (int q = 0; q < 3; ++q) {
         p0[q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8, off);
         p1[0][q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8, off);
         p1[1][q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8 + 1, off);
@@ -474,7 +474,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
     for (int c = 0; c < nc; ++c) {
       if (c + 1 < nc) {
         qp += kstep;
-        pp += (size_t)p.Hv * (OUTS * 8 * kFrag);
+        pp += (size_t)p.Hv * (3 * 8 * kFrag);
         dp += p.Hv;
       }
       __syncthreads();
@@ -499,12 +499,12 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       __syncthreads();
 #pragma unroll
       for (int u = 0; u < NT; ++u) {
-        v8bf ub[2][OUTS];
-        get8<OUTS>(ut, ub[0], 16 * u + lr, lg * 8);
-        get8<OUTS>(ut, ub[1], 16 * u + lr, 32 + lg * 8);
-        o[u][0] = mfma_parts<OUTS>(p0, ub[0], o[u][0]);
-        o[u][1] = mfma_parts<OUTS>(p1[0], ub[0], o[u][1]);
-        o[u][1] = mfma_parts<OUTS>(p1[1], ub[1], o[u][1]);
+        v8bf ub[2][3];
+        get8<3>(ut, ub[0], 16 * u + lr, lg * 8);
+        get8<3>(ut, ub[1], 16 * u + lr, 32 + lg * 8);
+        o[u][0] = mfma_parts<3>(p0, ub[0], o[u][0]);
+        o[u][1] = mfma_parts<3>(p1[0], ub[0], o[u][1]);
+        o[u][1] = mfma_parts<3>(p1[1], ub[1], o[u][1]);
         *reinterpret_cast<v4f*>(&os[16 * u + lr][16 * j + 4 * lg]) = o[u][0];
         *reinterpret_cast<v4f*>(&os[16 * u + lr][16 * (3 - j) + 4 * lg]) = o[u][1];
       }
@@ -520,7 +520,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       np = reinterpret_cast<float*>(a.saved + p.off_n) + (v0 * p.dv + at.col0) * kChunk;
       sp = reinterpret_cast<float*>(a.saved + p.off_s) + (v0 * p.dv + at.col0) * p.dk;
     }
-    using A = Ahead<PARTS, OUTS, DKP, false>;
+    using A = Ahead<PARTS, 3, DKP, false>;
     A ahead;
     ahead.set(p, a, at, j * 64 + lane);
     const int whole = (int)(at.r.len / kChunk);
@@ -900,8 +900,8 @@ void go(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s)
   const unsigned heads = (unsigned)(p->sequences * p->Hv);
   const unsigned grid = (heads + 7) / 8 * 8 * ((p->dv + DS - 1) / DS);
   if (bwd) delta_scan_bwd_kernel<T, PARTS, OUTS, DKP, DS><<<grid, 512, 0, s>>>(*p, a);
-  else if (a.saved) delta_scan_kernel<T, PARTS, OUTS, DKP, true, DS><<<grid, 512, 0, s>>>(*p, a);
-  else delta_scan_kernel<T, PARTS, OUTS, DKP, false, DS><<<grid, 512, 0, s>>>(*p, a);
+  else if (a.saved) delta_scan_kernel<T, PARTS, DKP, true, DS><<<grid, 512, 0, s>>>(*p, a);
+  else delta_scan_kernel<T, PARTS, DKP, false, DS><<<grid, 512, 0, s>>>(*p, a);
 }
 
 // bf16 at 64 < dk <= 128: while blocks of 16 columns are no more than the 256 CUs, more

@@ -159,7 +159,6 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
   p->training = (flags & S4DPLR_DELTA_TRAINING) != 0;
   p->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
   p->parts = dtype == S4DPLR_BF16 ? 1 : dtype == S4DPLR_F16 ? 2 : 3;
-  p->outs = dtype == S4DPLR_F32 ? 3 : 2;
   p->slots = tokens / s4::kChunk + sequences;
   const size_t ks = (size_t)p->slots * Hk, vs = (size_t)p->slots * Hv;
   const size_t kb = (size_t)p->parts * (p->dkp / 8) * s4::kFrag;   // 64 x dkp, all parts
@@ -173,7 +172,7 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
   p->off_q = take(ks * kb);
   p->off_kt = take(ks * kb);
   p->off_x = take(vs * 3 * 8 * s4::kFrag);
-  p->off_p = take(vs * p->outs * 8 * s4::kFrag);
+  p->off_p = take(vs * 3 * 8 * s4::kFrag);
   p->off_vec = take(vs * sizeof(s4::DeltaVec));
   if (p->training) {
     p->off_qt = take(ks * kb);
