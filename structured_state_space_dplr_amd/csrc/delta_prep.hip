@@ -25,8 +25,7 @@ constexpr int kLd = 68;   // floats from row to row of a 64 x 64 matrix in LDS
 
 }  // namespace
 
-// OUTS: parts of P backward.
-template <typename T, int PARTS, int OUTS, int DKP, bool BWD>
+template <typename T, int PARTS, int DKP, bool BWD>
 __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan p,
                                                          const DeltaArgs a) {
   constexpr int KS = DKP / 32;
@@ -185,10 +184,10 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   }
   __syncthreads();
 
-  // operands of X (three parts) and P, or of their transposes
+  // operands of X and P (three parts), or of their transposes
   {
     unsigned char* xo = a.ws + p.off_x + vslot * (3 * 8 * kFrag);
-    unsigned char* po = a.ws + p.off_p + vslot * (OUTS * 8 * kFrag);
+    unsigned char* po = a.ws + p.off_p + vslot * (3 * 8 * kFrag);
 #pragma unroll
     for (int ks = 0; ks < 2; ++ks) {
       if (BWD ? ks < w / 2 : ks > w / 2) continue;   // zero, and never read
@@ -199,15 +198,15 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
         x[i] = BWD ? am[k0 + i][row] : am[row][k0 + i];
         y[i] = BWD ? pm[k0 + i][row] : pm[row][k0 + i];
       }
-      v8bf xs[3], ps[OUTS];
+      v8bf xs[3], ps[3];
       split8<3>(x, xs);
-      split8<OUTS>(y, ps);
+      split8<3>(y, ps);
 #pragma unroll
-      for (int i = 0; i < 3; ++i)
-        *reinterpret_cast<v8bf*>(xo + (size_t)((i * 4 + w) * 2 + ks) * kFrag + lane * 16) = xs[i];
-#pragma unroll
-      for (int i = 0; i < OUTS; ++i)
-        *reinterpret_cast<v8bf*>(po + (size_t)((i * 4 + w) * 2 + ks) * kFrag + lane * 16) = ps[i];
+      for (int i = 0; i < 3; ++i) {
+        const size_t f = (size_t)((i * 4 + w) * 2 + ks) * kFrag + lane * 16;
+        *reinterpret_cast<v8bf*>(xo + f) = xs[i];
+        *reinterpret_cast<v8bf*>(po + f) = ps[i];
+      }
     }
   }
   // K^T (then, through the same memory, Q^T).  Row 4 g + e of tile t of a k step of dk is
@@ -240,14 +239,14 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
 
 namespace {
 
-template <typename T, int PARTS, int OUTS>
+template <typename T, int PARTS>
 hipError_t prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
   const dim3 grid((unsigned)p->slots, (unsigned)p->Hv);
 #define S4_GO(dkp)                                                                     \
   if (bwd)                                                                             \
-    delta_prep_kernel<T, PARTS, OUTS, dkp, true><<<grid, 256, 0, s>>>(*p, a);          \
+    delta_prep_kernel<T, PARTS, dkp, true><<<grid, 256, 0, s>>>(*p, a);                \
   else                                                                                 \
-    delta_prep_kernel<T, PARTS, 3, dkp, false><<<grid, 256, 0, s>>>(*p, a)
+    delta_prep_kernel<T, PARTS, dkp, false><<<grid, 256, 0, s>>>(*p, a)
   if (p->dkp == 64) { S4_GO(64); }
   else if (p->dkp == 128) { S4_GO(128); }
   else { S4_GO(256); }
@@ -259,9 +258,9 @@ hipError_t prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStr
 
 hipError_t launch_delta_prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd,
                              hipStream_t s) {
-  if (p->dtype == S4DPLR_F32) return prep<float, 3, 3>(p, a, bwd, s);
-  if (p->dtype == S4DPLR_BF16) return prep<bf16, 1, 2>(p, a, bwd, s);
-  return prep<f16, 2, 2>(p, a, bwd, s);
+  if (p->dtype == S4DPLR_F32) return prep<float, 3>(p, a, bwd, s);
+  if (p->dtype == S4DPLR_BF16) return prep<bf16, 1>(p, a, bwd, s);
+  return prep<f16, 2>(p, a, bwd, s);
 }
 
 }  // namespace s4

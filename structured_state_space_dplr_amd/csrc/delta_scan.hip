@@ -181,16 +181,16 @@ __device__ __forceinline__ void store_rows(T* to, unsigned ld, const float (&m)[
 // Lines of a chunk's operands to bring into the L2: K, then Q (forward) or Q^T
 // (backward), K^T, X, P, shared among the slices of a head; and the slice's own rows
 // of V or dO with the decays.  Chunks are counted from the sequence's first.
-template <int PARTS, int OUTS, int DKP, bool BWD>
+template <int PARTS, int DKP, bool BWD>
 struct Ahead {
   static constexpr int kTouch = 5;            // lines a lane and chunk, at most
   static constexpr int kSets = 4;             // chunks in flight
   static constexpr int KL = PARTS * DKP;      // lines of a 64 x DKP operand (128 bytes each)
-  static constexpr int XL = 3 * 8 * kFrag / 128, PL = OUTS * 8 * kFrag / 128;
-  static constexpr int kLines = 3 * KL + XL + PL;
+  static constexpr int XL = 3 * 8 * kFrag / 128;   // lines of X, and of P
+  static constexpr int kLines = 3 * KL + 2 * XL;
   const unsigned char *k, *q, *t, *x, *p, *v, *d;
   long ldv;                                   // bytes from row to row of V or dO
-  size_t kstep, xstep, pstep, dstep;
+  size_t kstep, xstep, dstep;
   int id, first, step;                        // this lane's lines: first + i step
   static constexpr int kSize = PARTS == 3 ? 4 : 2;   // bytes of an element
 
@@ -203,7 +203,7 @@ struct Ahead {
     q = a.ws + (BWD ? pl.off_qt : pl.off_q) + f;
     t = a.ws + pl.off_kt + f;
     x = a.ws + pl.off_x + g * (XL * 128);
-    p = a.ws + pl.off_p + g * (PL * 128);
+    p = a.ws + pl.off_p + g * (XL * 128);
     v = (const unsigned char*)(BWD ? a.dout : a.v);
     ldv = (BWD ? (long)pl.Hv * pl.dv : a.ldv) * kSize;
     v += at.r.start * ldv + ((size_t)at.h * pl.dv + at.col0) * kSize;
@@ -212,7 +212,6 @@ struct Ahead {
     id = lane;
     kstep = (size_t)pl.Hk * kbytes;
     xstep = (size_t)pl.Hv * (XL * 128);
-    pstep = (size_t)pl.Hv * (PL * 128);
     first = at.slice * 128 + lane;
     step = at.slices * 128;
   }
@@ -233,7 +232,7 @@ struct Ahead {
       } else if ((l -= KL) < XL) {
         from = x + c * (long)xstep + l * 128;
       } else {
-        from = p + c * (long)pstep + (l - XL) * 128;
+        from = p + c * (long)xstep + (l - XL) * 128;
       }
       h[i] = *(const GLOBAL unsigned char*)from;
     }
@@ -520,7 +519,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
       np = reinterpret_cast<float*>(a.saved + p.off_n) + (v0 * p.dv + at.col0) * kChunk;
       sp = reinterpret_cast<float*>(a.saved + p.off_s) + (v0 * p.dv + at.col0) * p.dk;
     }
-    using A = Ahead<PARTS, 3, DKP, false>;
+    using A = Ahead<PARTS, DKP, false>;
     A ahead;
     ahead.set(p, a, at, j * 64 + lane);
     const int whole = (int)(at.r.len / kChunk);
@@ -567,7 +566,7 @@ __global__ __launch_bounds__(512) void delta_scan_kernel(const s4dplr_delta_plan
 // Waves 0 - 3 walk this chain, 4 and 5 prepare the products with dO a chunk ahead, 6
 // and 7 store dV (the gradient of v, and fp32 [dv][64] for stage 3) and Z before its
 // update ([dv][dk], for stage 3).
-template <typename T, int PARTS, int OUTS, int DKP, int DS>
+template <typename T, int PARTS, int DKP, int DS>
 __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_plan p,
                                                              const DeltaArgs a) {
   using O = Own<DKP>;
@@ -738,11 +737,11 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
     // row tiles j and 3 - j: one of them reaches over both k steps of P^T
     const int j = wave - 4, ra = 16 * j + 4 * lg, rb = 16 * (3 - j) + 4 * lg;
     constexpr int QT = DKP / 32;   // tiles of Q^T a wave
-    v8bf p0[2][OUTS], p1[OUTS], qa[QT][2][PARTS];
+    v8bf p0[2][3], p1[3], qa[QT][2][PARTS];
     v4f ev[2];
     T go[NT][2][4];
     const unsigned char* qp = a.ws + p.off_qt + k0 + (size_t)j * QT * 2 * kFrag;
-    const unsigned char* pp = a.ws + p.off_p + v0 * (OUTS * 8 * kFrag);
+    const unsigned char* pp = a.ws + p.off_p + v0 * (3 * 8 * kFrag);
     const T* gp = (const T*)a.dout + row1 * ldo + (size_t)at.h * p.dv;
     unsigned ooff[2][4], ocol[NT];
 #pragma unroll
@@ -775,7 +774,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
           }
       }
 #pragma unroll
-      for (int q = 0; q < OUTS; ++q) {
+      for (int q = 0; q < 3; ++q) {
         p0[0][q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8, off);
         p0[1][q] = load_frag(pp + (size_t)j * 2 * kFrag, q * 8 + 1, off);
         p1[q] = load_frag(pp + (size_t)(3 - j) * 2 * kFrag, q * 8 + 1, off);
@@ -832,7 +831,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
     };
     auto back = [&](int c) {   // chunk c's operands are used up: the next
       if (c > 0) {
-        pp -= (size_t)p.Hv * (OUTS * 8 * kFrag);
+        pp -= (size_t)p.Hv * (3 * 8 * kFrag);
         qp -= kstep;
         gp -= (size_t)kChunk * ldo;
         dp -= p.Hv;
@@ -858,7 +857,7 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
     T* op = a.dv ? (T*)a.dv + row1 * ldo + (size_t)at.h * p.dv + at.col0 : nullptr;
     float* fp = reinterpret_cast<float*>(a.ws + p.off_dv) + (v0 * p.dv + at.col0) * kChunk;
     float* zp = reinterpret_cast<float*>(a.ws + p.off_ds) + (v0 * p.dv + at.col0) * p.dk;
-    using A = Ahead<PARTS, OUTS, DKP, true>;
+    using A = Ahead<PARTS, DKP, true>;
     A ahead;
     ahead.set(p, a, at, j * 64 + lane);
     auto touch = [&](int c, unsigned (&h)[A::kTouch]) {
@@ -895,11 +894,11 @@ __global__ __launch_bounds__(512) void delta_scan_bwd_kernel(const s4dplr_delta_
 
 namespace {
 
-template <typename T, int PARTS, int OUTS, int DKP, int DS>
+template <typename T, int PARTS, int DKP, int DS>
 void go(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
   const unsigned heads = (unsigned)(p->sequences * p->Hv);
   const unsigned grid = (heads + 7) / 8 * 8 * ((p->dv + DS - 1) / DS);
-  if (bwd) delta_scan_bwd_kernel<T, PARTS, OUTS, DKP, DS><<<grid, 512, 0, s>>>(*p, a);
+  if (bwd) delta_scan_bwd_kernel<T, PARTS, DKP, DS><<<grid, 512, 0, s>>>(*p, a);
   else if (a.saved) delta_scan_kernel<T, PARTS, DKP, true, DS><<<grid, 512, 0, s>>>(*p, a);
   else delta_scan_kernel<T, PARTS, DKP, false, DS><<<grid, 512, 0, s>>>(*p, a);
 }
@@ -911,25 +910,25 @@ void go(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s)
 // dk <= 64 two blocks of 16 columns share a CU and are the faster ones (5003 tokens in
 // 13 sequences, 8 heads of 64 x 128: 42 us, 48 with 32).  Operands of two and three
 // parts, and dk > 128, leave no room for 32 columns.
-template <typename T, int PARTS, int OUTS>
+template <typename T, int PARTS>
 hipError_t scan(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
   const long blocks = (long)p->sequences * p->Hv * ((p->dv + 15) / 16);
   if constexpr (PARTS == 1) {
     if (p->dkp == 128 && p->dv > 16 && blocks > 256) {
-      go<T, PARTS, OUTS, 128, 32>(p, a, bwd, s);
+      go<T, PARTS, 128, 32>(p, a, bwd, s);
       return hipGetLastError();
     }
   }
-  if (p->dkp == 64) go<T, PARTS, OUTS, 64, 16>(p, a, bwd, s);
-  else if (p->dkp == 128) go<T, PARTS, OUTS, 128, 16>(p, a, bwd, s);
-  else go<T, PARTS, OUTS, 256, 16>(p, a, bwd, s);
+  if (p->dkp == 64) go<T, PARTS, 64, 16>(p, a, bwd, s);
+  else if (p->dkp == 128) go<T, PARTS, 128, 16>(p, a, bwd, s);
+  else go<T, PARTS, 256, 16>(p, a, bwd, s);
   return hipGetLastError();
 }
 
 hipError_t scan_any(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
-  if (p->dtype == S4DPLR_F32) return scan<float, 3, 3>(p, a, bwd, s);
-  if (p->dtype == S4DPLR_BF16) return scan<bf16, 1, 2>(p, a, bwd, s);
-  return scan<f16, 2, 2>(p, a, bwd, s);
+  if (p->dtype == S4DPLR_F32) return scan<float, 3>(p, a, bwd, s);
+  if (p->dtype == S4DPLR_BF16) return scan<bf16, 1>(p, a, bwd, s);
+  return scan<f16, 2>(p, a, bwd, s);
 }
 
 }  // namespace
