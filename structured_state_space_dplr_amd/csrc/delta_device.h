@@ -4,8 +4,8 @@
 // of bf16 parts (hi, mid, lo: 8 significant bits each), so a bf16 input is one
 // part, fp16 two, fp32 three; values computed on the way (states, the inverse, the
 // pairs' products, corrections) take three, which keeps fp32 accuracy (the dropped cross
-// products are below 2^-24 relative).  The pairs' products that only reach the gradients
-// of 16-bit q and k take two.  Three parts of products cost 6 matrix instructions where the fp32
+// products are below 2^-24 relative), so 16-bit outputs are those of fp32 tensors of the same
+// values, rounded once.  Three parts of products cost 6 matrix instructions where the fp32
 // instruction would take 16 times the bf16 one's time.
 #pragma once
 

@@ -100,7 +100,7 @@ constexpr bool three_blocks(int parts, int dkp, bool grouped) {
   return parts == 1 && dkp <= 128 && !grouped;
 }
 
-template <typename T, int PARTS, int OUTS, int DKP, bool GROUPED>
+template <typename T, int PARTS, int DKP, bool GROUPED>
 __global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) void delta_grads_kernel(const s4dplr_delta_plan p,
                                                              const DeltaArgs a) {
   constexpr int CT = kCols / 16, KS = DKP / 32;
@@ -353,16 +353,16 @@ __global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) voi
       if constexpr (!kAhead) load_kq(ks);
       const int j0 = ks * 32 + lg * 8;
       float x[8];
-      v8bf ya[OUTS], yt[OUTS], ba[OUTS];
+      v8bf ya[3], yt[3], ba[3];
 #pragma unroll
       for (int q = 0; q < 8; ++q) x[q] = mem.pr.ym[row][j0 + q];
-      split8<OUTS>(x, ya);
+      split8<3>(x, ya);
 #pragma unroll
       for (int q = 0; q < 8; ++q) x[q] = mem.pr.ym[j0 + q][row];
-      split8<OUTS>(x, yt);
+      split8<3>(x, yt);
 #pragma unroll
       for (int q = 0; q < 8; ++q) x[q] = -(mem.pr.bm[row][j0 + q] + mem.pr.bm[j0 + q][row]);
-      split8<OUTS>(x, ba);
+      split8<3>(x, ba);
 #pragma unroll
       for (int i = 0; i < CT; ++i) {
         dq[i] = mfma_parts<3>(kc[ks][i], ya, dq[i]);
@@ -429,13 +429,13 @@ __global__ __launch_bounds__(256) void delta_gates_kernel(const s4dplr_delta_pla
 
 namespace {
 
-template <typename T, int PARTS, int OUTS>
+template <typename T, int PARTS>
 hipError_t grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) {
   const int nb = (p->dk + kCols - 1) / kCols;
   const dim3 grid((unsigned)((p->slots + 7) / 8 * 8 * nb), (unsigned)p->Hk);
-#define S4_GO(dkp)                                                                           \
-  (p->Hv > p->Hk ? delta_grads_kernel<T, PARTS, OUTS, dkp, true><<<grid, 256, 0, s>>>(*p, a) \
-                 : delta_grads_kernel<T, PARTS, OUTS, dkp, false><<<grid, 256, 0, s>>>(*p, a))
+#define S4_GO(dkp)                                                                     \
+  (p->Hv > p->Hk ? delta_grads_kernel<T, PARTS, dkp, true><<<grid, 256, 0, s>>>(*p, a) \
+                 : delta_grads_kernel<T, PARTS, dkp, false><<<grid, 256, 0, s>>>(*p, a))
   if (p->dkp == 64) S4_GO(64);
   else if (p->dkp == 128) S4_GO(128);
   else S4_GO(256);
@@ -450,9 +450,9 @@ hipError_t grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) 
 }  // namespace
 
 hipError_t launch_delta_grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) {
-  if (p->dtype == S4DPLR_F32) return grads<float, 3, 3>(p, a, s);
-  if (p->dtype == S4DPLR_BF16) return grads<bf16, 1, 2>(p, a, s);
-  return grads<f16, 2, 2>(p, a, s);
+  if (p->dtype == S4DPLR_F32) return grads<float, 3>(p, a, s);
+  if (p->dtype == S4DPLR_BF16) return grads<bf16, 1>(p, a, s);
+  return grads<f16, 2>(p, a, s);
 }
 
 }  // namespace s4

@@ -11,7 +11,7 @@ that nearly cancel show what an operand of too few bits loses."""
 import pytest
 import torch
 
-from test_gpu_delta import backward, check_forward, close, forward, inputs, reference, reference_grads
+from test_gpu_delta import backward, check_backward, check_forward, forward, inputs, reference
 
 pytestmark = pytest.mark.gpu
 
@@ -66,7 +66,8 @@ def test_16_bit_tensors_give_the_fp32_gradients(s4, dtype, S, T, Hk, Hv, dk, dv)
     got, want = backward(s4, x, S)[2], backward(s4, widened(x), S)[2]
     for n in ("state", "g", "beta"):
         assert torch.equal(got[n], want[n]), "d" + n
-    assert torch.equal(got["v"], want["v"].to(dtype)), "dv"
+    for n in ("q", "k", "v"):
+        assert torch.equal(got[n], want[n].to(dtype)), "d" + n
 
 
 @pytest.mark.parametrize("dtype", [BF, F16, F32])
@@ -74,9 +75,7 @@ def test_16_bit_tensors_give_the_fp32_gradients(s4, dtype, S, T, Hk, Hv, dk, dv)
 def test_related_keys_and_queries(s4, dtype, share):
     x = related(1, 200, 1, 1, 2, 32, 24, dtype, share)
     check_forward(s4, x, 1)
-    got, want = backward(s4, x, 1)[2], reference_grads(x, 1, None)
-    for n in ("state", "v", "g", "beta"):
-        close(got[n], want[n], "d" + n, 4.0 if n in ("g", "beta") else 1.0)
+    check_backward(s4, x, 1)
 
 
 @pytest.mark.parametrize("dtype", [BF, F16])
