@@ -76,6 +76,21 @@ inline int step_limit(const s4dplr_delta_plan* p) {
   return (long)p->sequences * p->Hv * ((p->dv + 15) / 16) > 256 ? 16 : 8;
 }
 
+// Where a sequence lies in the packed rows, and its chunks in the slots.  Chunks
+// of sequence s are slots first(s) = floor(start / 64) + s and on: disjoint for
+// any lengths, since ceil((b - a) / 64) <= floor(b / 64) - floor(a / 64) + 1.
+struct Rows {
+  long start, len;
+  constexpr long first(int s) const { return start / kChunk + s; }
+  constexpr int chunks() const { return (int)((len + kChunk - 1) / kChunk); }
+};
+// The sequence from row a to row b of n.  Offsets outside [0, n] and falling ones, whatever
+// their values, are clamped before they are subtracted: no access leaves the buffers.
+constexpr Rows clamp_rows(int n, int a, int b) {
+  const int start = a < 0 ? 0 : a > n ? n : a, end = b < start ? start : b > n ? n : b;
+  return Rows{start, end - start};
+}
+
 hipError_t launch_delta_steps(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);
 hipError_t launch_delta_prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd,
                              hipStream_t s);

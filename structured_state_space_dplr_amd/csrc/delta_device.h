@@ -150,28 +150,9 @@ __device__ __forceinline__ float exp_diff(double x) {
   return ldexpf(__builtin_amdgcn_exp2f((float)(x - n)), (int)n);
 }
 
-// Where a sequence lies in the packed rows, and its chunks in the slots.  Chunks
-// of sequence s are slots first(s) = floor(start / 64) + s and on: disjoint for
-// any lengths, since ceil((b - a) / 64) <= floor(b / 64) - floor(a / 64) + 1.
-// Offsets outside [0, tokens] or falling ones are clamped, so no access leaves
-// the buffers.
-struct Rows {
-  long start, len;
-  __device__ __forceinline__ long first(int s) const { return start / kChunk + s; }
-  __device__ __forceinline__ int chunks() const { return (int)((len + kChunk - 1) / kChunk); }
-};
 __device__ __forceinline__ Rows rows_of(const s4dplr_delta_plan& p, const int* offsets, int s) {
-  Rows r;
-  if (!offsets) {
-    r.len = p.each;
-    r.start = (long)p.each * s;
-    return r;
-  }
-  const int n = (int)p.tokens, a = offsets[s], b = offsets[s + 1];
-  const int start = a < 0 ? 0 : a > n ? n : a, len = (b > n ? n : b) - start;
-  r.start = start;
-  r.len = len < 0 ? 0 : len;
-  return r;
+  if (!offsets) return Rows{(long)p.each * s, p.each};
+  return clamp_rows((int)p.tokens, offsets[s], offsets[s + 1]);
 }
 
 // Block -> (sequence and head, slice of the dv columns).  Blocks go round robin
