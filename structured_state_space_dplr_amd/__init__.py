@@ -21,7 +21,8 @@ The token-major operators (``layer_norm_fwd`` / ``layer_norm_bwd`` and, on a
 ``DeltaPlan``, ``delta_fwd`` / ``delta_bwd``) take float32, bfloat16 or float16
 tensors of any size and alignment, launch on the device of their tensors, and
 ``stream=None`` is that device's current stream.  With ``S4DPLR_VALIDATE=1``
-their inputs are checked to be finite and the log decays g to be <= 0.
+their inputs are checked to be finite, the log decays g to be <= 0 and offsets
+to rise within the rows; rows outside every sequence may hold anything.
 """
 from __future__ import annotations
 
@@ -567,7 +568,7 @@ def layer_norm_bwd(x, gamma, mean, rstd, dy, dx, dgamma, dbeta, ws, axis: int = 
     outer, D, inner, stat = _norm_dims(x, axis)
     dev = x.device
     if validation_enabled():
-        check_preconditions("layer_norm_bwd", x=x, gamma=gamma, dy=dy)
+        check_preconditions("layer_norm_bwd", x=x, gamma=gamma, mean=mean, rstd=rstd, dy=dy)
     f32, full = torch.float32, x.shape
     need = _norm_workspace(outer, D, inner, "layer_norm_bwd")
     args = (_tensor(x, "x", x.dtype, full), _tensor(gamma, "gamma", f32, (D,), dev, True),
@@ -634,7 +635,33 @@ class DeltaPlan:
             pass
 
 
-def _delta_inputs(where, plan, q, k, v, g, beta, ws, scale, offsets):
+def _validate_delta(where, plan, offsets, rows, states):
+    """The preconditions of ``delta_fwd`` and ``delta_bwd``: offsets that rise within the rows,
+    finite values and g <= 0 in the sequences' rows (the others are not read)."""
+    lo, hi = 0, plan.tokens
+    if offsets is not None:
+        at = [int(i) for i in _host(offsets).flatten()]
+        for i, (a, b) in enumerate(zip([0, *at], [*at, plan.tokens])):
+            if a > b:
+                what = f"offsets[{i}] = {b} < {a}" if i < len(at) else f"offsets end at {a} > {b} rows"
+                raise S4DPLRPreconditionError(where, what)
+        lo, hi = at[0], at[-1]
+    for name, t in {**rows, **states}.items():
+        if t is None:
+            continue
+        h = _host(t)
+        bad = ~(h <= 0) if name == "g" else ~torch.isfinite(h)      # g = -infinity is a reset
+        if name in rows and h.dim() > 0:
+            bad[:lo] = False
+            bad[hi:] = False
+        if bool(bad.any()):
+            idx = tuple(int(i) for i in bad.nonzero()[0])
+            raise S4DPLRPreconditionError(where, f"g must be <= 0, not so at index {idx}" if name == "g"
+                                          else f"{name} is not finite at index {idx}")
+
+
+def _delta_inputs(where, plan, q, k, v, g, beta, ws, scale, offsets, state=None, dout=None,
+                  dstate_out=None):
     if not isinstance(plan, DeltaPlan):
         raise TypeError("pass a DeltaPlan")
     if not plan.handle:
@@ -642,11 +669,8 @@ def _delta_inputs(where, plan, q, k, v, g, beta, ws, scale, offsets):
     if not isinstance(v, torch.Tensor):
         raise TypeError("v: expected a torch.Tensor")
     if validation_enabled():
-        check_preconditions(where, q=q, k=k, v=v, beta=beta)
-        bad = ~(_host(g) <= 0)          # -infinity is a reset
-        if bool(bad.any()):
-            idx = tuple(int(i) for i in bad.nonzero()[0])
-            raise S4DPLRPreconditionError(where, f"g must be <= 0, not so at index {idx}")
+        _validate_delta(where, plan, offsets, dict(q=q, k=k, v=v, g=g, beta=beta, dout=dout),
+                        dict(state=state, dstate_out=dstate_out))
     dev, dt, f32 = v.device, plan.dtype, torch.float32
     keys, heads = plan._keys, plan._heads
     off = None
@@ -669,7 +693,8 @@ def delta_fwd(plan: "DeltaPlan", q, k, v, g, beta, state, o, state_out, ws, save
     matrices.  offsets: [sequences + 1] int32 on the GPU, or None for equal
     lengths.  scale: None is dk ** -0.5.  saved: ``plan.saved()`` for a later
     ``delta_bwd``."""
-    dev, args, w = _delta_inputs("delta_fwd", plan, q, k, v, g, beta, ws, scale, offsets)
+    dev, args, w = _delta_inputs("delta_fwd", plan, q, k, v, g, beta, ws, scale, offsets,
+                                 state=state)
     st, f32 = plan._states, torch.float32
     args += (_tensor(state, "state", f32, st, dev, True),
              _tensor(o, "o", plan.dtype, plan._vals, dev),
@@ -683,7 +708,8 @@ def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, 
     """Gradients of ``delta_fwd`` with the same inputs and the ``saved`` buffer
     it filled, from ``dout`` and ``dstate_out`` (None: zeros); any of dq, dk, dv,
     dg, dbeta, dstate may be None."""
-    dev, args, w = _delta_inputs("delta_bwd", plan, q, k, v, g, beta, ws, scale, offsets)
+    dev, args, w = _delta_inputs("delta_bwd", plan, q, k, v, g, beta, ws, scale, offsets,
+                                 dout=dout, dstate_out=dstate_out)
     dt, f32 = plan.dtype, torch.float32
     st, keys, vals, heads = plan._states, plan._keys, plan._vals, plan._heads
     args += (_workspace(saved, "saved", plan.saved_bytes, dev),
