@@ -6,7 +6,10 @@
 // the [batch][H][L] layout normalized over its H channels.  Elements are fp32,
 // bf16 or fp16; all arithmetic is fp32, each output is rounded once.  The
 // variance is the mean of squared deviations from the mean (two passes over
-// registers), so a large common offset costs no digits.
+// registers).  A mean m of fp32 sums is off by some of its own steps c, which counts
+// where values are large against their spread; the second pass finds it,
+//   c = sum (x - m) / D,  mean = m + c,  variance = sum (x - m)^2 / D - c^2,
+// so the mean is off by its last rounding and the variance by that of its own size.
 //
 // Both directions are bound by HBM: forward reads x and writes y, backward reads
 // x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 46 us (5.8 TB/s,
@@ -86,7 +89,8 @@ struct RowPart {
 };
 
 // Rows of 32 values a lane over 16 waves: those have 128 registers a lane, so gamma and beta
-// are read where they are used (2048 x 32768 bf16 108 -> 72 us).
+// are read where they are used (2048 x 32768 bf16 108 -> 72 us; 60 since the forward pass joins
+// its waves' parts a lane each, which leaves it without spills; fp32 114).
 constexpr bool wide_rows(int values, int waves) { return waves > 4 && values > 16; }
 
 // The same value, unknown to the compiler: a load at it is not taken out of the loop, where
@@ -96,11 +100,20 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
+// Sum over every group of N lanes, 4 or 16, in all of them.
+template <int N>
+__device__ __forceinline__ float sum_of(float v) {
+  static_assert(N == 4 || N == 16, "");
+  if constexpr (N == 16) return sum16(v);
+  v += dpp<0xB1>(v);
+  return v + dpp<0x4E>(v);
+}
+
 // Forward over rows.  WPR waves share a row (blocks of 256 threads hold 4 rows at WPR =
 // 1), and a block walks over rows blockIdx, blockIdx + gridDim, ..., the next row on its
-// way while one is computed: gamma and beta are read once.  A wave takes mean and
-// squared deviations of its own part; the parts are joined by
-//   m = sum n_w m_w / D,  M = sum M_w + n_w (m_w - m)^2,
+// way while one is computed: gamma and beta are read once.  A wave takes mean (m_w + c_w)
+// and squared deviations M_w of its own part; the parts are joined by
+//   t_w = (m_w - m_0) + c_w,  t = sum n_w t_w / D,  m = m_0 + t,  M = sum M_w + n_w (t_w - t)^2,
 // with one barrier a row (two sets of slots in turn).
 template <typename T, int NV, int WPR, bool WHOLE>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_kernel(
@@ -109,7 +122,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
   using Part = RowPart<T, NV, WPR, WHOLE>;
   constexpr int VEC = Part::VEC, E = Part::E;
   constexpr int RPB = WPR == 1 ? kRowThreads / 64 : 1;
-  __shared__ float red[2][2][WPR];
+  __shared__ float red[2][3][WPR];
   const int tid = WPR == 1 ? threadIdx.x & 63 : threadIdx.x;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   long row = (long)blockIdx.x * RPB + (WPR == 1 ? w : 0);
@@ -122,16 +135,20 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
     Part::columns(gamma, D, tid, 1.f, gm);
     Part::columns(beta, D, tid, 0.f, bt);
   }
-  // elements of the wave's part
-  float n = (float)D;
+  // elements of the wave's part, and of part lane % WPR
+  float n = (float)D, n_of = n;
   if constexpr (WPR > 1) {
-    int c = 0;
+    auto elements = [&](int k) {
+      int c = 0;
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-      const int left = D - Part::at(i, 64 * w);
-      c += left < 0 ? 0 : left < 64 * VEC ? left : 64 * VEC;
-    }
-    n = (float)c;
+      for (int i = 0; i < NV; ++i) {
+        const int left = D - Part::at(i, 64 * k);
+        c += left < 0 ? 0 : left < 64 * VEC ? left : 64 * VEC;
+      }
+      return (float)c;
+    };
+    n = elements(w);
+    n_of = elements(tid % WPR);
   }
   int turn = 0;
   for (; row < rows; turn ^= 1) {
@@ -140,7 +157,7 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
     const long here = row;
     row += (long)gridDim.x * RPB;
     if (row < rows) next.load(x + row * D, D, tid);
-    float s = 0.f, q = 0.f;
+    float s = 0.f, q = 0.f, e = 0.f;
 #pragma unroll
     for (int i = 0; i < E; ++i) s += v[i];
     float m = n > 0.f ? sum64(s) / n : 0.f;
@@ -148,37 +165,30 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
     for (int i = 0; i < NV; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
-        const float d = v[i * VEC + j] - m;
-        q += Part::at(i, tid) + j < D ? d * d : 0.f;
+        const float d = Part::at(i, tid) + j < D ? v[i * VEC + j] - m : 0.f;
+        q = fmaf(d, d, q);
+        e += d;
       }
-    q = sum64(q);
-    if constexpr (WPR > 1) {
+    e = sum64(e);
+    const float c = n > 0.f ? e / n : 0.f;
+    q = sum64(q) - e * c;
+    if constexpr (WPR == 1) {
+      m += c;
+    } else {
       if (tid % 64 == 0) {
         red[turn][0][w] = m;
         red[turn][1][w] = q;
+        red[turn][2][w] = c;
       }
       __syncthreads();
-      float part[WPR], len[WPR];
-      m = q = 0.f;
-#pragma unroll
-      for (int k = 0; k < WPR; ++k) {
-        int c = 0;
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-          const int left = D - Part::at(i, 64 * k);
-          c += left < 0 ? 0 : left < 64 * VEC ? left : 64 * VEC;
-        }
-        len[k] = (float)c;
-        part[k] = red[turn][0][k];
-        m = fmaf(len[k], part[k], m);
-      }
-      m /= (float)D;
-#pragma unroll
-      for (int k = 0; k < WPR; ++k) {
-        const float d = part[k] - m;
-        q += fmaf(len[k] * d, d, red[turn][1][k]);
-      }
+      // every lane one part, and sums over the WPR lanes
+      const int k = tid % WPR;
+      const float m0 = red[turn][0][0], part = (red[turn][0][k] - m0) + red[turn][2][k];
+      const float t = sum_of<WPR>(n_of * part) / (float)D, d = part - t;
+      q = sum_of<WPR>(fmaf(n_of * d, d, red[turn][1][k]));
+      m = m0 + t;
     }
+    q = q < 0.f ? 0.f : q;   // NaN stays
     const float r = 1.f / sqrtf(q / (float)D + eps);
     if constexpr (kWide) {
       using One = RowPart<T, 1, WPR, WHOLE>;
@@ -529,7 +539,7 @@ __global__ __launch_bounds__(64 * W) void norm_channels_kernel(
     float* __restrict__ mean, float* __restrict__ rstd, unsigned positions, int D, unsigned inner,
     float eps) {
   using P = Pack<T, VP>;
-  __shared__ float red[2][1][W][64 * VP];
+  __shared__ float red0[1][W][64 * VP], red1[2][W][64 * VP];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const unsigned tiles = (positions + 64 * VP - 1) / (64 * VP);
   for (unsigned tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
@@ -553,32 +563,44 @@ __global__ __launch_bounds__(64 * W) void norm_channels_kernel(
     if constexpr (EPT > 0)
 #pragma unroll
       for (int k = 0; k < EPT; ++k) v[k] = load_channel<T, VP>(xp, w + W * k, D, inner, on);
-    float s[1][VP], m[VP], r[VP];
+    // Many channels: a wave sums differences from its first one, since thousands of additions
+    // after one another would leave the mean more than a few steps off.
+    float s[1][VP], e[2][VP], x0[VP], m[VP], r[VP];
 #pragma unroll
-    for (int q = 0; q < VP; ++q) s[0][q] = 0.f;
-    channels([&](int k, int d) {
+    for (int q = 0; q < VP; ++q) s[0][q] = e[0][q] = e[1][q] = x0[q] = 0.f;
+    if constexpr (EPT == 0) {
+      const P t = load_channel<T, VP>(xp, w, D, inner, on);
 #pragma unroll
-      for (int q = 0; q < VP; ++q) s[0][q] += d < D ? to_f32(v[k].v[q]) : 0.f;
-      if constexpr (EPT > 0) forget(v[k]);
-    });
-    wave_sums<1, W, VP>(s, red[0], w, lane);
-#pragma unroll
-    for (int q = 0; q < VP; ++q) {
-      m[q] = s[0][q] / (float)D;
-      s[0][q] = 0.f;
+      for (int q = 0; q < VP; ++q) x0[q] = w < D ? to_f32(t.v[q]) : 0.f;
     }
     channels([&](int k, int d) {
 #pragma unroll
+      for (int q = 0; q < VP; ++q) s[0][q] += d < D ? to_f32(v[k].v[q]) - x0[q] : 0.f;
+      if constexpr (EPT > 0) forget(v[k]);
+    });
+    if constexpr (EPT == 0)
+#pragma unroll
+      for (int q = 0; q < VP; ++q) s[0][q] = fmaf((float)((D - w + W - 1) / W), x0[q], s[0][q]);
+    wave_sums<1, W, VP>(s, red0, w, lane);
+#pragma unroll
+    for (int q = 0; q < VP; ++q) m[q] = s[0][q] / (float)D;
+    channels([&](int k, int d) {
+#pragma unroll
       for (int q = 0; q < VP; ++q) {
-        const float t = to_f32(v[k].v[q]) - m[q];
-        s[0][q] = d < D ? fmaf(t, t, s[0][q]) : s[0][q];
+        const float t = d < D ? to_f32(v[k].v[q]) - m[q] : 0.f;
+        e[0][q] = fmaf(t, t, e[0][q]);
+        e[1][q] += t;
       }
       if constexpr (EPT > 0) forget(v[k]);
     });
-    wave_sums<1, W, VP>(s, red[1], w, lane);
+    wave_sums<2, W, VP>(e, red1, w, lane);
 #pragma unroll
-    for (int q = 0; q < VP; ++q) r[q] = 1.f / sqrtf(s[0][q] / (float)D + eps);
-    if (!on) continue;   // red[0] is free: every wave has passed the second barrier
+    for (int q = 0; q < VP; ++q) {
+      const float c = e[1][q] / (float)D, var = e[0][q] / (float)D - c * c;
+      m[q] += c;
+      r[q] = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);   // NaN stays
+    }
+    if (!on) continue;   // red0 is free: every wave has passed the second barrier
     T* yp = y + ps.at;
     channels([&](int k, int d) {
       if (d >= D) return;
