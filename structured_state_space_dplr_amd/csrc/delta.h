@@ -64,6 +64,7 @@ struct DeltaArgs {
   float* dstate;              // may be NULL
   unsigned char *ws, *saved;
   int step_tokens;            // sequences of at most so many tokens go token by token
+  int least;                  // max(1, step_tokens + 1)
 };
 
 // Longest sequence that is taken token by token.  A token costs 1.4 us (128 sequences,
@@ -76,12 +77,18 @@ inline int step_limit(const s4dplr_delta_plan* p) {
   return (long)p->sequences * p->Hv * ((p->dv + 15) / 16) > 256 ? 16 : 8;
 }
 
-// Where a sequence lies in the packed rows, and its chunks in the slots.  Chunks
-// of sequence s are slots first(s) = floor(start / 64) + s and on: disjoint for
-// any lengths, since ceil((b - a) / 64) <= floor(b / 64) - floor(a / 64) + 1.
+// Where a sequence lies in the packed rows, and its chunks in the slots.  `least` is the
+// shortest length that a call takes by chunks.  Chunks of sequence s are slots
+//   first(s) = floor(start / 64) + min(s, floor(start / least))
+// and on: disjoint for any lengths, since ceil((b - a) / 64) <= floor(b / 64) - floor(a / 64) + 1
+// and the second term grows behind every sequence of `least` tokens or more; and below
+// floor(tokens / 64) + min(sequences, floor(tokens / least)).
 struct Rows {
   long start, len;
-  constexpr long first(int s) const { return start / kChunk + s; }
+  constexpr long first(int s, int least) const {
+    const long before = start / least;
+    return start / kChunk + (s < before ? s : before);
+  }
   constexpr int chunks() const { return (int)((len + kChunk - 1) / kChunk); }
 };
 // The sequence from row a to row b of n.  Offsets outside [0, n] and falling ones, whatever
@@ -89,6 +96,19 @@ struct Rows {
 constexpr Rows clamp_rows(int n, int a, int b) {
   const int start = a < 0 ? 0 : a > n ? n : a, end = b < start ? start : b > n ? n : b;
   return Rows{start, end - start};
+}
+
+// Whether a packed call without `saved` takes its short sequences token by token, in a
+// launch of their own.  The lengths are known to the device only.  Where sequences are short
+// in the mean, both forms run, each on its own sequences; else all go by chunks, which one
+// more launch for the few short ones would not make faster.
+inline bool packed_steps(const s4dplr_delta_plan* p) {
+  return p->tokens <= (long)step_limit(p) * p->sequences;
+}
+// Slots that the plan's calls need, at most.
+inline long chunk_slots(const s4dplr_delta_plan* p) {
+  const long most = p->tokens / (p->training || !packed_steps(p) ? 1 : step_limit(p) + 1);
+  return p->tokens / kChunk + (p->sequences < most ? p->sequences : most);
 }
 
 hipError_t launch_delta_steps(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s);

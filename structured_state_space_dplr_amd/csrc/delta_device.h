@@ -168,13 +168,13 @@ __device__ __forceinline__ bool slice_of(int heads, int slices, int* head, int* 
 // The sequence whose chunks include `slot`, by all lanes of a wave together: the last
 // with first(s) <= slot, 64 sequences probed at a time (first(s) rises with s; for
 // offsets out of order some sequence is returned, and the caller's bounds hold).
-__device__ __forceinline__ int sequence_of(const s4dplr_delta_plan& p, const int* offsets,
+__device__ __forceinline__ int sequence_of(const s4dplr_delta_plan& p, const DeltaArgs& a,
                                            long slot) {
   const int lane = threadIdx.x & 63;
   int s = 0;
   for (int n = p.sequences;;) {   // sequences s .. s + n are left
     const int step = (n + 63) / 64, at = lane * step;
-    const bool le = at < n && rows_of(p, offsets, s + at).first(s + at) <= slot;
+    const bool le = at < n && rows_of(p, a.offsets, s + at).first(s + at, a.least) <= slot;
     const int c = __popcll(__ballot(le));
     if (c == 0) return s;
     s += (c - 1) * step;

@@ -125,9 +125,9 @@ __global__ __launch_bounds__(256, three_blocks(PARTS, DKP, GROUPED) ? 3 : 2) voi
   if (slot >= p.slots) return;
   const int hk = blockIdx.y, group = GROUPED ? p.Hv / p.Hk : 1;
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int s = sequence_of(p, a.offsets, slot);
+  const int s = sequence_of(p, a, slot);
   const Rows r = rows_of(p, a.offsets, s);
-  const long c = slot - r.first(s);
+  const long c = slot - r.first(s, a.least);
   if (c < 0 || c * kChunk >= r.len) return;
   const long t0 = r.start + c * kChunk;
   const int n = (int)(r.len - c * kChunk < kChunk ? r.len - c * kChunk : kChunk);
@@ -450,6 +450,7 @@ hipError_t grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) 
 }  // namespace
 
 hipError_t launch_delta_grads(const s4dplr_delta_plan* p, const DeltaArgs& a, hipStream_t s) {
+  if (p->slots == 0) return hipSuccess;   // no tokens
   if (p->dtype == S4DPLR_F32) return grads<float, 3>(p, a, s);
   if (p->dtype == S4DPLR_BF16) return grads<bf16, 1>(p, a, s);
   return grads<f16, 2>(p, a, s);

@@ -36,9 +36,9 @@ __global__ __launch_bounds__(256) void delta_prep_kernel(const s4dplr_delta_plan
   const long slot = blockIdx.x;
   const int h = blockIdx.y, hk = h / (p.Hv / p.Hk);
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int s = sequence_of(p, a.offsets, slot);
+  const int s = sequence_of(p, a, slot);
   const Rows r = rows_of(p, a.offsets, s);
-  const long c = slot - r.first(s);
+  const long c = slot - r.first(s, a.least);
   if (c < 0 || c * kChunk >= r.len || r.len <= a.step_tokens) return;
   const long t0 = r.start + c * kChunk;
   const int n = (int)(r.len - c * kChunk < kChunk ? r.len - c * kChunk : kChunk);
@@ -258,6 +258,7 @@ hipError_t prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStr
 
 hipError_t launch_delta_prep(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd,
                              hipStream_t s) {
+  if (p->slots == 0) return hipSuccess;   // no tokens
   if (p->dtype == S4DPLR_F32) return prep<float, 3>(p, a, bwd, s);
   if (p->dtype == S4DPLR_BF16) return prep<bf16, 1>(p, a, bwd, s);
   return prep<f16, 2>(p, a, bwd, s);

@@ -57,7 +57,7 @@ __device__ __forceinline__ bool place_of(const s4dplr_delta_plan& p, const Delta
   o->hk = o->h / (p.Hv / p.Hk);
   o->r = rows_of(p, a.offsets, s);
   o->nc = o->r.chunks();
-  o->slot0 = o->r.first(s);
+  o->slot0 = o->r.first(s, a.least);
   o->lr = lane & 15;
   o->lg = lane >> 4;
   o->col0 = o->slice * DS;

@@ -159,7 +159,7 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
   p->training = (flags & S4DPLR_DELTA_TRAINING) != 0;
   p->dkp = dk <= 64 ? 64 : dk <= 128 ? 128 : 256;
   p->parts = dtype == S4DPLR_BF16 ? 1 : dtype == S4DPLR_F16 ? 2 : 3;
-  p->slots = tokens / s4::kChunk + sequences;
+  p->slots = s4::chunk_slots(p);
   const size_t ks = (size_t)p->slots * Hk, vs = (size_t)p->slots * Hv;
   const size_t kb = (size_t)p->parts * (p->dkp / 8) * s4::kFrag;   // 64 x dkp, all parts
   size_t off = 0;
@@ -180,11 +180,11 @@ s4dplr_status s4dplr_delta_plan_create(s4dplr_delta_plan** out, int sequences, l
     p->off_ds = take(vs * dk * dv * sizeof(float));
     p->off_gates = take(dk > 64 ? (size_t)((dk + 63) / 64) * 2 * tokens * Hv * sizeof(float) : 0);
   }
-  p->total = off;
+  p->total = off > 0 ? off : kAlign;   // never none: a caller's pointer to it is not NULL
   off = 0;
   p->off_n = take(vs * s4::kChunk * dv * sizeof(float));
   p->off_s = take(vs * dk * dv * sizeof(float));
-  p->saved_total = p->training ? off : 0;
+  p->saved_total = p->training ? (off > 0 ? off : kAlign) : 0;
   *out = p;
   return S4DPLR_OK;
 }
@@ -236,6 +236,7 @@ static s4dplr_status delta_inputs(const s4dplr_delta_plan* p, const void* q, lon
   a->scale = scale;
   a->ws = static_cast<unsigned char*>(const_cast<void*>(ws));
   a->step_tokens = -1;
+  a->least = 1;
   return S4DPLR_OK;
 }
 
@@ -265,15 +266,15 @@ s4dplr_status s4dplr_delta_fwd(const s4dplr_delta_plan* p, const void* q, long l
   a.o = o;
   a.state_out = state_out;
   a.saved = static_cast<unsigned char*>(saved);
-  // The lengths of a packed batch are known to the device only.  Where its sequences
-  // are short in the mean, both forms run, each on its own sequences; else all go by
-  // chunks, which one more launch for the few short ones would not make faster.
   bool steps = false, chunks = true;
   if (!saved) {
     const long limit = s4::step_limit(p);
     chunks = (offsets ? p->tokens : p->each) > limit;
-    steps = !chunks || (offsets && p->tokens <= limit * p->sequences);
-    if (steps) a.step_tokens = (int)limit;
+    steps = !chunks || (offsets && s4::packed_steps(p));
+    if (steps) {
+      a.step_tokens = (int)limit;
+      a.least = (int)limit + 1;
+    }
   }
   hipError_t e = hipSuccess;
   if (chunks) {

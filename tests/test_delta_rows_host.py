@@ -26,3 +26,17 @@ def test_rows_and_slots(tmp_path):
     run = subprocess.run([exe], capture_output=True, text=True, timeout=300)
     assert run.returncode == 0, (run.stdout + run.stderr)[-4000:]
     assert "ok" in run.stdout
+
+
+@pytest.mark.parametrize("sequences,tokens,most", [
+    (1, 1, 1 << 10), (16, 16, 1 << 10), (128, 128, 16 << 20), (4096, 4096, 1 << 29),
+    (16384, 16384, 3 << 29), (128, 1024, 128 << 20)])
+def test_workspace_of_short_sequences(sequences, tokens, most):
+    """Single tokens (bf16, 8 key and 16 value heads of 128 x 128) leave a workspace for what may
+    still be long, not a chunk of 1.2 MB each."""
+    import structured_state_space_dplr_amd as s4
+    plan = s4.DeltaPlan(sequences, tokens, 8, 16, 128, 128, device="cpu")
+    assert 0 < plan.workspace_bytes <= most
+    assert plan.workspace().numel() >= plan.workspace_bytes if most < 1 << 20 else True
+    trained = s4.DeltaPlan(sequences, tokens, 8, 16, 128, 128, training=True, device="cpu")
+    assert trained.workspace_bytes > sequences * (1 << 20) and trained.saved_bytes > 0
