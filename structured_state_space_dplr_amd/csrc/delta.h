@@ -67,12 +67,15 @@ struct DeltaArgs {
   int least;                  // max(1, step_tokens + 1)
 };
 
-// Longest sequence that is taken token by token.  A token costs 1.4 us (128 sequences,
-// 16 heads of 128 x 128: 14 us), a chunk with its preparation what 9 to 16 tokens do:
-// one sequence, 16 heads of 128 x 128: 8 tokens 15.5 us against 18.7, 16 tokens 27.3
-// against 17.4; 16 sequences: 16 tokens 43.1 against 44.3, 24 tokens 59.8 against 44.9;
-// 128 sequences: 249 against 259, 357 against 264.  The line is drawn where the chunked
-// form's blocks (16 columns each) fill the 256 CUs.
+// Longest sequence that is taken token by token.  In bf16 a token costs 1.4 us (128 sequences,
+// 16 heads of 128 x 128: 14 us), a chunk with its preparation what 9 to 16 tokens do.  Token by
+// token against by chunks, 16 heads of 128 x 128: one sequence, 8 tokens 15.5 us against
+// 16.9, 12 tokens 21.2 against 16.9; 16 sequences, 16 tokens 43.3 against 43.6, 24 tokens 60.4
+// against 43.7; 128 sequences, 16 tokens 255 against 270, 24 tokens 370 against 276.  (8 heads of
+// 64 x 64, 128 sequences: 16 tokens 66 against 81, 24 tokens 95 against 81.)  The line is
+// drawn where the chunked form's blocks (16 columns each) fill the 256 CUs.  It holds for all
+// types, though a chunk costs more in fp16 and fp32: 128 sequences of 24 tokens 367 against 459
+// in fp16, 335 against 575 in fp32, one sequence of 12 tokens 18.4 against 20.0 in fp32.
 inline int step_limit(const s4dplr_delta_plan* p) {
   return (long)p->sequences * p->Hv * ((p->dv + 15) / 16) > 256 ? 16 : 8;
 }

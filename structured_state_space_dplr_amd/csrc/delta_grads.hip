@@ -16,8 +16,11 @@
 // linear in the columns: each block writes its part, and delta_gates_kernel adds the
 // parts (dk <= 64: there is one, and it is the result).  Blocks of 64 columns keep a
 // wave under 256 registers and a block under 50 KB of LDS: two or three share a CU
-// and one computes while another loads.  (At 4096 chunks and heads of 128 x 128: 428 us,
-// 1.1 GB read; a block for all 128 columns, one to a CU, took 790.)
+// and one computes while another loads.  (At 4096 chunks and heads of 128 x 128: 438 us,
+// 1.1 GB read; a block for all 128 columns, one to a CU, took 790.)  It waits for loads and
+// for LDS: of the CUs' busy time the matrix units take 23 %, vector instructions 36 % and LDS
+// 38 %, over half of that for bank conflicts.  fp32 and fp16 at dk > 128 spill (fp32 243
+// registers a lane, 341 with grouped heads; fp16 9 and 95).
 //
 // N, S, dV and Z are [dv][..] in memory, 32 of dv a step, and go through LDS as bf16
 // parts; the products' k index is dv, so operands come out of LDS with the
@@ -29,7 +32,9 @@ namespace s4 {
 namespace {
 
 constexpr int kLd = 68;
-constexpr int kLdS = 64 + 16;   // bf16 from row to row of a staged tile: 8 banks
+// bf16 from row to row of a staged tile: rows follow one another by 40 banks, so rows 8 apart
+// share theirs and the transposing read of 8-column steps meets 8 words on one bank.
+constexpr int kLdS = 64 + 16;
 constexpr int kCols = 64;       // columns of dk of a block
 
 // A tile of 32 rows (of dv) by 64 columns of an fp32 matrix, by 256 threads: 4 columns
@@ -92,10 +97,10 @@ __device__ __forceinline__ void store4(T* p, int n, v4f x) {
 
 }  // namespace
 
-// Three blocks a CU where 168 registers a lane do: bf16, one value head a key head (no
-// sums over heads are held), and each step's tiles loaded when it begins, since the
-// other blocks compute meanwhile (485 -> 428 us at 4096 chunks and heads of 128 x
-// 128).  Elsewhere two blocks, with the next step's tiles on their way.
+// Three blocks a CU where 168 registers a lane nearly do (9 and 14 are spilled): bf16, one
+// value head a key head (no sums over heads are held), and each step's tiles loaded
+// when it begins, since the other blocks compute meanwhile (485 -> 428 us at 4096 chunks
+// and heads of 128 x 128).  Elsewhere two blocks, with the next step's tiles on their way.
 constexpr bool three_blocks(int parts, int dkp, bool grouped) {
   return parts == 1 && dkp <= 128 && !grouped;
 }

@@ -8,7 +8,7 @@
 // pass takes X^T, P^T and Q^T instead of X and P.
 //
 // It is bound by what it reads and writes beside short dependent products (256 chunks of 16
-// value heads and 8 key heads of 128 in bf16: 94 us; of 16 key heads 118 us, and 130
+// value heads and 8 key heads of 128 in bf16: 98 us; of 16 key heads 123 us, and 135
 // backward, which transposes Q too); 256 threads and 53 KB of LDS let three blocks share a CU, so that
 // one writes while another computes.
 //

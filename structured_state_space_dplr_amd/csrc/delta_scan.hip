@@ -6,8 +6,8 @@
 //
 // A step is a chain of small products with an exchange between waves after each,
 // so its time is latency and instruction issue, not bandwidth (256 chunks after one
-// another, 16 heads of 128 x 128 in bf16: 448 us forward, 1.75 us a chunk; 4 sequences of 64
-// chunks: 300 us forward with N and S saved, 284 us backward).  Of the 8 waves, 0 - 3
+// another, 16 heads of 128 x 128 in bf16: 466 us forward, 1.8 us a chunk; 4 sequences of 64
+// chunks: 317 us forward with N and S saved, 295 us backward).  Of the 8 waves, 0 - 3
 // walk the chain: wave w owns a quarter of S's rows in fp32 accumulators.  K^T is
 // stored with its rows permuted so that the two accumulator tiles of 32 rows hold 8
 // neighbouring rows a lane: a matrix operand's layout, so S enters K S straight from
@@ -905,11 +905,13 @@ void go(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s)
 
 // bf16 at 64 < dk <= 128: while blocks of 16 columns are no more than the 256 CUs, more
 // of them at once is what counts; beyond, blocks of 32 columns share the loads of a
-// chunk's operands, which bound the step (4 sequences of 4096 tokens, 16 heads of 128
-// x 128, 512 blocks of 16: forward with saving 340 -> 300 us, backward 318 -> 286 us).  At
-// dk <= 64 two blocks of 16 columns share a CU and are the faster ones (5003 tokens in
-// 13 sequences, 8 heads of 64 x 128: 42 us, 48 with 32).  Operands of two and three
-// parts, and dk > 128, leave no room for 32 columns.
+// chunk's operands (4 sequences of 4096 tokens, 16 heads of 128 x 128, 512 blocks of 16:
+// forward with saving 359 -> 317 us, backward 414 -> 295 us).  At dk <= 64 blocks of 16 columns
+// are the faster ones (5003 tokens in 13 sequences, 8 heads of 64 x 128: 46 us, 51 with
+// 32).  Three parts and dk > 128 leave no room for 32 columns.  fp16 has it (162 304 bytes of
+// LDS, no spills) and would gain by it (the same sizes, whole passes: forward 629 us, 525 with
+// 32 columns; backward 1256 and 1097).  fp32 at dk > 128 spills about 160 registers a
+// lane, in the loop over the chunks: 64 chunks of 8 heads of 256 x 128 take 574 us, 162 in bf16.
 template <typename T, int PARTS>
 hipError_t scan(const s4dplr_delta_plan* p, const DeltaArgs& a, bool bwd, hipStream_t s) {
   const long blocks = (long)p->sequences * p->Hv * ((p->dv + 15) / 16);

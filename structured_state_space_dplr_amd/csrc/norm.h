@@ -30,9 +30,10 @@ struct NormArgs {
 // per tile of work (a row, 4 rows up to 512 values, or 64 positions) up to two a CU, one for
 // rows above 2048 values and for channels above 64, whose blocks keep more loads on
 // their way.  More blocks cost more traffic of partial sums, fewer leave the memory
-// idle: 16384 x 2048 bf16 50.5 us with eight a CU, 42.0 with four, 42.6 with two, 51.6 with one;
-// 16384 x 4096 95.1 with four, 79.4 with two, 77.4 with one; channels of 32 x 256 x 1024
-// fp32 30.2 with two, 25.9 with one.  Above 16384 values or kNormChannels channels the
+// idle.  Whole calls, with the partial rows' sum: 16384 x 2048 bf16 51.4 us with eight a CU, 41.9
+// with four, 42.6 with two (half the workspace), 51.2 with one; 16384 x 4096 92.7 with four, 80.1
+// with two, 76.7 with one; 4096 x 4096 30.6, 25.3 and 24.3; channels of 32 x 256 x 1024
+// fp32 30.2 with two, 25.4 with one.  Above 16384 values or kNormChannels channels the
 // columns' sums have their own kernel, whose blocks take some columns each.
 inline long norm_parts(long outer, long D, long inner) {
   const long tiles = inner > 1 ? (outer * inner + 63) / 64 : D <= 512 ? (outer + 3) / 4 : outer;

@@ -12,10 +12,10 @@
 // so the mean is off by its last rounding and the variance by that of its own size.
 //
 // Both directions are bound by HBM: forward reads x and writes y, backward reads
-// x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 46 us (5.8 TB/s,
-// part of it from the last-level cache), backward of 16384 x 2048 41 us with the columns'
-// sums (4.9 TB/s); fp32 channels 32 x 256 x 1024: 15.7 us (4.3 TB/s) and 25.9 us (3.9
-// TB/s).
+// x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 47 us (5.7 TB/s,
+// part of it from the last-level cache), backward of 16384 x 2048 42 us with the columns'
+// sums (4.8 TB/s); fp32 channels 32 x 256 x 1024: 15.5 us (4.3 TB/s) and 25.4 us (4.0
+// TB/s); bf16 channels 11.8 us (2.8 TB/s) and 19.9 us (2.5 TB/s).
 #include "norm.h"
 
 #include "vec.h"
@@ -236,7 +236,10 @@ __device__ __forceinline__ void block_sums(float& s1, float& s2, float (&red)[2]
 
 // Backward over rows.  A block walks over rows as in the forward pass; every lane
 // keeps the same columns, so the columns' sums of dgamma and dbeta stay in its
-// registers and leave the block once, as row blockIdx of part [2][gridDim][D].
+// registers and leave the block once, as row blockIdx of part [2][gridDim][D].  Rows of 8193 to
+// 16384 values spill (fp32 44 registers a lane; 16 bits 17, and 72 where D is no multiple of 8):
+// 4096 x 16384 117 us in bf16 and 248 in fp32, 1.5 times what a copy of their bytes takes,
+// 4096 x 16380 bf16 176.
 template <typename T, int NV, int WPR, bool WHOLE>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bwd_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
@@ -332,8 +335,8 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_bw
 
 // Backward over wide rows, in two kernels, since a row's columns leave no registers for
 // their sums: dx by rows (x and dy are read again behind the row's sums, from the
-// caches), and the columns' sums.  2048 x 32768 bf16 160 us (in one kernel, which spilled,
-// 639), 512 x 32768 fp32 80 (314).
+// caches), and the columns' sums.  2048 x 32768 bf16 156 us (in one kernel, which spilled,
+// 639), 512 x 32768 fp32 76 (314).
 template <typename T, int WPR, bool WHOLE>
 __global__ __launch_bounds__(64 * WPR) void norm_wide_dx_kernel(
     const T* __restrict__ x, const float* __restrict__ gamma, const float* __restrict__ mean,
@@ -803,9 +806,9 @@ long ceil_div(long a, long b) { return (a + b - 1) / b; }
 
 // Vectors a lane holds and waves a row takes: one wave up to 2 vectors a lane, then
 // 4 waves, then 16.  On either side: one wave with 4 vectors, 16384 x 2048 bf16 backward
-// 54.6 us instead of 40.8 (forward 26.1 and 26.8); 4 waves from 2 vectors on, 65536 x 512
-// fp32 forward 63.3 us instead of 42.9; 16 waves from 16 vectors on, 8192 x 8192 bf16
-// forward 64.5 us instead of 46.3.
+// 41.1 us instead of 38.8 (forward 23.3 instead of 28.7); 4 waves from 2 vectors on, 65536 x
+// 512 fp32 forward 76.6 us instead of 45.8, backward 124 instead of 75; 16 waves from 16
+// vectors on, 8192 x 8192 bf16 forward 55.5 us instead of 43.6, backward 80.5 instead of 81.9.
 template <typename T, typename F>
 void row_shape(int D, F f) {
   const int vecs = (int)ceil_div(D, 64 * Vec<T>::N);
@@ -828,8 +831,8 @@ void row_shape(int D, F f) {
 }
 
 // Two positions a lane for 16-bit elements of an even inner axis, if the blocks still
-// fill the 256 CUs (32 x 512 x 1024 bf16 forward 21.7 us against 26.2, gradients 40.6
-// against 46.1).
+// fill the 256 CUs (32 x 512 x 1024 bf16 forward 24.1 us against 28.7, gradients 40.4
+// against 46.3).
 template <typename T, typename F>
 void by_positions(const NormArgs& a, F f) {
   if constexpr (sizeof(T) == 2)
@@ -858,10 +861,10 @@ hipError_t fwd(const NormArgs& a, hipStream_t s) {
     return hipGetLastError();
   }
   // 16 waves of few channels each for 16-bit elements, 8 for fp32, whose lines fill the
-  // loads (32 x 512 x 1024 with 16 against 8: bf16 21.7 against 24.9 us, fp32 33.7 against
-  // 28.3; 8 x 512 x 256 bf16 10.3 against 16.3).  Above 512 channels they are
-  // read again (16 x 1024 x 1024 bf16 31.2 us against 35.3 in registers; fp32 44.5
-  // against 40.8).
+  // loads (32 x 512 x 1024 with 16 against 8: bf16 24.1 against 27.8 us, fp32 35.3 against
+  // 29.9; 8 x 512 x 256 bf16 10.7 against 16.6).  Above 512 channels they are
+  // read again (16 x 1024 x 1024 bf16 31.6 us against 36.7 in registers; fp32 44.8
+  // against 50.0).
   const unsigned n = (unsigned)(a.outer * a.inner), inner = (unsigned)a.inner;
   by_positions<T>(a, [&](auto vp) {
     constexpr int VP = decltype(vp)::value;
