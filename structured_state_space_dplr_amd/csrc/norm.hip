@@ -9,7 +9,8 @@
 // registers).  A mean m of fp32 sums is off by some of its own steps c, which counts
 // where values are large against their spread; the second pass finds it,
 //   c = sum (x - m) / D,  mean = m + c,  variance = sum (x - m)^2 / D - c^2,
-// so the mean is off by its last rounding and the variance by that of its own size.
+// which is applied where c is more than 2^-20 of the deviation (below, the sum's own rounding
+// is no smaller).
 //
 // Both directions are bound by HBM: forward reads x and writes y, backward reads
 // x and dy and writes dx.  Measured, bf16 rows: forward of 16384 x 4096 47 us (5.7 TB/s,
@@ -100,20 +101,34 @@ __device__ __forceinline__ int opaque(int x) {
   return x;
 }
 
-// Sum over every group of N lanes, 4 or 16, in all of them.
+// Sum over every group of N lanes, 4 or 16, the same bits in all of them: a lane's own product
+// must not enter the first addition unrounded, as a contraction would have it.
 template <int N>
 __device__ __forceinline__ float sum_of(float v) {
+#pragma clang fp contract(off)
   static_assert(N == 4 || N == 16, "");
-  if constexpr (N == 16) return sum16(v);
-  v += dpp<0xB1>(v);
-  return v + dpp<0x4E>(v);
+  v += dpp<0xB1>(v);    // quad_perm [1, 0, 3, 2]
+  v += dpp<0x4E>(v);    // quad_perm [2, 3, 0, 1]
+  if constexpr (N == 16) {
+    v += dpp<0x141>(v);   // row_half_mirror
+    v += dpp<0x140>(v);   // row_mirror
+  }
+  return v;
+}
+
+// The error that counts of a mean of n values, from the sums e of what they differ by and q
+// of its squares; 0 too where either is not finite.
+__device__ __forceinline__ float lost(float e, float q, float n) {
+  const float c = e / n;
+  return c * e > 0x1p-40f * q ? c : 0.f;
 }
 
 // Forward over rows.  WPR waves share a row (blocks of 256 threads hold 4 rows at WPR =
 // 1), and a block walks over rows blockIdx, blockIdx + gridDim, ..., the next row on its
 // way while one is computed: gamma and beta are read once.  A wave takes mean (m_w + c_w)
 // and squared deviations M_w of its own part; the parts are joined by
-//   t_w = (m_w - m_0) + c_w,  t = sum n_w t_w / D,  m = m_0 + t,  M = sum M_w + n_w (t_w - t)^2,
+//   m = sum n_w m_w / D,  t_w = (m_w - m) + c_w,  c = sum n_w t_w / D,  mean = m + c,
+//   M = sum (M_w + n_w t_w^2) - D c^2,
 // with one barrier a row (two sets of slots in turn).
 template <typename T, int NV, int WPR, bool WHOLE>
 __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_kernel(
@@ -170,8 +185,9 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
         e += d;
       }
     e = sum64(e);
-    const float c = n > 0.f ? e / n : 0.f;
-    q = sum64(q) - e * c;
+    q = sum64(q);
+    float c = lost(e, q, n);
+    q -= e * c;
     if constexpr (WPR == 1) {
       m += c;
     } else {
@@ -183,10 +199,13 @@ __global__ __launch_bounds__(WPR > 4 ? 64 * WPR : kRowThreads) void norm_rows_ke
       __syncthreads();
       // every lane one part, and sums over the WPR lanes
       const int k = tid % WPR;
-      const float m0 = red[turn][0][0], part = (red[turn][0][k] - m0) + red[turn][2][k];
-      const float t = sum_of<WPR>(n_of * part) / (float)D, d = part - t;
-      q = sum_of<WPR>(fmaf(n_of * d, d, red[turn][1][k]));
-      m = m0 + t;
+      m = sum_of<WPR>(n_of * red[turn][0][k]) / (float)D;
+      const float part = (red[turn][0][k] - m) + red[turn][2][k];
+      e = sum_of<WPR>(n_of * part);
+      q = sum_of<WPR>(fmaf(n_of * part, part, red[turn][1][k]));
+      c = lost(e, q, (float)D);
+      q -= e * c;
+      m += c;
     }
     q = q < 0.f ? 0.f : q;   // NaN stays
     const float r = 1.f / sqrtf(q / (float)D + eps);
@@ -599,9 +618,9 @@ __global__ __launch_bounds__(64 * W) void norm_channels_kernel(
     wave_sums<2, W, VP>(e, red1, w, lane);
 #pragma unroll
     for (int q = 0; q < VP; ++q) {
-      const float c = e[1][q] / (float)D, var = e[0][q] / (float)D - c * c;
+      const float c = lost(e[1][q], e[0][q], (float)D), sq = e[0][q] - e[1][q] * c;
       m[q] += c;
-      r[q] = 1.f / sqrtf((var < 0.f ? 0.f : var) + eps);   // NaN stays
+      r[q] = 1.f / sqrtf((sq < 0.f ? 0.f : sq) / (float)D + eps);   // NaN stays
     }
     if (!on) continue;   // red0 is free: every wave has passed the second barrier
     T* yp = y + ps.at;
