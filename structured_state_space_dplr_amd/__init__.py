@@ -639,8 +639,8 @@ def _validate_delta(where, plan, offsets, rows, states):
     """The preconditions of ``delta_fwd`` and ``delta_bwd``: offsets that rise within the rows,
     finite values and g <= 0 in the sequences' rows (the others are not read)."""
     lo, hi = 0, plan.tokens
-    if offsets is not None:
-        at = [int(i) for i in _host(offsets).flatten()]
+    at = [] if offsets is None else [int(i) for i in _host(offsets).flatten()]
+    if len(at) == plan.sequences + 1:       # any other length is refused behind this
         for i, (a, b) in enumerate(zip([0, *at], [*at, plan.tokens])):
             if a > b:
                 what = f"offsets[{i}] = {b} < {a}" if i < len(at) else f"offsets end at {a} > {b} rows"

@@ -56,6 +56,11 @@ def test_offsets_that_do_not_rise_within_the_rows(s4, offsets, bwd):
     refused(s4, "offsets", delta_inputs(), offsets, bwd=bwd)
 
 
+@pytest.mark.parametrize("offsets", [[], [0], [0, 5, 10, 10]])
+def test_offsets_of_another_length(s4, offsets):
+    refused(s4, "GPU tensor", delta_inputs(), offsets)      # the tensors' own checks come next
+
+
 @pytest.mark.parametrize("name,bwd", [("q", 0), ("k", 0), ("v", 0), ("beta", 0), ("state", 0),
                                       ("q", 1), ("v", 1), ("dout", 1), ("dstate_out", 1)])
 @pytest.mark.parametrize("value", [NAN, INF])
