@@ -41,6 +41,11 @@ inline long norm_parts(long outer, long D, long inner) {
   return tiles < 1 ? 1 : tiles < most ? tiles : most;
 }
 
+// out0[c] = sum_b part[0][b][c] and out1[c] = sum_b part[1][b][c] of nb rows of D floats, each
+// may be NULL; always in the same order.
+hipError_t launch_columns(const float* part, int nb, int D, float* out0, float* out1,
+                          hipStream_t s);
+
 hipError_t launch_norm_fwd(const NormArgs& a, int dtype, hipStream_t s);
 hipError_t launch_norm_bwd(const NormArgs& a, int dtype, hipStream_t s);
 
