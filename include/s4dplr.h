@@ -478,6 +478,89 @@ s4dplr_status s4dplr_delta_bwd(const s4dplr_delta_plan* plan, const void* q, lon
 /* Release a plan (NULL is ignored).  Host-only. */
 void s4dplr_delta_plan_destroy(s4dplr_delta_plan* plan);
 
+/* ------------------------------------------------------------------------
+ * Root-mean-square norm with the residual stream's addition, and products of
+ * 8-bit matrices: what stands before and around a token-major layer.
+ *
+ * An 8-bit matrix holds e4m3 values (q, largest 448) and a scale for each 128 of
+ * them, a power of two (e8m0: byte b stands for 2^(b - 127), 255 for NaN); a
+ * value stands for q times its scale.  Groups are 128 neighbouring columns of one
+ * row, the last one of a row shorter, or 128 x 128 blocks ("square").
+ * A group's scale is the least power of two s with max |value| <= 448 s, 2^-126 at
+ * least.  A group that holds an infinity or NaN becomes NaN.
+ * ---------------------------------------------------------------------- */
+
+/*
+ * Per row of D values:
+ *   h = x + residual (rounded to `dtype`),  r = 1 / sqrt(mean_d h^2 + eps),  y = h r gamma_d.
+ *   x, residual, h, y: [rows][D] elements of `dtype`; residual may be NULL (h = x).  h may
+ *                      be NULL (not written) or residual itself.
+ *   gamma : [D] float32 or NULL (1).
+ *   y     : may be NULL if q is given.
+ *   q, scales: both NULL, or y in 8 bits: e4m3 [rows][D], e8m0 [rows][ceil(D / 128)].
+ *   rstd  : [rows] float32, the r that s4dplr_rms_norm_bwd reads; may be NULL.
+ * rows = 0 is a no-op.  Limits: 0 <= rows < 2^31, 1 <= D <= 32768, eps >= 0 and
+ * finite (ERR_SHAPE); h^2 and its sums within float32.
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS (an output overlaps an
+ * input or another output), ERR_UNSUPPORTED (dtype), ERR_HIP.
+ */
+s4dplr_status s4dplr_rms_norm_fwd(const void* x, const void* residual, const float* gamma, void* h,
+                                  void* y, void* q, void* scales, float* rstd, long rows, long D,
+                                  float eps, int dtype, hipStream_t stream);
+
+/* Bytes of workspace of s4dplr_rms_norm_bwd (partial sums of dgamma).
+ * Errors: ERR_NULL, ERR_SHAPE. */
+s4dplr_status s4dplr_rms_norm_workspace_bytes(long rows, long D, size_t* bytes);
+
+/*
+ * Gradients of s4dplr_rms_norm_fwd from dy = dloss/dy (of y in 8 bits: as if it were not
+ * rounded) and dh = dloss/dh, what the residual stream brings (NULL: none), with xh = h
+ * rstd and w = dy gamma:
+ *   dx = dh + rstd (w - xh mean_d (w xh))   (the gradient of x, and of residual),
+ *   dgamma_d = sum over the rows of dy xh.
+ * h (x where there was no residual), dy, dh, dx: elements of `dtype`; dx may be dh itself.
+ * dx and dgamma may be NULL (not computed); outputs are overwritten, not
+ * accumulated.  dgamma is summed in a fixed order: equal calls give equal bits.
+ * rows = 0 writes dgamma = 0.  Limits and errors as above, and ERR_WORKSPACE (ws not 256-byte aligned).
+ */
+s4dplr_status s4dplr_rms_norm_bwd(const void* h, const float* gamma, const float* rstd,
+                                  const void* dy, const void* dh, void* dx, float* dgamma,
+                                  long rows, long D, int dtype, void* ws, hipStream_t stream);
+
+/*
+ * x [rows][cols] (elements of `dtype`, rows ldx elements apart) as an 8-bit matrix, as its
+ * transposed one, or both:
+ *   q [rows][cols], scales [rows][ceil(cols / 128)]: groups along the rows,
+ *   qt [cols][rows], scales_t [cols][ceil(rows / 128)]: groups along the columns of x;
+ * with `square` both have the scales of 128 x 128 blocks, [ceil(rows / 128)][ceil(cols / 128)]
+ * and its transpose.  Either pair may be NULL.  Every value is rounded once, to
+ * nearest with ties to even.  No rows or columns: a no-op.
+ * Limits: rows <= 2^22, cols and ldx < 2^24, ldx >= cols, fewer than 2^23 blocks (ERR_SHAPE).
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (dtype), ERR_HIP.
+ */
+s4dplr_status s4dplr_quantize_fp8(const void* x, long ldx, void* q, void* scales, void* qt,
+                                  void* scales_t, long rows, long cols, int square, int dtype,
+                                  hipStream_t stream);
+
+/*
+ * out [M][N] = A B^T of 8-bit matrices A [M][K] and B [N][K], groups along K:
+ *   out_mn = sum over the groups g of sa_mg sb_ng sum_k a_mk b_nk   (k in group g).
+ * lda, ldb, ldo: elements from one row to the next.  a_scales [M][ceil(K / 128)], b_scales
+ * [N][ceil(K / 128)], with b_square [ceil(N / 128)][ceil(K / 128)].  out: elements of `dtype`,
+ * rounded once.  Sums are fp32.  16-bit outputs come from the 8-bit matrix
+ * instructions, which add up the products inside an instruction with fewer bits: off by about
+ * 2^-16 of the result (7e-5 where a group's values span eight powers of two); a float32 output from
+ * the bf16 ones, exact in every product.
+ * The layer's products: output X W^T (X by rows, W square), dX = dY W (dY by rows, W's
+ * transpose, square), dW = dY^T X (the transposes of both, by their rows).
+ * M or N = 0 is a no-op, K = 0 writes zeros.  Limits: sizes and pitches below 2^24,
+ * ceil(M / 64) ceil(N / 128) < 2^23 (ERR_SHAPE).
+ * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (dtype), ERR_HIP.
+ */
+s4dplr_status s4dplr_matmul_fp8(const void* a, long lda, const void* a_scales, const void* b,
+                                long ldb, const void* b_scales, int b_square, void* out, long ldo,
+                                long M, long N, long K, int dtype, hipStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -23,6 +23,10 @@ tensors of any size and alignment, launch on the device of their tensors, and
 ``stream=None`` is that device's current stream.  With ``S4DPLR_VALIDATE=1``
 their inputs are checked to be finite, the log decays g to be <= 0 and offsets
 to rise within the rows; rows outside every sequence may hold anything.
+
+``rms_norm_fwd`` / ``rms_norm_bwd``, ``quantize_fp8`` and ``matmul_fp8`` follow the same
+conventions.  A matrix in 8 bits is a float8_e4m3fn tensor with a float8_e8m0fnu tensor of
+scales, one for each 128 columns of a row or for each 128 x 128 block.
 """
 from __future__ import annotations
 
@@ -40,6 +44,7 @@ __all__ = [
     "conv_apply", "recurrent_prepare", "recurrent_scan", "conv_bwd", "kernel_gen_bwd",
     "block_forward", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
     "DeltaPlan", "delta_fwd", "delta_bwd",
+    "rms_norm_fwd", "rms_norm_bwd", "rms_norm_workspace_bytes", "quantize_fp8", "matmul_fp8",
     "plan_destroy", "Plan", "LIB_PATH",
 ]
 
@@ -112,6 +117,16 @@ _lib.s4dplr_delta_bwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l] + [_p] * 3 + [cty
                                   + [_p] * 11)
 _lib.s4dplr_delta_plan_destroy.restype = None
 _lib.s4dplr_delta_plan_destroy.argtypes = [_p]
+_lib.s4dplr_rms_norm_fwd.restype = _i
+_lib.s4dplr_rms_norm_fwd.argtypes = [_p] * 8 + [_l] * 2 + [ctypes.c_float, _i, _p]
+_lib.s4dplr_rms_norm_workspace_bytes.restype = _i
+_lib.s4dplr_rms_norm_workspace_bytes.argtypes = [_l] * 2 + [ctypes.POINTER(ctypes.c_size_t)]
+_lib.s4dplr_rms_norm_bwd.restype = _i
+_lib.s4dplr_rms_norm_bwd.argtypes = [_p] * 7 + [_l] * 2 + [_i, _p, _p]
+_lib.s4dplr_quantize_fp8.restype = _i
+_lib.s4dplr_quantize_fp8.argtypes = [_p, _l] + [_p] * 4 + [_l] * 2 + [_i, _i, _p]
+_lib.s4dplr_matmul_fp8.restype = _i
+_lib.s4dplr_matmul_fp8.argtypes = [_p, _l, _p, _p, _l, _p, _i, _p] + [_l] * 4 + [_i, _p]
 _lib.s4dplr_plan_destroy.restype = None
 _lib.s4dplr_plan_destroy.argtypes = [_p]
 
@@ -720,3 +735,171 @@ def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, 
              _tensor(dbeta, "dbeta", f32, heads, dev, True),
              _tensor(dstate, "dstate", f32, st, dev, True), w)
     _check(_launch(dev, stream, _lib.s4dplr_delta_bwd, args), "delta_bwd")
+
+
+# ------------------------------- root-mean-square norm and 8-bit products
+
+_E4M3, _E8M0 = torch.float8_e4m3fn, torch.float8_e8m0fnu
+_GROUP = 128
+
+
+def _groups(n: int) -> int:
+    return -(-n // _GROUP)
+
+
+def _matrix(t, name, dtype, device=None, shape=None):
+    """Device pointer and row pitch of a matrix whose rows are contiguous (a column
+    range of a wider one will do)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name}: must be a GPU tensor")
+    if t.dtype != dtype:
+        raise TypeError(f"{name}: must be {dtype}, got {t.dtype}")
+    if t.dim() != 2 or (shape is not None and tuple(t.shape) != shape):
+        raise ValueError(f"{name}: expected {'a matrix' if shape is None else f'shape {shape}'}, "
+                         f"got {tuple(t.shape)}")
+    if device is not None and t.device != device:
+        raise ValueError(f"{name}: on {t.device}, expected {device}")
+    rows, cols = t.shape
+    sr, sc = t.stride()
+    if (cols > 1 and sc != 1) or (rows > 1 and sr < cols):
+        raise ValueError(f"{name}: each row must be contiguous and apart from the others, "
+                         f"got strides {(sr, sc)}")
+    return t.data_ptr(), sr if rows > 1 else cols
+
+
+def _rms_dims(x):
+    """Rows and D of a tensor normalized along its last axis."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: expected a torch.Tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x: must be float32, bfloat16 or float16, got {x.dtype}")
+    if x.dim() < 1:
+        raise ValueError("x: expected at least one dimension")
+    rows = 1
+    for n in x.shape[:-1]:
+        rows *= n
+    return rows, x.shape[-1]
+
+
+def rms_norm_fwd(x, residual, gamma, h, y, rstd=None, q=None, scales=None, eps: float = 1e-5,
+                 stream=None) -> None:
+    """``h`` = x + residual, ``y`` = the root-mean-square norm of h along the last
+    axis times gamma.
+
+    residual: None (h = x) or like x; h: None or like x (may be ``residual``).  y: like x,
+    or None if ``q`` (float8_e4m3fn, the shape of x) and ``scales`` (float8_e8m0fnu,
+    [..., ceil(D / 128)]) take it in 8 bits; both may be given.  gamma: [D] float32 or None
+    (1).  rstd: float32, the shape of x without the last axis, what ``rms_norm_bwd`` reads."""
+    rows, D = _rms_dims(x)
+    dev, dt, shape = x.device, x.dtype, x.shape
+    if validation_enabled():
+        check_preconditions("rms_norm_fwd", x=x, residual=residual, gamma=gamma)
+    args = (_tensor(x, "x", dt, shape), _tensor(residual, "residual", dt, shape, dev, True),
+            _tensor(gamma, "gamma", torch.float32, (D,), dev, True),
+            _tensor(h, "h", dt, shape, dev, True), _tensor(y, "y", dt, shape, dev, True),
+            _tensor(q, "q", _E4M3, shape, dev, True),
+            None if scales is None else _tensor(scales, "scales", _E8M0,
+                                                shape[:-1] + (_groups(D),), dev),
+            _tensor(rstd, "rstd", torch.float32, shape[:-1], dev, True),
+            rows, D, eps, _DTYPES[dt])
+    _check(_launch(dev, stream, _lib.s4dplr_rms_norm_fwd, args), "rms_norm_fwd")
+
+
+@functools.lru_cache(maxsize=1024)
+def _rms_workspace(rows, D, where):
+    n = ctypes.c_size_t()
+    _check(_lib.s4dplr_rms_norm_workspace_bytes(rows, D, ctypes.byref(n)), where)
+    return n.value
+
+
+def rms_norm_workspace_bytes(x) -> int:
+    """Bytes of workspace of ``rms_norm_bwd`` for this ``x``."""
+    return _rms_workspace(*_rms_dims(x), "rms_norm_workspace_bytes")
+
+
+def rms_norm_bwd(h, gamma, rstd, dy, dh, dx, dgamma, ws, stream=None) -> None:
+    """Gradients of ``rms_norm_fwd`` from ``dy`` and ``dh`` (None: zeros): ``dx`` (of x
+    and of the residual alike; may be ``dh``) and ``dgamma``, either may be None.  h: x where
+    there was no residual.  ``ws``: a 256-byte aligned GPU tensor of
+    ``rms_norm_workspace_bytes``."""
+    rows, D = _rms_dims(h)
+    dev, dt, shape, f32 = h.device, h.dtype, h.shape, torch.float32
+    if validation_enabled():
+        check_preconditions("rms_norm_bwd", h=h, gamma=gamma, rstd=rstd, dy=dy, dh=dh)
+    args = (_tensor(h, "h", dt, shape), _tensor(gamma, "gamma", f32, (D,), dev, True),
+            _tensor(rstd, "rstd", f32, shape[:-1], dev), _tensor(dy, "dy", dt, shape, dev),
+            _tensor(dh, "dh", dt, shape, dev, True), _tensor(dx, "dx", dt, shape, dev, True),
+            _tensor(dgamma, "dgamma", f32, (D,), dev, True), rows, D, _DTYPES[dt],
+            _workspace(ws, "ws", _rms_workspace(rows, D, "rms_norm_bwd"), dev))
+    _check(_launch(dev, stream, _lib.s4dplr_rms_norm_bwd, args), "rms_norm_bwd")
+
+
+def _square(scales, name, rows, cols):
+    """Whether the scales of a rows x cols matrix are those of 128 x 128 blocks."""
+    if not isinstance(scales, torch.Tensor):
+        raise TypeError(f"{name}: expected a torch.Tensor")
+    shape, across = tuple(scales.shape), _groups(cols)
+    if shape == (rows, across):
+        return False
+    if shape == (_groups(rows), across):
+        return True
+    raise ValueError(f"{name}: expected shape {(rows, across)} or {(_groups(rows), across)}, "
+                     f"got {shape}")
+
+
+def quantize_fp8(x, q, scales, qt=None, scales_t=None, stream=None) -> None:
+    """The matrix ``x`` in 8 bits: ``q`` (float8_e4m3fn, like x) with ``scales``
+    (float8_e8m0fnu) for each 128 columns of a row, its transpose ``qt`` with
+    ``scales_t`` for each 128 rows of a column, or both; either pair may be None.
+    scales: [rows, ceil(cols / 128)], scales_t: [cols, ceil(rows / 128)], or, for
+    128 x 128 blocks, [ceil(rows / 128), ceil(cols / 128)] and its transpose."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x: expected a torch.Tensor")
+    if x.dtype not in _DTYPES:
+        raise TypeError(f"x: must be float32, bfloat16 or float16, got {x.dtype}")
+    xp, ldx = _matrix(x, "x", x.dtype)
+    if validation_enabled():
+        check_preconditions("quantize_fp8", x=x)
+    (rows, cols), dev, kinds = x.shape, x.device, []
+    out = []
+    for t, s, name, r, c in ((q, scales, "", rows, cols), (qt, scales_t, "_t", cols, rows)):
+        if t is None and s is None:
+            out += [None, None]
+            continue
+        if r > 1 and c > 0:     # one row: both kinds are the same
+            kinds.append(_square(s, "scales" + name, r, c))
+        sq = kinds[-1] if kinds else False
+        out += [_tensor(t, "qt" if name else "q", _E4M3, (r, c), dev),
+                _tensor(s, "scales" + name, _E8M0, (_groups(r) if sq else r, _groups(c)), dev)]
+    if len(set(kinds)) > 1:
+        raise ValueError("scales, scales_t: both by rows or both by 128 x 128 blocks")
+    args = (xp, ldx, *out, rows, cols, int(any(kinds)), _DTYPES[x.dtype])
+    _check(_launch(dev, stream, _lib.s4dplr_quantize_fp8, args), "quantize_fp8")
+
+
+def matmul_fp8(a, a_scales, b, b_scales, out, stream=None) -> None:
+    """``out`` [M, N] = a b^T of 8-bit matrices a [M, K] and b [N, K] (float8_e4m3fn).
+
+    a_scales: [M, ceil(K / 128)] float8_e8m0fnu; b_scales: [N, ceil(K / 128)], or
+    [ceil(N / 128), ceil(K / 128)] for 128 x 128 blocks.  out: float32, bfloat16 or
+    float16.  a, b and out may be column ranges of wider matrices."""
+    if not isinstance(out, torch.Tensor):
+        raise TypeError("out: expected a torch.Tensor")
+    if out.dtype not in _DTYPES:
+        raise TypeError(f"out: must be float32, bfloat16 or float16, got {out.dtype}")
+    op, ldo = _matrix(out, "out", out.dtype)
+    (M, N), dev = out.shape, out.device
+    ap, lda = _matrix(a, "a", _E4M3, dev)
+    K = a.shape[1]
+    if a.shape[0] != M:
+        raise ValueError(f"a: expected shape {(M, K)}, got {tuple(a.shape)}")
+    bp, ldb = _matrix(b, "b", _E4M3, dev, (N, K))
+    square = _square(b_scales, "b_scales", N, K)
+    if validation_enabled():
+        check_preconditions("matmul_fp8", a=a, a_scales=a_scales, b=b, b_scales=b_scales)
+    args = (ap, lda, _tensor(a_scales, "a_scales", _E8M0, (M, _groups(K)), dev), bp, ldb,
+            _tensor(b_scales, "b_scales", _E8M0, tuple(b_scales.shape), dev), int(square),
+            op, ldo, M, N, K, _DTYPES[out.dtype])
+    _check(_launch(dev, stream, _lib.s4dplr_matmul_fp8, args), "matmul_fp8")

@@ -18,7 +18,8 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libs4dplr.so")
 SOURCES = ["kernels.hip", "big.hip", "recurrent.hip", "backward.hip", "vandermonde.hip", "block.hip",
            "noalloc.hip", "rank.hip", "norm.hip", "delta_step.hip", "delta_prep.hip",
-           "delta_scan.hip", "delta_grads.hip", "api.cpp", "token_api.cpp"]
+           "delta_scan.hip", "delta_grads.hip", "rms.hip", "quantize.hip", "matmul.hip", "api.cpp",
+           "token_api.cpp", "dense_api.cpp"]
 ARCH = "gfx950"
 
 
