@@ -478,6 +478,80 @@ s4dplr_status s4dplr_delta_bwd(const s4dplr_delta_plan* plan, const void* q, lon
 /* Release a plan (NULL is ignored).  Host-only. */
 void s4dplr_delta_plan_destroy(s4dplr_delta_plan* plan);
 
+/*
+ * Linear attention with a decay for each head.  Per sequence and value head h, with the
+ * key head h Hk / Hv, a_t = exp(g_t) and the dk x dv state S (fp32):
+ *   S <- a_t S + k_t v_t^T,   o_t = scale S^T q_t.
+ * Tensors, packed sequences and offsets are those of the gated delta rule above.  g is
+ * [tokens][Hv] float32, with g_fixed [Hv] (one decay for all tokens), or NULL (a_t = 1).
+ *
+ * Preconditions not checked on the device: finite values, and g <= 0 (g = -infinity is a
+ * reset: nothing of the state is kept).
+ */
+typedef struct s4dplr_linear_attention_plan s4dplr_linear_attention_plan;
+
+/* Plan flag: reserve what the backward pass needs. */
+#define S4DPLR_LINEAR_ATTENTION_TRAINING 1u
+
+/*
+ * Plan for `sequences` sequences of together `tokens` rows.  Host-only.  Limits:
+ * sequences >= 1, tokens >= 0, 1 <= dk, dv <= 256, Hk >= 1, Hv a multiple of Hk up to
+ * 65535, sequences * Hv <= 2^18, tokens * Hv < 2^31 (ERR_SHAPE).  Errors: ERR_NULL,
+ * ERR_SHAPE, ERR_UNSUPPORTED (dtype, flags).  A plan is immutable and may be used
+ * from several threads and streams, each with its own workspace.
+ */
+s4dplr_status s4dplr_linear_attention_plan_create(s4dplr_linear_attention_plan** out,
+                                                  int sequences, long tokens, int Hk, int Hv,
+                                                  int dk, int dv, int dtype, unsigned flags);
+
+/* Bytes of workspace, and of the buffer `saved` that the forward pass of a
+ * training plan fills for the backward pass (0 without the flag; may be NULL).
+ * The workspace holds nothing between calls.  Errors: ERR_NULL. */
+s4dplr_status s4dplr_linear_attention_plan_bytes(const s4dplr_linear_attention_plan* plan,
+                                                 size_t* workspace, size_t* saved);
+
+/*
+ * Forward pass.  ldq, ldk, ldv: elements from one row of q, k, v to the next (at
+ * least Hk dk, Hk dk, Hv dv, below 2^24); o is contiguous.  state: [sequences][Hv][dk][dv]
+ * float32, the states before the first rows, NULL for zeros; state_out: the states after the
+ * last rows, may be NULL (not written) or `state` itself.  saved: NULL, or (plans with
+ * S4DPLR_LINEAR_ATTENTION_TRAINING) the buffer for s4dplr_linear_attention_bwd, 256-byte
+ * aligned.  Short sequences are taken token by token in one launch, longer ones by chunks
+ * on the matrix cores, in segments that are joined through their states; both compute the
+ * same recurrence.  tokens = 0 passes the states on.
+ * Errors: ERR_NULL, ERR_SHAPE (a row pitch; without offsets, tokens not a multiple of
+ * sequences), ERR_ALIGN, ERR_ALIAS (an output overlaps an input, another output or the
+ * workspace), ERR_WORKSPACE (ws or saved not 256-byte aligned), ERR_UNSUPPORTED (saved without
+ * the flag), ERR_HIP.
+ */
+s4dplr_status s4dplr_linear_attention_fwd(const s4dplr_linear_attention_plan* plan, const void* q,
+                                          long ldq, const void* k, long ldk, const void* v,
+                                          long ldv, const float* g, int g_fixed,
+                                          const int* offsets, float scale, const float* state,
+                                          void* o, float* state_out, void* saved, void* ws,
+                                          hipStream_t stream);
+
+/*
+ * Gradients of s4dplr_linear_attention_fwd with the same inputs and the buffer it filled:
+ * from dout = dloss/do [tokens][Hv][dv] (contiguous) and dstate_out = dloss/dstate_out (NULL
+ * for zeros) to dq, dk [tokens][Hk][dk], dv [tokens][Hv][dv] (contiguous, elements of the
+ * plan's dtype), dg (float32, the shape of g) and dstate [sequences][Hv][dk][dv] (float32; may
+ * be dstate_out itself).  Any output may be NULL (not written; dg must be where g is); outputs
+ * are overwritten, not accumulated.  dg is taken from q . dq and k . dk by sums in 64 bits.
+ * Gradients of shared key heads are summed over their value heads in a fixed order: equal calls
+ * give equal bits.  `saved` is only read.  Errors as for s4dplr_linear_attention_fwd.
+ */
+s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* plan, const void* q,
+                                          long ldq, const void* k, long ldk, const void* v,
+                                          long ldv, const float* g, int g_fixed,
+                                          const int* offsets, float scale, const void* saved,
+                                          const void* dout, const float* dstate_out, void* dq,
+                                          void* dk, void* dv, float* dg, float* dstate, void* ws,
+                                          hipStream_t stream);
+
+/* Release a plan (NULL is ignored).  Host-only. */
+void s4dplr_linear_attention_plan_destroy(s4dplr_linear_attention_plan* plan);
+
 /* ------------------------------------------------------------------------
  * Root-mean-square norm with the residual stream's addition, and products of
  * 8-bit matrices: what stands before and around a token-major layer.

@@ -44,6 +44,7 @@ __all__ = [
     "conv_apply", "recurrent_prepare", "recurrent_scan", "conv_bwd", "kernel_gen_bwd",
     "block_forward", "layer_norm_fwd", "layer_norm_bwd", "layer_norm_workspace_bytes",
     "DeltaPlan", "delta_fwd", "delta_bwd",
+    "LinearAttentionPlan", "linear_attention_fwd", "linear_attention_bwd",
     "rms_norm_fwd", "rms_norm_bwd", "rms_norm_workspace_bytes", "quantize_fp8", "matmul_fp8",
     "plan_destroy", "Plan", "LIB_PATH",
 ]
@@ -117,6 +118,18 @@ _lib.s4dplr_delta_bwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l] + [_p] * 3 + [cty
                                   + [_p] * 11)
 _lib.s4dplr_delta_plan_destroy.restype = None
 _lib.s4dplr_delta_plan_destroy.argtypes = [_p]
+_lib.s4dplr_linear_attention_plan_create.restype = _i
+_lib.s4dplr_linear_attention_plan_create.argtypes = _lib.s4dplr_delta_plan_create.argtypes
+_lib.s4dplr_linear_attention_plan_bytes.restype = _i
+_lib.s4dplr_linear_attention_plan_bytes.argtypes = _lib.s4dplr_delta_plan_bytes.argtypes
+_lib.s4dplr_linear_attention_fwd.restype = _i
+_lib.s4dplr_linear_attention_fwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l, _p, _i, _p,
+                                              ctypes.c_float] + [_p] * 6)
+_lib.s4dplr_linear_attention_bwd.restype = _i
+_lib.s4dplr_linear_attention_bwd.argtypes = ([_p, _p, _l, _p, _l, _p, _l, _p, _i, _p,
+                                              ctypes.c_float] + [_p] * 10)
+_lib.s4dplr_linear_attention_plan_destroy.restype = None
+_lib.s4dplr_linear_attention_plan_destroy.argtypes = [_p]
 _lib.s4dplr_rms_norm_fwd.restype = _i
 _lib.s4dplr_rms_norm_fwd.argtypes = [_p] * 8 + [_l] * 2 + [ctypes.c_float, _i, _p]
 _lib.s4dplr_rms_norm_workspace_bytes.restype = _i
@@ -441,7 +454,7 @@ class Plan:
 # ------------------------------------------------- token-major operators
 
 _DTYPES = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}
-DELTA_TRAINING = 1
+DELTA_TRAINING = LINEAR_ATTENTION_TRAINING = 1
 
 
 def _tensor(t, name, dtype, shape, device=None, optional=False):
@@ -735,6 +748,123 @@ def delta_bwd(plan: "DeltaPlan", q, k, v, g, beta, saved, dout, dstate_out, dq, 
              _tensor(dbeta, "dbeta", f32, heads, dev, True),
              _tensor(dstate, "dstate", f32, st, dev, True), w)
     _check(_launch(dev, stream, _lib.s4dplr_delta_bwd, args), "delta_bwd")
+
+
+class LinearAttentionPlan:
+    """A plan of linear attention with decay: ``sequences`` sequences packed into
+    ``tokens`` rows, Hk key heads of dk and Hv value heads of dv values.
+    ``training`` reserves what ``linear_attention_bwd`` needs."""
+
+    def __init__(self, sequences: int, tokens: int, Hk: int, Hv: int, dk: int, dv: int,
+                 dtype=torch.bfloat16, training: bool = False, device=None):
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype: must be float32, bfloat16 or float16, got {dtype}")
+        self.handle = 0
+        self.sequences, self.tokens, self.Hk, self.Hv = sequences, tokens, Hk, Hv
+        self.dk, self.dv, self.dtype, self.training = dk, dv, dtype, training
+        if not all(abs(n) < 1 << 31 for n in (sequences, tokens, Hk, Hv, dk, dv)):
+            raise S4DPLRError(2, "linear_attention_plan_create")      # ctypes would wrap them
+        h = _p()
+        _check(_lib.s4dplr_linear_attention_plan_create(
+            ctypes.byref(h), sequences, tokens, Hk, Hv, dk, dv, _DTYPES[dtype],
+            LINEAR_ATTENTION_TRAINING if training else 0), "linear_attention_plan_create")
+        self.handle = h.value
+        a, b = ctypes.c_size_t(), ctypes.c_size_t()
+        _check(_lib.s4dplr_linear_attention_plan_bytes(self.handle, ctypes.byref(a),
+                                                       ctypes.byref(b)),
+               "linear_attention_plan_bytes")
+        self.workspace_bytes, self.saved_bytes = a.value, b.value
+        self._keys, self._vals = (tokens, Hk, dk), (tokens, Hv, dv)
+        self._heads, self._states = (tokens, Hv), (sequences, Hv, dk, dv)
+        self._scale = dk ** -0.5
+        self.device = torch.device("cuda" if device is None else device)
+        self._ws = None
+
+    def workspace(self):
+        """A workspace tensor, one per plan object: calls that can overlap in
+        time, and graphs that can replay together, need one each."""
+        if self._ws is None:
+            self._ws = _aligned(self.workspace_bytes, self.device)
+        return self._ws
+
+    def saved(self):
+        """A new buffer for ``linear_attention_fwd(saved=...)``, one per layer and step."""
+        if not self.training:
+            raise ValueError("saved: the plan was made without training=True")
+        return _aligned(self.saved_bytes, self.device)
+
+    def close(self) -> None:
+        if self.handle:
+            _lib.s4dplr_linear_attention_plan_destroy(self.handle)
+            self.handle = 0
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+def _linear_inputs(where, plan, q, k, v, g, ws, scale, offsets, state=None, dout=None,
+                   dstate_out=None):
+    if not isinstance(plan, LinearAttentionPlan):
+        raise TypeError("pass a LinearAttentionPlan")
+    if not plan.handle:
+        raise ValueError("the plan is closed")
+    if not isinstance(v, torch.Tensor):
+        raise TypeError("v: expected a torch.Tensor")
+    fixed = isinstance(g, torch.Tensor) and g.dim() == 1
+    if validation_enabled():
+        rows, whole = dict(q=q, k=k, v=v, dout=dout), dict(state=state, dstate_out=dstate_out)
+        (whole if fixed else rows)["g"] = g
+        _validate_delta(where, plan, offsets, rows, whole)
+    dev, dt, keys = v.device, plan.dtype, plan._keys
+    off = None
+    if offsets is not None:
+        off = _tensor(offsets, "offsets", torch.int32, (plan.sequences + 1,), dev)
+    return dev, (plan.handle, *_rows(q, "q", dt, keys, dev), *_rows(k, "k", dt, keys, dev),
+                 *_rows(v, "v", dt, plan._vals, dev),
+                 _tensor(g, "g", torch.float32, (plan.Hv,) if fixed else plan._heads, dev, True),
+                 fixed, off, plan._scale if scale is None else float(scale)), \
+        _workspace(ws, "ws", plan.workspace_bytes, dev)
+
+
+def linear_attention_fwd(plan: "LinearAttentionPlan", q, k, v, g, state, o, state_out, ws,
+                         saved=None, scale=None, offsets=None, stream=None) -> None:
+    """``o`` and the states behind the last rows, from ``state`` (None: zeros).
+
+    q, k: [tokens, Hk, dk]; v, o: [tokens, Hv, dv]; g (log decay): [tokens, Hv] float32, [Hv]
+    (one decay for all tokens) or None (no decay); state, state_out: [sequences, Hv, dk, dv]
+    float32, may be one tensor, state_out may be None.  q, k, v may be column ranges of wider
+    matrices.  offsets: [sequences + 1] int32 on the GPU, or None for equal lengths.  scale: None
+    is dk ** -0.5.  saved: ``plan.saved()`` for a later ``linear_attention_bwd``."""
+    dev, args, w = _linear_inputs("linear_attention_fwd", plan, q, k, v, g, ws, scale, offsets,
+                                  state=state)
+    st, f32 = plan._states, torch.float32
+    args += (_tensor(state, "state", f32, st, dev, True),
+             _tensor(o, "o", plan.dtype, plan._vals, dev),
+             _tensor(state_out, "state_out", f32, st, dev, True),
+             None if saved is None else _workspace(saved, "saved", plan.saved_bytes, dev), w)
+    _check(_launch(dev, stream, _lib.s4dplr_linear_attention_fwd, args), "linear_attention_fwd")
+
+
+def linear_attention_bwd(plan: "LinearAttentionPlan", q, k, v, g, saved, dout, dstate_out, dq, dk,
+                         dv, dg, dstate, ws, scale=None, offsets=None, stream=None) -> None:
+    """Gradients of ``linear_attention_fwd`` with the same inputs and the ``saved`` buffer
+    it filled, from ``dout`` and ``dstate_out`` (None: zeros); any of dq, dk, dv,
+    dg (the shape of g), dstate may be None."""
+    dev, args, w = _linear_inputs("linear_attention_bwd", plan, q, k, v, g, ws, scale, offsets,
+                                  dout=dout, dstate_out=dstate_out)
+    dt, f32 = plan.dtype, torch.float32
+    st, keys, vals = plan._states, plan._keys, plan._vals
+    heads = (plan.Hv,) if isinstance(g, torch.Tensor) and g.dim() == 1 else plan._heads
+    args += (_workspace(saved, "saved", plan.saved_bytes, dev),
+             _tensor(dout, "dout", dt, vals, dev),
+             _tensor(dstate_out, "dstate_out", f32, st, dev, True),
+             _tensor(dq, "dq", dt, keys, dev, True), _tensor(dk, "dk", dt, keys, dev, True),
+             _tensor(dv, "dv", dt, vals, dev, True), _tensor(dg, "dg", f32, heads, dev, True),
+             _tensor(dstate, "dstate", f32, st, dev, True), w)
+    _check(_launch(dev, stream, _lib.s4dplr_linear_attention_bwd, args), "linear_attention_bwd")
 
 
 # ------------------------------- root-mean-square norm and 8-bit products

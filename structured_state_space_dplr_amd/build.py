@@ -18,8 +18,9 @@ CSRC = os.path.join(PKG, "csrc")
 LIB = os.path.join(PKG, "libs4dplr.so")
 SOURCES = ["kernels.hip", "big.hip", "recurrent.hip", "backward.hip", "vandermonde.hip", "block.hip",
            "noalloc.hip", "rank.hip", "norm.hip", "delta_step.hip", "delta_prep.hip",
-           "delta_scan.hip", "delta_grads.hip", "rms.hip", "quantize.hip", "matmul.hip", "api.cpp",
-           "token_api.cpp", "dense_api.cpp"]
+           "delta_scan.hip", "delta_grads.hip", "rms.hip", "quantize.hip", "matmul.hip",
+           "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip", "linear_step.hip",
+           "linear_join.hip", "api.cpp", "token_api.cpp", "dense_api.cpp", "linear_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -1,0 +1,129 @@
+// Linear attention with decay: the plan, the layout of its buffers and the launchers.
+#pragma once
+
+#include <hip/hip_runtime_api.h>
+
+#include <cstddef>
+
+#include "s4dplr.h"
+
+struct s4dplr_linear_attention_plan {
+  int sequences;
+  long tokens;
+  int each;     // tokens / sequences
+  int Hk, Hv, dk, dv;
+  int dtype;
+  bool training;
+  // Sequences of more than `segment` rows are cut into segments of so many, each a block's
+  // work; the states between them have slots.  Segments of sequence s are slots
+  //   floor(start / segment) + min(s, floor(start / (segment + 1)))
+  // and on, disjoint for any lengths (a long sequence has one more segment than it has whole
+  // ones at most), and fewer than `slots`.
+  int segment;
+  long slots;
+  // Workspace, byte offsets.
+  size_t off_states;           // [slot][Hv] states: before each segment, backward behind it
+  size_t off_decay;            // [slot][Hv] float: the segment's whole decay
+  size_t off_dots, off_dotk;   // backward: [dot_parts][Hv][tokens] parts of q . dq and of k . dk
+  size_t off_edge;             // backward: [sequences + slots][Hv][dot_parts] parts of <S, dS> before
+  size_t off_dgsum;            // backward: [sequences + slots][Hv] sums of dg over a segment
+  size_t off_dq, off_dk;       // backward, Hv > Hk: [tokens][Hv][dk] float
+  size_t total;
+  // saved (training): [slot][Hv] states before each segment, [sequences][Hv] states before
+  // sequences of one segment
+  size_t off_first;
+  size_t saved_total;
+};
+
+namespace s4 {
+
+constexpr int kLinChunk = 64;    // tokens a chunk
+constexpr int kDotParts = 16;    // waves that share the columns of a head, at most
+
+// Longest sequence that is taken token by token.
+inline int lin_step_limit(const s4dplr_linear_attention_plan*) { return 8; }
+
+struct LinRows {
+  long start, len;
+  constexpr long slot(int s, int segment) const {
+    const long before = start / (segment + 1);
+    return start / segment + (s < before ? s : before);
+  }
+  constexpr int segments(int segment) const { return (int)((len + segment - 1) / segment); }
+};
+
+// One pass of the recurrence
+//   out_t = read (decay to t) S^T x_t + pair sum_{j <= t} (decay from j to t) (x_t . y_j) w_j,
+//   S <- (decay) S + update sum_j (decay from j) y_j w_j^T
+// over all sequences, forwards or (rev) from their ends.  The forward pass and the three
+// gradients are this pass with their tensors in other places.
+struct LinPass {
+  const void *x, *y, *w;
+  long ldx, ldy, ldw;             // elements from one row to the next
+  int gx, gy, gw;                 // value heads that share a head of x, y, w
+  int dx, dw;
+  void* out;                      // [tokens][Hv][dw]
+  int out_f32;                    // out is float, not the tensors' type
+  const float* g;                 // NULL: no decay
+  long ldg;                       // Hv, or 0: one decay a head
+  const int* offsets;
+  const float* first;             // states before the first rows, NULL: zeros
+  const float* before;            // [slot] states before the segments
+  float* last;                    // states behind the last rows, may be NULL
+  float* copy;                    // [sequences] states before sequences of one segment, may be NULL
+  long rs, cs;                    // a state's element (row of dx, column of dw) is at rs row + cs column
+  float read, pair, update;
+  int rev;
+  // sums over the columns of out times `dot`, by waves: [part][Hv][tokens]; may be NULL
+  const void* dot;
+  long lddot;
+  int gdot;
+  float* dot_out;
+  // sums of the state behind a segment times the saved one; may be NULL
+  const float *edge_first, *edge_slots;
+  float* edge_out;                // [sequences + slots][Hv][kDotParts]
+  float* states;                  // the sums' pass: [slot] what each segment adds
+  float* decay;                   // [slot][Hv]
+  int sequences, each, Hv, dk, dv, segment;
+  long tokens, slots;
+  int step_tokens;                // sequences of at most so many rows are not this pass's
+};
+
+struct LinStep {
+  const void *q, *k, *v;
+  long ldq, ldk, ldv;
+  const float* g;
+  long ldg;
+  const int* offsets;
+  float scale;
+  const float* state;
+  void* o;
+  float* state_out;
+  int sequences, each, Hk, Hv, dk, dv, step_tokens;
+  long tokens;
+};
+
+hipError_t launch_linear_steps(const LinStep& a, int dtype, hipStream_t s);
+// What the segments add to the states, then (scan) the states before them.
+hipError_t launch_linear_sums(const LinPass& a, int dtype, hipStream_t s);
+hipError_t launch_linear_pass(const LinPass& a, int dtype, hipStream_t s);
+// out [tokens][Hk][d] = the sums over each group of heads of part [tokens][Hv][d], in the
+// sequences' rows.
+hipError_t launch_linear_groups(const float* part, void* out, const int* offsets, int sequences,
+                                long tokens, int Hk, int Hv, int d, int dtype, hipStream_t s);
+// dg from the passes' dots and edges; dg is [tokens][Hv] or (ldg == 0) [Hv].
+struct LinGates {
+  const float *dots, *dotk, *edge;
+  int parts_q, parts_k, parts_edge;
+  float *dg, *sums;
+  const float* g;
+  long ldg;
+  const int* offsets;
+  int sequences, each, Hv, segment;
+  long tokens, slots;
+};
+hipError_t launch_linear_gates(const LinGates& a, hipStream_t s);
+// Waves that share the columns of a pass with these sizes.
+int linear_parts(int dx, int dw, int dtype);
+
+}  // namespace s4

@@ -1,0 +1,19 @@
+// Linear attention's chunked pass for bf16 tensors.
+#include "linear_pass.h"
+
+namespace s4 {
+
+hipError_t linear_pass_bf16(const LinPass& a, bool sum, hipStream_t s) {
+  return sum ? linear_launch<bf16, 1, true>(a, s) : linear_launch<bf16, 1, false>(a, s);
+}
+
+int linear_parts_bf16(int dx, int dw) {
+  int parts = 0;
+  linear_shape<1>(dx, dw, [&](auto, auto cw, auto) {
+    constexpr int COLS = 4 * decltype(cw)::value;
+    parts = (dw + COLS - 1) / COLS * 4;
+  });
+  return parts;
+}
+
+}  // namespace s4

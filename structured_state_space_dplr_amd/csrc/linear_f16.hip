@@ -1,0 +1,19 @@
+// Linear attention's chunked pass for f16 tensors.
+#include "linear_pass.h"
+
+namespace s4 {
+
+hipError_t linear_pass_f16(const LinPass& a, bool sum, hipStream_t s) {
+  return sum ? linear_launch<f16, 2, true>(a, s) : linear_launch<f16, 2, false>(a, s);
+}
+
+int linear_parts_f16(int dx, int dw) {
+  int parts = 0;
+  linear_shape<2>(dx, dw, [&](auto, auto cw, auto) {
+    constexpr int COLS = 4 * decltype(cw)::value;
+    parts = (dw + COLS - 1) / COLS * 4;
+  });
+  return parts;
+}
+
+}  // namespace s4

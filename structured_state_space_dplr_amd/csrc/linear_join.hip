@@ -1,0 +1,190 @@
+// Linear attention: what joins the blocks of a pass.  The states before the segments from what
+// the segments add, the gradients of shared heads, and the gradient of the decays.
+#include "linear_device.h"
+
+namespace s4 {
+
+namespace {
+
+// Per sequence of several segments and head, element by element: from the state before the first
+// segment (rev: behind the last), slot m takes the state before segment m (behind it),
+//   run <- decay_m run + added_m.
+// Bound by the states' read and write; the next slots' loads go ahead of the sums.
+__global__ __launch_bounds__(256) void linear_scan_kernel(const LinPass p) {
+  const int s = blockIdx.x / p.Hv, h = blockIdx.x % p.Hv;
+  const LinRows r = lin_rows(p, s);
+  if (r.len <= p.segment) return;
+  const long sz = (long)p.dk * p.dv, at = (long)blockIdx.y * 256 + threadIdx.x;
+  if (at >= sz) return;
+  const long base = r.slot(s, p.segment);
+  int n = r.segments(p.segment);
+  if (base + n > p.slots) n = (int)(p.slots - base);
+  float run = p.first ? p.first[((size_t)s * p.Hv + h) * sz + at] : 0.f;
+  constexpr int AHEAD = 8;
+  for (int m0 = 0; m0 < n; m0 += AHEAD) {
+    float add[AHEAD], dec[AHEAD];
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int m = m0 + i < n ? m0 + i : n - 1;
+      const size_t slot = (size_t)(base + (p.rev ? n - 1 - m : m)) * p.Hv + h;
+      add[i] = p.states[slot * sz + at];
+      dec[i] = p.decay[slot];
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
+      const int m = m0 + i;
+      if (m >= n) break;
+      const size_t slot = (size_t)(base + (p.rev ? n - 1 - m : m)) * p.Hv + h;
+      p.states[slot * sz + at] = run;
+      run = fmaf(dec[i], run, add[i]);   // behind the last one: not used
+    }
+  }
+}
+
+template <typename T>
+__global__ __launch_bounds__(256) void linear_groups_kernel(const float* __restrict__ part,
+                                                            T* __restrict__ out,
+                                                            const int* __restrict__ offsets,
+                                                            int sequences, long tokens, int Hk,
+                                                            int group, int d) {
+  // the rows of the sequences, which lie one behind the other
+  long lo = 0, hi = tokens;
+  if (offsets) {
+    const Rows r = clamp_rows((int)tokens, offsets[0], offsets[sequences]);
+    lo = r.start;
+    hi = r.start + r.len;
+  }
+  const long n = hi * Hk * d;
+  for (long at = lo * Hk * d + (long)blockIdx.x * 256 + threadIdx.x; at < n; at += (long)gridDim.x * 256) {
+    const long row = at / d, c = at % d;   // row: token and key head
+    const float* from = part + row * group * d + c;
+    float s = from[0];
+    for (int i = 1; i < group; ++i) s += from[(long)i * d];
+    out[at] = from_f32<T>(s);
+  }
+}
+
+// dg_t = <S_{t-1}, gradient of S_{t-1} by what comes later>: the edge before the segment, and
+// behind token i  + k_i . dk_i - q_i . dq_i  of the token itself.  The sums are held in 64 bits
+// over a segment of a few hundred tokens.  One wave per segment and head.  Where exp(g) is 0
+// nothing of the state before is left, and dg is 0.
+__global__ __launch_bounds__(64) void linear_gates_kernel(const LinGates a) {
+  const int lane = threadIdx.x, h = blockIdx.y;
+  LinItem it;
+  const long skip = a.offsets || a.each <= a.segment ? 0 : a.sequences;
+  const long item = skip + blockIdx.x;
+  if (!lin_item(a, item, &it)) {
+    if (lane == 0 && a.ldg == 0) a.sums[item * a.Hv + h] = 0.f;
+    return;
+  }
+  double run = 0.0, total = 0.0;
+  if (it.len > 0)
+    for (int i = 0; i < a.parts_edge; ++i) run += a.edge[(item * a.Hv + h) * kDotParts + i];
+  for (int t0 = 0; t0 < it.len; t0 += 64) {
+    const bool in = t0 + lane < it.len;
+    const long tok = it.start + t0 + lane;
+    double own = 0.0;
+    float g = 0.f;
+    if (in) {
+      for (int i = 0; i < a.parts_k; ++i) own += a.dotk[((size_t)i * a.Hv + h) * a.tokens + tok];
+      for (int i = 0; i < a.parts_q; ++i) own -= a.dots[((size_t)i * a.Hv + h) * a.tokens + tok];
+      g = a.g[tok * a.ldg + h];
+    }
+    double x = own;
+#pragma unroll
+    for (int off = 1; off < 64; off <<= 1) {
+      const double y = __shfl_up(x, off);
+      if (lane >= off) x += y;
+    }
+    const double dg = expf(g) == 0.f ? 0.0 : run + (x - own);
+    if (in && a.ldg) a.dg[tok * a.Hv + h] = (float)dg;
+    total += in ? dg : 0.0;
+    run += __shfl(x, 63);
+  }
+  if (a.ldg == 0) {
+#pragma unroll
+    for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off);
+    if (lane == 0) a.sums[item * a.Hv + h] = (float)total;
+  }
+}
+
+// dg of one decay a head: the items' sums, always in the same order.
+__global__ __launch_bounds__(256) void linear_gate_sums_kernel(const float* __restrict__ sums,
+                                                               long first, long last, int Hv,
+                                                               float* __restrict__ dg) {
+  __shared__ double red[256];
+  const int h = blockIdx.x;
+  double s = 0.0;
+  for (long i = first + threadIdx.x; i < last; i += 256) s += sums[i * Hv + h];
+  red[threadIdx.x] = s;
+  __syncthreads();
+  if (threadIdx.x >= 64) return;
+  s = (red[threadIdx.x] + red[threadIdx.x + 64]) + (red[threadIdx.x + 128] + red[threadIdx.x + 192]);
+#pragma unroll
+  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
+  if (threadIdx.x == 0) dg[h] = (float)s;
+}
+
+}  // namespace
+
+hipError_t linear_pass_bf16(const LinPass& a, bool sum, hipStream_t s);
+hipError_t linear_pass_f16(const LinPass& a, bool sum, hipStream_t s);
+hipError_t linear_pass_f32(const LinPass& a, bool sum, hipStream_t s);
+int linear_parts_bf16(int dx, int dw);
+int linear_parts_f16(int dx, int dw);
+int linear_parts_f32(int dx, int dw);
+
+namespace {
+hipError_t pass(const LinPass& a, bool sum, int dtype, hipStream_t s) {
+  return dtype == S4DPLR_F32 ? linear_pass_f32(a, sum, s)
+         : dtype == S4DPLR_BF16 ? linear_pass_bf16(a, sum, s) : linear_pass_f16(a, sum, s);
+}
+}  // namespace
+
+int linear_parts(int dx, int dw, int dtype) {
+  return dtype == S4DPLR_F32 ? linear_parts_f32(dx, dw)
+         : dtype == S4DPLR_BF16 ? linear_parts_bf16(dx, dw) : linear_parts_f16(dx, dw);
+}
+
+hipError_t launch_linear_pass(const LinPass& a, int dtype, hipStream_t s) {
+  return pass(a, false, dtype, s);
+}
+
+hipError_t launch_linear_sums(const LinPass& a, int dtype, hipStream_t s) {
+  if (a.slots == 0 || (!a.offsets && a.each <= a.segment)) return hipSuccess;   // one segment each
+  const hipError_t e = pass(a, true, dtype, s);
+  if (e != hipSuccess) return e;
+  const long sz = (long)a.dk * a.dv;
+  linear_scan_kernel<<<dim3((unsigned)(a.sequences * a.Hv), (unsigned)((sz + 255) / 256)), 256, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_groups(const float* part, void* out, const int* offsets, int sequences,
+                                long tokens, int Hk, int Hv, int d, int dtype, hipStream_t s) {
+  const long n = tokens * Hk * d;
+  if (n == 0) return hipSuccess;
+  const long blocks = (n + 255) / 256;
+  const unsigned grid = (unsigned)(blocks < (1 << 16) ? blocks : 1 << 16);
+  if (dtype == S4DPLR_F32)
+    linear_groups_kernel<float><<<grid, 256, 0, s>>>(part, (float*)out, offsets, sequences, tokens, Hk,
+                                                   Hv / Hk, d);
+  else if (dtype == S4DPLR_BF16)
+    linear_groups_kernel<bf16><<<grid, 256, 0, s>>>(part, (bf16*)out, offsets, sequences, tokens, Hk,
+                                                   Hv / Hk, d);
+  else
+    linear_groups_kernel<f16><<<grid, 256, 0, s>>>(part, (f16*)out, offsets, sequences, tokens, Hk,
+                                                   Hv / Hk, d);
+  return hipGetLastError();
+}
+
+hipError_t launch_linear_gates(const LinGates& a, hipStream_t s) {
+  const bool all_long = !a.offsets && a.each > a.segment, all_short = !a.offsets && !all_long;
+  const long first = all_long ? a.sequences : 0, last = all_short ? a.sequences : a.sequences + a.slots;
+  if (last > first)
+    linear_gates_kernel<<<dim3((unsigned)(last - first), (unsigned)a.Hv), 64, 0, s>>>(a);
+  if (a.ldg == 0)
+    linear_gate_sums_kernel<<<dim3((unsigned)a.Hv), 256, 0, s>>>(a.sums, first, last, a.Hv, a.dg);
+  return hipGetLastError();
+}
+
+}  // namespace s4

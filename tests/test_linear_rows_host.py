@@ -1,0 +1,28 @@
+"""CPU test: where linear attention looks for a sequence's segments and their slots
+(csrc/linear.h, which the kernels use as it is), built with g++ under the undefined-behaviour
+sanitizer and driven with rising, falling, negative and extreme offsets
+(tests/host/linear_rows.cpp)."""
+import os
+import shutil
+import subprocess
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+CSRC = os.path.join(ROOT, "structured_state_space_dplr_amd", "csrc")
+HOST = os.path.join(ROOT, "tests", "host")
+
+
+@pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
+                    reason="needs g++ and the ROCm headers")
+def test_segments_and_slots(tmp_path):
+    exe = str(tmp_path / "rows")
+    cmd = ["g++", "-std=c++17", "-O1", "-g", "-fsanitize=undefined", "-fno-sanitize-recover=all",
+           "-D__HIP_PLATFORM_AMD__", "-I", os.path.join(ROOT, "include"), "-I", CSRC,
+           "-I", "/opt/rocm/include", os.path.join(CSRC, "linear_api.cpp"),
+           os.path.join(HOST, "linear_rows.cpp"), "-o", exe]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    assert res.returncode == 0, res.stderr[-4000:]
+    run = subprocess.run([exe], capture_output=True, text=True, timeout=300)
+    assert run.returncode == 0, (run.stdout + run.stderr)[-4000:]
+    assert "ok" in run.stdout
