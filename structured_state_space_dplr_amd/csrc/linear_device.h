@@ -43,8 +43,12 @@ struct LinItem {
   long slot, start;
   int len;
 };
+__device__ __forceinline__ long uniform(long v) {
+  return (long)(unsigned)__builtin_amdgcn_readfirstlane((int)v) |
+         (long)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;
+}
 template <typename A>
-__device__ __forceinline__ bool lin_item(const A& p, long item, LinItem* w) {
+__device__ __forceinline__ bool find_item(const A& p, long item, LinItem* w) {
   if (item < p.sequences) {
     const LinRows r = lin_rows(p, (int)item);
     if (r.len > p.segment) return false;
@@ -61,6 +65,17 @@ __device__ __forceinline__ bool lin_item(const A& p, long item, LinItem* w) {
   const long left = r.len - m * p.segment;
   *w = LinItem{s, (int)m, of, slot, r.start + m * p.segment, (int)(left < p.segment ? left : p.segment)};
   return true;
+}
+
+// The item's rows, known to be the same for all lanes.
+template <typename A>
+__device__ __forceinline__ bool lin_item(const A& p, long item, LinItem* w) {
+  LinItem t = {};
+  const bool found = find_item(p, item, &t);
+  *w = LinItem{__builtin_amdgcn_readfirstlane(t.s), __builtin_amdgcn_readfirstlane(t.m),
+               __builtin_amdgcn_readfirstlane(t.of), uniform(t.slot), uniform(t.start),
+               __builtin_amdgcn_readfirstlane(t.len)};
+  return __builtin_amdgcn_readfirstlane(found) != 0;
 }
 
 }  // namespace s4

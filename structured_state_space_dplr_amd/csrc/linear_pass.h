@@ -17,71 +17,98 @@
 
 namespace s4 {
 
-// Eight elements of a row on their way.  WHOLE: rows have a multiple of 8 elements.  Columns
-// behind d come from the row's start and are not used.
+// Eight elements of a row on their way, `at` bytes behind `base` (uniform).  WHOLE: rows have a
+// multiple of 8 elements.  Columns behind d come from the row's start and are not used.
 template <typename T, bool WHOLE>
-__device__ __forceinline__ void fetch8(const T* __restrict__ row, int col, int d, T (&t)[8]) {
+__device__ __forceinline__ void fetch8(const unsigned char* __restrict__ base, unsigned at, int col,
+                                       int d, T (&t)[8]) {
   if constexpr (WHOLE) {
-    __builtin_memcpy(t, row + (col < d ? col : 0), sizeof(t));
+    __builtin_memcpy(t, base + (at + (col < d ? col : 0) * (unsigned)sizeof(T)), sizeof(t));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = row[col + i < d ? col + i : 0];
+    for (int i = 0; i < 8; ++i)
+      __builtin_memcpy(&t[i], base + (at + (col + i < d ? col + i : 0) * (unsigned)sizeof(T)), sizeof(T));
   }
 }
 
 // A tile of C rows x COLS columns of a tensor's head, on its way to LDS.
 template <typename T, int PARTS, int C, int COLS, bool WHOLE>
 struct LinTile {
-  static constexpr int LD = COLS + 8, N = C * COLS / 8 / 256;
+  static constexpr int LD = COLS + 8, N = C * COLS / 8 / 256, STEP = 256 / (COLS / 8);
   static_assert(N * 256 * 8 == C * COLS, "");
   T v[N][8];
-  // rows t0 .. t0 + n of the tensor; in reverse with rev
-  __device__ __forceinline__ void fetch(const void* p, long ld, long head, long t0, int n, int rev,
-                                        int c0, int d) {
+  // `n` rows from `base` on, ld elements apart (64 rows of less than 2^24 elements: offsets of
+  // 32 bits), in reverse with rev; columns c0 and on
+  __device__ __forceinline__ void fetch(const unsigned char* base, unsigned ld, int n, int rev, int c0,
+                                        int d) {
+    const int r0 = threadIdx.x / (COLS / 8), c = c0 + threadIdx.x % (COLS / 8) * 8;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + threadIdx.x, r = at / (COLS / 8), c = c0 + at % (COLS / 8) * 8;
-      int row = rev ? n - 1 - r : r;
-      row = row < 0 ? 0 : row < n ? row : n - 1;   // behind the end: a row that is there, unused
-      fetch8<T, WHOLE>((const T*)p + (t0 + row) * ld + head, c, d, v[i]);
+      int row = r0 + i * STEP;
+      row = row < n ? row : n - 1;   // behind the end: a row that is there, unused
+      row = rev ? n - 1 - row : row;
+      fetch8<T, WHOLE>(base, (unsigned)row * (ld * (unsigned)sizeof(T)), c, d, v[i]);
     }
   }
   __device__ __forceinline__ void stage(__bf16 (*to)[C][LD], int n, int c0, int d) const {
+    const int r0 = threadIdx.x / (COLS / 8), c = threadIdx.x % (COLS / 8) * 8;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int at = i * 256 + threadIdx.x, r = at / (COLS / 8), c = at % (COLS / 8) * 8;
-      float x[8];
+      const int r = r0 + i * STEP;
+      if constexpr (WHOLE && sizeof(T) == 2 && PARTS == 1) {
+        v8bf x;
+        __builtin_memcpy(&x, v[i], 16);
+        typedef int v4i __attribute__((ext_vector_type(4)));
+        v4i y;
+        __builtin_memcpy(&y, v[i], 16);
+        y = r < n && c0 + c < d ? y : v4i{0, 0, 0, 0};
+        *reinterpret_cast<v4i*>(&to[0][r][c]) = y;
+      } else {
+        float x[8];
 #pragma unroll
-      for (int j = 0; j < 8; ++j) x[j] = r < n && c0 + c + j < d ? to_f32(v[i][j]) : 0.f;
-      v8bf parts[PARTS];
-      split8<PARTS>(x, parts);
+        for (int j = 0; j < 8; ++j)
+          x[j] = r < n && c0 + c + (WHOLE ? 0 : j) < d ? to_f32(v[i][j]) : 0.f;
+        v8bf parts[PARTS];
+        split8<PARTS>(x, parts);
 #pragma unroll
-      for (int q = 0; q < PARTS; ++q) *reinterpret_cast<v8bf*>(&to[q][r][c]) = parts[q];
+        for (int q = 0; q < PARTS; ++q) *reinterpret_cast<v8bf*>(&to[q][r][c]) = parts[q];
+      }
     }
   }
 };
 
 // A head's state: row 4 g + e of tile t is row 32 (t / 2) + 8 g + 4 (t % 2) + e of dx, g = lane / 16.
-template <int TILES, int CT, typename F>
-__device__ __forceinline__ void each_state(int col0, int dx, int dw, long rs, long cs, F f) {
+template <int TILES, int CT>
+__device__ __forceinline__ void store_state(float* __restrict__ to, int col0, int dx, int dw, int rs,
+                                            int cs, const v4f (&S)[TILES][CT]) {
   const int lr = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
 #pragma unroll
-  for (int t = 0; t < TILES; ++t)
+  for (int c = 0; c < CT; ++c) {
+    const int col = col0 + 16 * c + lr;
+    if (col >= dw) continue;
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int row = 32 * (t >> 1) + 8 * lg + 4 * (t & 1), col = col0 + 16 * c + lr;
-      const long at = row * rs + col * cs;
-      const bool in = col < dw;
+    for (int t = 0; t < TILES; ++t) {
+      const int row = 32 * (t >> 1) + 8 * lg + 4 * (t & 1);
+      float* at = to + (row * rs + col * cs);
+      if (row + 4 <= dx) {
+        if (rs == 1) {
+          __builtin_memcpy(at, &S[t][c], 16);
+        } else {
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
-        if (in && row + e < dx) f(t, c, e, at + e * rs);
+          for (int e = 0; e < 4; ++e) at[e * rs] = S[t][c][e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 3; ++e)
+          if (row + e < dx) at[e * rs] = S[t][c][e];
+      }
     }
+  }
 }
-
-// The same for a state that is read: no load under a condition, 0 where there is none.
+// Read without a load under a condition: 0 where there is none.
 template <int TILES, int CT>
 __device__ __forceinline__ void load_state(const float* __restrict__ from, int col0, int dx, int dw,
-                                           long rs, long cs, v4f (&S)[TILES][CT]) {
+                                           int rs, int cs, v4f (&S)[TILES][CT]) {
   const int lr = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
 #pragma unroll
   for (int t = 0; t < TILES; ++t)
@@ -97,10 +124,13 @@ __device__ __forceinline__ void load_state(const float* __restrict__ from, int c
     }
 }
 
-template <typename T, int PARTS, int DX, int CW, int C, bool WHOLE, bool SUM>
+enum { kSum, kOut, kGrad };   // what a segment adds; a pass; a pass with `dot` and out in float
+
+template <typename T, int PARTS, int DX, int CW, int C, bool WHOLE, int MODE>
 __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_pass_kernel(
     const LinPass p) {
   constexpr int TILES = DX / 16, CT = CW / 16, KS = DX / 32, RT = C / 16, COLS = 4 * CW;
+  constexpr bool SUM = MODE == kSum;
   using XTile = LinTile<T, PARTS, C, DX, WHOLE>;
   using WTile = LinTile<T, PARTS, C, COLS, WHOLE>;
   __shared__ __attribute__((aligned(16))) __bf16 ys[PARTS][C][DX + 8];
@@ -114,19 +144,21 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
   const int lr = lane & 15, lg = lane >> 4;
   const int slices = (p.dw + COLS - 1) / COLS;
   // blocks go round robin over the 8 XCDs; the slices of a head share one
-  const int g8 = blockIdx.x >> 3, slice = g8 % slices;
-  const long unit = (long)(g8 / slices) * 8 + (blockIdx.x & 7);
+  const unsigned g8 = blockIdx.x >> 3;
+  const int slice = g8 % slices;
+  const unsigned unit = g8 / slices * 8 + (blockIdx.x & 7);
   // items to be found: all sequences, or slots alone
   const long skip = p.offsets || p.each <= p.segment ? (SUM ? p.sequences : 0) : p.sequences;
-  const int h = (int)(unit % p.Hv);
+  const int h = unit % p.Hv;
   LinItem it;
   if (!lin_item(p, skip + unit / p.Hv, &it)) return;
   if (it.of == 0 && it.len <= p.step_tokens) return;
   // the segment that is processed last has nobody to add to
   if (SUM && (p.rev ? it.m == 0 : it.m == it.of - 1)) return;
-  const int chunks = (it.len + C - 1) / C;
+  const int len = it.len, chunks = (len + C - 1) / C;
   const int col0 = slice * COLS + w * CW;
   const size_t sz = (size_t)p.dk * p.dv;
+  const int rs = (int)p.rs, cs = (int)p.cs;
 
   v4f S[TILES][CT];
 #pragma unroll
@@ -136,40 +168,40 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
   if constexpr (!SUM) {
     const float* from = it.of ? p.before + ((size_t)it.slot * p.Hv + h) * sz
                               : p.first ? p.first + ((size_t)it.s * p.Hv + h) * sz : nullptr;
-    if (from) load_state(from, col0, p.dx, p.dw, p.rs, p.cs, S);
-    if (p.copy && !it.of) {
-      float* to = p.copy + ((size_t)it.s * p.Hv + h) * sz;
-      each_state<TILES, CT>(col0, p.dx, p.dw, p.rs, p.cs,
-                            [&](int t, int c, int e, long at) { to[at] = S[t][c][e]; });
-    }
+    if (from) load_state(from, col0, p.dx, p.dw, rs, cs, S);
+    if (p.copy && !it.of)
+      store_state(p.copy + ((size_t)it.s * p.Hv + h) * sz, col0, p.dx, p.dw, rs, cs, S);
   }
 
   XTile xr, yr;
   WTile wr;
   float gr = 0.f;
   double all = 0.0;   // the segment's decay
-  const long hx = (long)(h / p.gx) * p.dx, hy = (long)(h / p.gy) * p.dx, hw = (long)(h / p.gw) * p.dw;
-  // rows of chunk i of this pass's order
-  auto rows_at = [&](int i, long* t0) {
-    const int c = p.rev ? chunks - 1 - i : i;
-    *t0 = it.start + (long)c * C;
-    return it.len - c * C < C ? it.len - c * C : C;
-  };
+  // the head's columns in the segment's first row
+  typedef const unsigned char* Bytes;
+  const Bytes xb = (Bytes)p.x + (it.start * p.ldx + (long)(h / p.gx) * p.dx) * (long)sizeof(T);
+  const Bytes yb = (Bytes)p.y + (it.start * p.ldy + (long)(h / p.gy) * p.dx) * (long)sizeof(T);
+  const Bytes wb = (Bytes)p.w + (it.start * p.ldw + (long)(h / p.gw) * p.dw) * (long)sizeof(T);
+  const float* gb = p.g ? p.g + it.start * p.ldg + h : nullptr;
+  const long ldo = (long)p.Hv * p.dw;
+  // first row and number of rows of chunk i of this pass's order
+  auto first_of = [&](int i) { return (p.rev ? chunks - 1 - i : i) * C; };
+  auto rows_of = [&](int c0) { return len - c0 < C ? len - c0 : C; };
   auto fetch = [&](int i) {
-    long t0;
-    const int n = rows_at(i, &t0);
-    if constexpr (!SUM) xr.fetch(p.x, p.ldx, hx, t0, n, p.rev, 0, p.dx);
-    yr.fetch(p.y, p.ldy, hy, t0, n, p.rev, 0, p.dx);
-    wr.fetch(p.w, p.ldw, hw, t0, n, p.rev, slice * COLS, p.dw);
-    if (w == 0) {
-      const int row = p.rev ? n - 1 - lane : lane;
-      gr = p.g && lane < n ? p.g[(t0 + row) * p.ldg + h] : 0.f;
+    const int c0 = first_of(i), n = rows_of(c0);
+    if constexpr (!SUM)
+      xr.fetch(xb + c0 * (p.ldx * (long)sizeof(T)), (unsigned)p.ldx, n, p.rev, 0, p.dx);
+    yr.fetch(yb + c0 * (p.ldy * (long)sizeof(T)), (unsigned)p.ldy, n, p.rev, 0, p.dx);
+    wr.fetch(wb + c0 * (p.ldw * (long)sizeof(T)), (unsigned)p.ldw, n, p.rev, slice * COLS, p.dw);
+    if (w == 0 && gb) {
+      const int row = lane < n ? p.rev ? n - 1 - lane : lane : 0;
+      gr = gb[(c0 + row) * p.ldg];
+      gr = lane < n ? gr : 0.f;
     }
   };
   if (chunks > 0) fetch(0);
   for (int i = 0; i < chunks; ++i) {
-    long t0;
-    const int n = rows_at(i, &t0);
+    const int c0 = first_of(i), n = rows_of(c0);
     if (w == 0) {
       // decays as powers of two, summed in 64 bits, so that a difference keeps its digits behind
       // a large negative g (a reset); below -200 the decay is 0 in fp32 either way
@@ -320,50 +352,53 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
       }
     }
     if constexpr (!SUM) {
-      const T* dp = (const T*)p.dot;
+      // rows of out of this chunk: base (uniform) and offsets of 32 bits
+      const long tok0 = it.start + c0;
+      const unsigned wide = MODE == kGrad && p.out_f32 ? 4 : sizeof(T);
+      unsigned char* ob = (unsigned char*)p.out + (tok0 * ldo + (long)h * p.dw) * wide;
+      const Bytes db = MODE == kGrad
+          ? (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T) : nullptr;
+      float* to = MODE == kGrad && p.dot
+          ? p.dot_out + ((size_t)(slice * 4 + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
-        const int row = 16 * r + lr;
-        const long tok = t0 + (p.rev ? n - 1 - row : row);
+        const int i = 16 * r + lr, row = p.rev ? n - 1 - i : i;
         float sum = 0.f;
-        if (row < n) {
-          const long at = (tok * p.Hv + h) * p.dw;
+        if (i < n) {
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
             const int col = col0 + 16 * c + 4 * lg;
             const v4f o = O[r][c];
-            if (col + 4 <= p.dw) {
-              if (p.out_f32) {
-                __builtin_memcpy((float*)p.out + at + col, &o, 16);
-              } else if (p.out) {
+            auto put = [&](int e0, int m) {   // columns e0 .. e0 + m of the four
+              unsigned char* q = ob + ((unsigned)row * ((unsigned)ldo * wide) + (col + e0) * wide);
+              if (MODE == kGrad && p.out_f32) {
+                __builtin_memcpy(q, (const float*)&o + e0, 4 * m);
+              } else if (MODE == kOut || p.out) {
                 T t[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
-                __builtin_memcpy((T*)p.out + at + col, t, sizeof(t));
+                __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if (dp) {
+              if (MODE == kGrad && p.dot) {
                 T t[4];
-                __builtin_memcpy(t, dp + tok * p.lddot + (long)(h / p.gdot) * p.dw + col, sizeof(t));
-#pragma unroll
-                for (int e = 0; e < 4; ++e) sum = fmaf(o[e], to_f32(t[e]), sum);
+                __builtin_memcpy(t, db + ((unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T)) +
+                                          (col + e0) * (unsigned)sizeof(T)), sizeof(T) * m);
+                for (int e = 0; e < m; ++e) sum = fmaf(o[e0 + e], to_f32(t[e]), sum);
               }
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e) {
-                if (col + e >= p.dw) continue;
-                if (p.out_f32) ((float*)p.out)[at + col + e] = o[e];
-                else if (p.out) ((T*)p.out)[at + col + e] = from_f32<T>(o[e]);
-                if (dp)
-                  sum = fmaf(o[e], to_f32(dp[tok * p.lddot + (long)(h / p.gdot) * p.dw + col + e]), sum);
-              }
+            };
+            if (col + 4 <= p.dw) {
+              put(0, 4);
+            } else if constexpr (!WHOLE) {
+              if (col < p.dw) put(0, 1);
+              if (col + 1 < p.dw) put(1, 1);
+              if (col + 2 < p.dw) put(2, 1);
             }
           }
         }
-        if (dp) {   // over the lanes that share the row
+        if (MODE == kGrad && p.dot) {   // over the lanes that share the row
           sum += __shfl_xor(sum, 16);
           sum += __shfl_xor(sum, 32);
-          if (lg == 0 && row < n)
-            p.dot_out[((size_t)(slice * 4 + w) * p.Hv + h) * p.tokens + tok] = sum;
+          if (lg == 0 && i < n) to[row] = sum;
         }
       }
     }
@@ -371,21 +406,16 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
   }
 
   if constexpr (SUM) {
-    float* to = p.states + ((size_t)it.slot * p.Hv + h) * sz;
-    each_state<TILES, CT>(col0, p.dx, p.dw, p.rs, p.cs,
-                          [&](int t, int c, int e, long at) { to[at] = S[t][c][e]; });
+    store_state(p.states + ((size_t)it.slot * p.Hv + h) * sz, col0, p.dx, p.dw, rs, cs, S);
     if (threadIdx.x == 0 && slice == 0) p.decay[(size_t)it.slot * p.Hv + h] = exp_diff(all);
   } else {
-    if (p.last && (it.of == 0 || (p.rev ? it.m == 0 : it.m == it.of - 1))) {
-      float* to = p.last + ((size_t)it.s * p.Hv + h) * sz;
-      each_state<TILES, CT>(col0, p.dx, p.dw, p.rs, p.cs,
-                            [&](int t, int c, int e, long at) { to[at] = S[t][c][e]; });
-    }
-    if (p.edge_out) {
+    if (p.last && (it.of == 0 || (p.rev ? it.m == 0 : it.m == it.of - 1)))
+      store_state(p.last + ((size_t)it.s * p.Hv + h) * sz, col0, p.dx, p.dw, rs, cs, S);
+    if (MODE == kOut && p.edge_out) {
       const float* with = it.of ? p.edge_slots + ((size_t)it.slot * p.Hv + h) * sz
                                 : p.edge_first + ((size_t)it.s * p.Hv + h) * sz;
       v4f other[TILES][CT];
-      load_state(with, col0, p.dx, p.dw, p.rs, p.cs, other);
+      load_state(with, col0, p.dx, p.dw, rs, cs, other);
       float sum = 0.f;
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
@@ -421,19 +451,19 @@ void linear_shape(int dx, int dw, F f) {
 #undef S4_CASE
 }
 
-template <typename T, int PARTS, bool SUM>
+template <typename T, int PARTS, int MODE>
 hipError_t linear_launch(const LinPass& a, hipStream_t s) {
   const bool all_long = !a.offsets && a.each > a.segment, all_short = !a.offsets && !all_long;
-  const long items = (all_long || SUM ? 0 : a.sequences) + (all_short ? 0 : a.slots);
+  const long items = (all_long || MODE == kSum ? 0 : a.sequences) + (all_short ? 0 : a.slots);
   if (items == 0) return hipSuccess;
   linear_shape<PARTS>(a.dx, a.dw, [&](auto dx, auto cw, auto c) {
     constexpr int DX = decltype(dx)::value, CW = decltype(cw)::value, C = decltype(c)::value;
     const long units = items * a.Hv;
     const unsigned grid = (unsigned)((units + 7) / 8 * 8 * ((a.dw + 4 * CW - 1) / (4 * CW)));
     if (a.dx % 8 == 0 && a.dw % 8 == 0)
-      linear_pass_kernel<T, PARTS, DX, CW, C, true, SUM><<<grid, 256, 0, s>>>(a);
+      linear_pass_kernel<T, PARTS, DX, CW, C, true, MODE><<<grid, 256, 0, s>>>(a);
     else
-      linear_pass_kernel<T, PARTS, DX, CW, C, false, SUM><<<grid, 256, 0, s>>>(a);
+      linear_pass_kernel<T, PARTS, DX, CW, C, false, MODE><<<grid, 256, 0, s>>>(a);
   });
   return hipGetLastError();
 }
