@@ -12,9 +12,9 @@ hipError_t linear_pass_bf16(const LinPass& a, bool sum, hipStream_t s) {
 
 int linear_parts_bf16(int dx, int dw) {
   int parts = 0;
-  linear_shape<1>(dx, dw, [&](auto, auto cw, auto) {
-    constexpr int COLS = 4 * decltype(cw)::value;
-    parts = (dw + COLS - 1) / COLS * 4;
+  linear_shape<1>(dx, dw, [&](auto, auto waves, auto cw, auto) {
+    constexpr int W = decltype(waves)::value, COLS = W * decltype(cw)::value;
+    parts = (dw + COLS - 1) / COLS * W;
   });
   return parts;
 }

@@ -31,17 +31,72 @@ __device__ __forceinline__ void fetch8(const unsigned char* __restrict__ base, u
   }
 }
 
+// Rows of tiles in LDS: their pieces of 16 bytes change places by the row's low bits.  Neither 16
+// rows of one piece (an operand by rows) nor 4 rows of 4 neighbouring pieces (a transposing read)
+// share banks then, for rows of 128 bytes or a multiple of 256.  Where a byte of a row lies is
+// (byte ^ turn(row)); turn(row + 16) = turn(row), turn(row + 4) = turn(row) ^ 16 if row % 8 < 4.
+template <int COLS>
+__device__ __forceinline__ unsigned turn(unsigned row) {
+  return COLS == 64 ? (row >> 1 & 1) << 6 | (row >> 2 & 3) << 4 : (row & 3) << 6 | (row >> 2 & 3) << 4;
+}
+
+// The thread's number, not known to be the one of another call: what is computed from it is
+// computed there, and not kept in registers through the loop (64 of which would be spilled).
+__device__ __forceinline__ unsigned thread() {
+  unsigned t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
+typedef __attribute__((address_space(3))) unsigned char Lds;
+
+__device__ __forceinline__ v8bf take(const Lds* at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) v8bf*>(at);
+}
+// Operand of 16 columns by 32 rows: as get_tr (delta_device.h); `lo` are rows r .. r + 4 of a lane's
+// share, `hi` the next four.
+__device__ __forceinline__ v8bf take_tr(const Lds* lo, const Lds* hi) {
+  typedef short v4s __attribute__((ext_vector_type(4)));
+  typedef __attribute__((address_space(3))) v4s lds4;
+  union {
+    v4s h[2];
+    v8bf v;
+  } u;
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)lo);
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds4*)hi);
+  return u.v;
+}
+template <typename V>
+__device__ __forceinline__ void put(Lds* at, V v) {
+  *reinterpret_cast<__attribute__((address_space(3))) V*>(at) = v;
+}
+template <typename V>
+__device__ __forceinline__ V get(const Lds* at) {
+  return *reinterpret_cast<const __attribute__((address_space(3))) V*>(at);
+}
+
+// c[i] += a b over the parts, for N independent c, which lie between two instructions of one.
+template <int KEEP, int PA, int PB, typename F>
+__device__ __forceinline__ void over_parts(F f) {
+#pragma unroll
+  for (int i = PA - 1; i >= 0; --i)
+#pragma unroll
+    for (int j = PB - 1; j >= 0; --j)
+      if (i + j < KEEP) f(i, j);
+}
+
 // A tile of C rows x COLS columns of a tensor's head, on its way to LDS.
-template <typename T, int PARTS, int C, int COLS, bool WHOLE>
+template <typename T, int PARTS, int C, int COLS, bool WHOLE, int THREADS>
 struct LinTile {
-  static constexpr int LD = COLS + 8, N = C * COLS / 8 / 256, STEP = 256 / (COLS / 8);
-  static_assert(N * 256 * 8 == C * COLS, "");
+  static constexpr int N = C * COLS / 8 / THREADS, STEP = THREADS / (COLS / 8);
+  static constexpr int ROW = 2 * COLS, PART = C * ROW;   // bytes in LDS
+  static_assert(N * THREADS * 8 == C * COLS && STEP % 8 == 0, "");
   T v[N][8];
   // `n` rows from `base` on, ld elements apart (64 rows of less than 2^24 elements: offsets of
   // 32 bits), in reverse with rev; columns c0 and on
   __device__ __forceinline__ void fetch(const unsigned char* base, unsigned ld, int n, int rev, int c0,
                                         int d) {
-    const int r0 = threadIdx.x / (COLS / 8), c = c0 + threadIdx.x % (COLS / 8) * 8;
+    const int tid = (int)thread(), r0 = tid / (COLS / 8), c = c0 + tid % (COLS / 8) * 8;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       int row = r0 + i * STEP;
@@ -50,19 +105,17 @@ struct LinTile {
       fetch8<T, WHOLE>(base, (unsigned)row * (ld * (unsigned)sizeof(T)), c, d, v[i]);
     }
   }
-  __device__ __forceinline__ void stage(__bf16 (*to)[C][LD], int n, int c0, int d) const {
-    const int r0 = threadIdx.x / (COLS / 8), c = threadIdx.x % (COLS / 8) * 8;
+  __device__ __forceinline__ void stage(Lds* to, int n, int c0, int d) const {
+    const int tid = (int)thread(), r0 = tid / (COLS / 8), c = tid % (COLS / 8) * 8;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       const int r = r0 + i * STEP;
+      Lds* at = to + ((unsigned)(r * ROW) | (2u * c ^ turn<COLS>(r)));
       if constexpr (WHOLE && sizeof(T) == 2 && PARTS == 1) {
-        v8bf x;
-        __builtin_memcpy(&x, v[i], 16);
         typedef int v4i __attribute__((ext_vector_type(4)));
         v4i y;
         __builtin_memcpy(&y, v[i], 16);
-        y = r < n && c0 + c < d ? y : v4i{0, 0, 0, 0};
-        *reinterpret_cast<v4i*>(&to[0][r][c]) = y;
+        put(at, r < n && c0 + c < d ? y : v4i{0, 0, 0, 0});
       } else {
         float x[8];
 #pragma unroll
@@ -71,7 +124,7 @@ struct LinTile {
         v8bf parts[PARTS];
         split8<PARTS>(x, parts);
 #pragma unroll
-        for (int q = 0; q < PARTS; ++q) *reinterpret_cast<v8bf*>(&to[q][r][c]) = parts[q];
+        for (int q = 0; q < PARTS; ++q) put(at + q * PART, parts[q]);
       }
     }
   }
@@ -105,43 +158,70 @@ __device__ __forceinline__ void store_state(float* __restrict__ to, int col0, in
     }
   }
 }
-// Read without a load under a condition: 0 where there is none.
+// The same value, for all that the compiler knows another one: a load of it is not put under the
+// condition under which it is used, where it would be waited for at once.
+__device__ __forceinline__ void touch(float& v) { asm volatile("" : "+v"(v)); }
+
 template <int TILES, int CT>
 __device__ __forceinline__ void load_state(const float* __restrict__ from, int col0, int dx, int dw,
                                            int rs, int cs, v4f (&S)[TILES][CT]) {
   const int lr = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+  auto row_of = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
+  if (rs == 1 && dx % 4 == 0) {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int c = 0; c < CT; ++c) {
+        const int row = row_of(t), col = col0 + 16 * c + lr;
+        __builtin_memcpy(&S[t][c], from + (col < dw && row < dx ? row + col * cs : 0), 16);
+      }
+  } else {
+#pragma unroll
+    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+      for (int c = 0; c < CT; ++c)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const int row = row_of(t) + e, col = col0 + 16 * c + lr;
+          S[t][c][e] = from[col < dw && row < dx ? row * rs + col * cs : 0];
+        }
+  }
 #pragma unroll
   for (int t = 0; t < TILES; ++t)
 #pragma unroll
-    for (int c = 0; c < CT; ++c) {
-      const int row = 32 * (t >> 1) + 8 * lg + 4 * (t & 1), col = col0 + 16 * c + lr;
+    for (int c = 0; c < CT; ++c)
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
-        const bool in = col < dw && row + e < dx;
-        const float v = from[in ? (row + e) * rs + col * cs : 0];
-        S[t][c][e] = in ? v : 0.f;
+        float v = S[t][c][e];
+        touch(v);
+        S[t][c][e] = col0 + 16 * c + lr < dw && row_of(t) + e < dx ? v : 0.f;
       }
-    }
 }
 
 enum { kSum, kOut, kGrad };   // what a segment adds; a pass; a pass with `dot` and out in float
 
-template <typename T, int PARTS, int DX, int CW, int C, bool WHOLE, int MODE>
-__global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_pass_kernel(
-    const LinPass p) {
-  constexpr int TILES = DX / 16, CT = CW / 16, KS = DX / 32, RT = C / 16, COLS = 4 * CW;
+// Blocks that share a CU: two where they fit into its LDS.
+constexpr int linear_blocks(int parts, int dx, int cols, int c, int mode) {
+  const int tiles = 2 * parts * c * (mode == kSum ? dx + cols : 2 * dx + cols);
+  const int pairs = mode == kSum ? 0 : 6 * c * (c + 8);
+  return 2 * (tiles + pairs + 2048) <= 160 * 1024 ? 2 : 1;
+}
+
+template <typename T, int PARTS, int DX, int WAVES, int CW, int C, bool WHOLE, int MODE>
+__global__ __launch_bounds__(64 * WAVES, WAVES / 4 * linear_blocks(PARTS, DX, WAVES * CW, C, MODE))
+void linear_pass_kernel(const LinPass p) {
+  constexpr int TILES = DX / 16, CT = CW / 16, KS = DX / 32, RT = C / 16, COLS = WAVES * CW;
   constexpr bool SUM = MODE == kSum;
-  using XTile = LinTile<T, PARTS, C, DX, WHOLE>;
-  using WTile = LinTile<T, PARTS, C, COLS, WHOLE>;
-  __shared__ __attribute__((aligned(16))) __bf16 ys[PARTS][C][DX + 8];
-  __shared__ __attribute__((aligned(16))) __bf16 ws[PARTS][C][COLS + 8];
-  __shared__ __attribute__((aligned(16))) __bf16 xs[SUM ? 1 : PARTS][SUM ? 1 : C][DX + 8];
-  __shared__ __attribute__((aligned(16))) __bf16 ps[SUM ? 1 : 3][SUM ? 1 : C][C + 8];
-  __shared__ float2 G[C];
-  __shared__ __attribute__((aligned(16))) float es[C], ds[C];
-  __shared__ float whole;
+  using XTile = LinTile<T, PARTS, C, DX, WHOLE, 64 * WAVES>;
+  using WTile = LinTile<T, PARTS, C, COLS, WHOLE, 64 * WAVES>;
+  // LDS: Y, W, (X, P by parts of C rows,) and of two chunks in turn G as pairs of floats, d, the whole decay
+  constexpr int PROW = 2 * (C + 8), PPART = C * PROW;
+  constexpr int oY = 0, oW = oY + PARTS * XTile::PART, oX = oW + PARTS * WTile::PART;
+  constexpr int oP = oX + (SUM ? 0 : PARTS * XTile::PART), oG = oP + (SUM ? 0 : 3 * PPART);
+  constexpr int oD = oG + 2 * 8 * C, oWhole = oD + 2 * 4 * C;
+  __shared__ __attribute__((aligned(512))) unsigned char memory[oWhole + 8];
+  Lds* const lds = (Lds*)memory;
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int lr = lane & 15, lg = lane >> 4;
   const int slices = (p.dw + COLS - 1) / COLS;
   // blocks go round robin over the 8 XCDs; the slices of a head share one
   const unsigned g8 = blockIdx.x >> 3;
@@ -193,79 +273,94 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
       xr.fetch(xb + c0 * (p.ldx * (long)sizeof(T)), (unsigned)p.ldx, n, p.rev, 0, p.dx);
     yr.fetch(yb + c0 * (p.ldy * (long)sizeof(T)), (unsigned)p.ldy, n, p.rev, 0, p.dx);
     wr.fetch(wb + c0 * (p.ldw * (long)sizeof(T)), (unsigned)p.ldw, n, p.rev, slice * COLS, p.dw);
-    if (w == 0 && gb) {
-      const int row = lane < n ? p.rev ? n - 1 - lane : lane : 0;
-      gr = gb[(c0 + row) * p.ldg];
-      gr = lane < n ? gr : 0.f;
-    }
   };
-  if (chunks > 0) fetch(0);
-  for (int i = 0; i < chunks; ++i) {
-    const int c0 = first_of(i), n = rows_of(c0);
-    if (w == 0) {
-      // decays as powers of two, summed in 64 bits, so that a difference keeps its digits behind
-      // a large negative g (a reset); below -200 the decay is 0 in fp32 either way
-      const double own = (gr < -200.f ? -200.0 : (double)gr) * 1.4426950408889634;
-      double x = own;
+  // wave 0: g of chunk i, a row a lane, two chunks ahead of its use
+  auto fetch_g = [&](int i) {
+    if (w != 0 || !gb || i >= chunks) return;
+    const int c0 = first_of(i), n = rows_of(c0), row = lane < n ? lane : n - 1;
+    gr = gb[(c0 + (p.rev ? n - 1 - row : row)) * p.ldg];
+  };
+  // wave 0: the decays of chunk i as powers of two, summed in 64 bits, so that a difference keeps its
+  // digits behind a large negative g (a reset); below -200 the decay is 0 in fp32 either way
+  auto decays = [&](int i) {
+    if (w != 0 || i >= chunks) return;
+    const float g = lane < rows_of(first_of(i)) ? gr : 0.f;
+    const double own = (g < -200.f ? -200.0 : (double)g) * 1.4426950408889634;
+    double x = own;
 #pragma unroll
-      for (int off = 1; off < 64; off <<= 1) {
-        const double y = __shfl_up(x, off);
-        if (lane >= off) x += y;
-      }
-      const double last = __shfl(x, 63);
-      if (p.rev) x -= own;
-      if (lane < C) {
-        const float hi = (float)x;
-        G[lane] = float2{hi, (float)(x - hi)};
-        es[lane] = exp_diff(x) * p.read;
-        ds[lane] = exp_diff(last - x) * p.update;
-      }
-      if (lane == 0) whole = exp_diff(last);
-      all += last;
+    for (int off = 1; off < 64; off <<= 1) {
+      const double y = __shfl_up(x, off);
+      if (lane >= off) x += y;
     }
-    if constexpr (!SUM) xr.stage(xs, n, 0, p.dx);
-    yr.stage(ys, n, 0, p.dx);
-    wr.stage(ws, n, slice * COLS, p.dw);
+    const double last = __shfl(x, 63);
+    if (p.rev) x -= own;
+    if (lane < C) {
+      const float hi = (float)x;
+      put(lds + oG + ((i & 1) * 8 * C + 8 * lane), v2f{hi, (float)(x - hi)});
+      put(lds + oD + ((i & 1) * 4 * C + 4 * lane), exp_diff(last - x) * p.update);
+    }
+    if (lane == 0) put(lds + oWhole + (i & 1) * 4, exp_diff(last));
+    all += last;
+  };
+  if (chunks > 0) {
+    fetch_g(0);
+    fetch(0);
+    decays(0);
+    fetch_g(1);
+  }
+  for (int i = 0; i < chunks; ++i) {
+    const int c0 = first_of(i), n = rows_of(c0), at = i & 1;
+    if constexpr (!SUM) xr.stage(lds + oX, n, 0, p.dx);
+    yr.stage(lds + oY, n, 0, p.dx);
+    wr.stage(lds + oW, n, slice * COLS, p.dw);
     __syncthreads();
     if (i + 1 < chunks) fetch(i + 1);
+    decays(i + 1);
+    fetch_g(i + 2);
 
     v4f O[SUM ? 1 : RT][CT];
     if constexpr (!SUM) {
-      // P's rows 16 w .. + 16, a lane one row and four neighbouring columns of each tile
-      if (w < RT) {
+      // P by strips of 16 rows, whose tiles the waves share out; a lane has one row and four
+      // neighbouring columns of a tile
+      constexpr int SHARE = WAVES / RT;
+      const int strip = w % RT;
+      {
+        const unsigned tid = thread(), r = tid & 15, g = (tid & 63) >> 4;
+        const unsigned row = r * XTile::ROW | (16 * g ^ turn<DX>(r));
         v8bf xo[KS][PARTS];
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks)
 #pragma unroll
           for (int q = 0; q < PARTS; ++q)
-            xo[ks][q] = *reinterpret_cast<const v8bf*>(&xs[q][16 * w + lr][32 * ks + 8 * lg]);
-        const float2 gi = G[16 * w + lr];
+            xo[ks][q] = take(lds + oX + q * XTile::PART + ((row ^ 64 * ks) + strip * 16 * XTile::ROW));
+        const v2f gi = get<v2f>(lds + oG + (at * 8 * C + 8 * (16 * strip + r)));
 #pragma unroll
-        for (int ct = 0; ct < RT; ++ct) {
-          if (ct > (w | 1)) continue;   // never read
+        for (int k = 0; k < (RT + SHARE - 1) / SHARE; ++k) {
+          const int ct = k * SHARE + w / RT;
+          if (ct > (strip | 1)) continue;   // never read
           v4f acc = {0.f, 0.f, 0.f, 0.f};
-          if (ct <= w) {
+          if (ct <= strip) {
 #pragma unroll
             for (int ks = 0; ks < KS; ++ks) {
               v8bf yo[PARTS];
 #pragma unroll
               for (int q = 0; q < PARTS; ++q)
-                yo[q] = *reinterpret_cast<const v8bf*>(&ys[q][16 * ct + lr][32 * ks + 8 * lg]);
+                yo[q] = take(lds + oY + q * XTile::PART + ((row ^ 64 * ks) + ct * 16 * XTile::ROW));
               acc = mfma_parts<3>(yo, xo[ks], acc);
             }
+            const Lds* gp = lds + oG + (at * 8 * C + 8 * (16 * ct + 4 * g));
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
-              const int j = 16 * ct + 4 * lg + e;
-              const float2 gj = G[j];
-              const float f = __builtin_amdgcn_exp2f((gi.x - gj.x) + (gi.y - gj.y));
-              acc[e] = j <= 16 * w + lr ? acc[e] * f * p.pair : 0.f;
+              const v2f gj = get<v2f>(gp + 8 * e);
+              const float f = __builtin_amdgcn_exp2f((gi[0] - gj[0]) + (gi[1] - gj[1]));
+              acc[e] = 16 * ct + 4 * g + e <= 16 * strip + r ? acc[e] * f * p.pair : 0.f;
             }
           }
           v4bf parts[3];
           split4<3>(acc, parts);
 #pragma unroll
           for (int q = 0; q < 3; ++q)
-            *reinterpret_cast<v4bf*>(&ps[q][16 * w + lr][16 * ct + 4 * lg]) = parts[q];
+            put(lds + oP + q * PPART + ((16 * strip + r) * PROW + 2 * (16 * ct + 4 * g)), parts[q]);
         }
       }
       // X S, transposed: a lane one row and four neighbouring columns
@@ -273,93 +368,155 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
       for (int r = 0; r < RT; ++r)
 #pragma unroll
         for (int c = 0; c < CT; ++c) O[r][c] = v4f{0.f, 0.f, 0.f, 0.f};
+      {
+        const unsigned tid = thread(), lr = tid & 15, g = (tid & 63) >> 4;
+        const unsigned row = lr * XTile::ROW | (16 * g ^ turn<DX>(lr));
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        v8bf so[CT][3];
+        for (int ks = 0; ks < KS; ++ks) {
+          v8bf so[CT][3];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) {
-          float t[8];
+          for (int c = 0; c < CT; ++c) {
+            float t[8];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            t[e] = S[2 * ks][c][e];
-            t[4 + e] = S[2 * ks + 1][c][e];
+            for (int e = 0; e < 4; ++e) {
+              t[e] = S[2 * ks][c][e];
+              t[4 + e] = S[2 * ks + 1][c][e];
+            }
+            split8<3>(t, so[c]);
           }
-          split8<3>(t, so[c]);
+          v8bf xo[RT][PARTS];
+#pragma unroll
+          for (int r = 0; r < RT; ++r)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q)
+              xo[r][q] = take(lds + oX + q * XTile::PART + r * 16 * XTile::ROW + (row ^ 64 * ks));
+          over_parts<3, 3, PARTS>([&](int i, int j) {
+#pragma unroll
+            for (int r = 0; r < RT; ++r)
+#pragma unroll
+              for (int c = 0; c < CT; ++c) O[r][c] = mfma(so[c][i], xo[r][j], O[r][c]);
+          });
         }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          v8bf xo[PARTS];
+          const v2f gi = get<v2f>(lds + oG + (at * 8 * C + 8 * lr) + 8 * 16 * r);
+          const float e = __builtin_amdgcn_exp2f(gi[0] + gi[1]) * p.read;
 #pragma unroll
-          for (int q = 0; q < PARTS; ++q)
-            xo[q] = *reinterpret_cast<const v8bf*>(&xs[q][16 * r + lr][32 * ks + 8 * lg]);
-#pragma unroll
-          for (int c = 0; c < CT; ++c) O[r][c] = mfma_parts<3>(so[c], xo, O[r][c]);
+          for (int c = 0; c < CT; ++c) O[r][c] *= e;
         }
-      }
-#pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        const float e = es[16 * r + lr];
-#pragma unroll
-        for (int c = 0; c < CT; ++c) O[r][c] *= e;
       }
     }
     {
-      const float a = whole;
+      const float a = get<float>(lds + oWhole + 4 * at);
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
 #pragma unroll
         for (int c = 0; c < CT; ++c) S[t][c] *= a;
     }
-    if constexpr (!SUM) __syncthreads();   // P is there
-#pragma unroll
-    for (int ks = 0; ks < C / 32; ++ks) {
-      v8bf wo[CT][PARTS];
-#pragma unroll
-      for (int c = 0; c < CT; ++c) get_tr<PARTS, 4>(ws, 32 * ks, w * CW + 16 * c, lr, lg, wo[c]);
-      if constexpr (!SUM) {
+    // `dot` in the rows and columns of O, on its way while the rest is computed
+    T dots[MODE == kGrad ? RT : 1][CT][4];
+    if constexpr (MODE == kGrad) {
+      if (p.dot) {
+        const int tid = (int)thread(), lr = tid & 15, lg = (tid & 63) >> 4;
+        const Bytes db = (Bytes)p.dot + ((it.start + c0) * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T);
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
-          if (ks > r / 2) continue;   // above the diagonal
-          v8bf po[3];
+          int row = 16 * r + lr;
+          row = row < n ? row : n - 1;
+          row = p.rev ? n - 1 - row : row;
 #pragma unroll
-          for (int q = 0; q < 3; ++q)
-            po[q] = *reinterpret_cast<const v8bf*>(&ps[q][16 * r + lr][32 * ks + 8 * lg]);
+          for (int c = 0; c < CT; ++c) {
+            const int col = col0 + 16 * c + 4 * lg;
+            const Bytes from = db + (unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T));
+            if constexpr (WHOLE) {
+              __builtin_memcpy(dots[r][c], from + (col < p.dw ? col : 0) * (unsigned)sizeof(T), 4 * sizeof(T));
+            } else {
 #pragma unroll
-          for (int c = 0; c < CT; ++c) O[r][c] = mfma_parts<3>(wo[c], po, O[r][c]);
+              for (int e = 0; e < 4; ++e)
+                __builtin_memcpy(&dots[r][c][e], from + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T), sizeof(T));
+            }
+          }
         }
       }
-      v8bf dw[CT][3];
-      float d[8];
-      __builtin_memcpy(d, &ds[32 * ks + 8 * lg], sizeof(d));
+    }
+    if constexpr (!SUM) __syncthreads();   // P is there
+    {
+      const unsigned tid = thread(), lr = tid & 15, g = (tid & 63) >> 4, row = 8 * g + (lr >> 2);
+      // four rows of four groups of four columns: of W neighbouring ones, of Y 8 columns apart
+      const unsigned wt = row * WTile::ROW | ((2 * CW * w + 8 * (lr & 3)) ^ turn<COLS>(row));
+      const unsigned yt = row * XTile::ROW | (16 * (lr & 3) ^ turn<DX>(row));
 #pragma unroll
-      for (int c = 0; c < CT; ++c) {
-        float t[8];
+      for (int ks = 0; ks < C / 32; ++ks) {
+        v8bf wo[CT][PARTS];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          float v = (float)wo[c][0][j];
+        for (int c = 0; c < CT; ++c)
 #pragma unroll
-          for (int q = 1; q < PARTS; ++q) v += (float)wo[c][q][j];
-          t[j] = v * d[j];
+          for (int q = 0; q < PARTS; ++q) {
+            const Lds* m = lds + oW + q * WTile::PART + ks * 32 * WTile::ROW;
+            wo[c][q] = take_tr(m + (wt ^ 32 * c), m + 4 * WTile::ROW + (wt ^ 32 * c ^ 16));
+          }
+        if constexpr (!SUM) {
+#pragma unroll
+          for (int r = 2 * ks; r < RT; r += 2) {   // two strips; those above are above the diagonal
+            v8bf po[2][3];
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+              for (int q = 0; q < 3; ++q)
+                po[k][q] = take(lds + oP + q * PPART + 16 * (r + k) * PROW + 64 * ks + (lr * PROW + 16 * g));
+            over_parts<3, PARTS, 3>([&](int i, int j) {
+#pragma unroll
+              for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) O[r + k][c] = mfma(wo[c][i], po[k][j], O[r + k][c]);
+            });
+          }
         }
-        split8<3>(t, dw[c]);
-      }
+        v8bf dw[CT][3];
+        {
+          const v4f d0 = get<v4f>(lds + oD + 128 * ks + (4 * C * at + 32 * g));
+          const v4f d1 = get<v4f>(lds + oD + 128 * ks + 16 + (4 * C * at + 32 * g));
 #pragma unroll
-      for (int t = 0; t < TILES; ++t) {
-        v8bf yo[PARTS];
-        get_tr<PARTS, 8>(ys, 32 * ks, 32 * (t >> 1) + 4 * (t & 1), lr, lg, yo);
+          for (int c = 0; c < CT; ++c) {
+            float t[8];
 #pragma unroll
-        for (int c = 0; c < CT; ++c) S[t][c] = mfma_parts<3>(yo, dw[c], S[t][c]);
+            for (int j = 0; j < 8; ++j) {
+              float v = (float)wo[c][0][j];
+#pragma unroll
+              for (int q = 1; q < PARTS; ++q) v += (float)wo[c][q][j];
+              t[j] = v * (j < 4 ? d0[j & 3] : d1[j & 3]);
+            }
+            split8<3>(t, dw[c]);
+          }
+        }
+#pragma unroll
+        for (int t = 0; t < TILES; t += 4) {
+          v8bf yo[4][PARTS];
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int q = 0; q < PARTS; ++q) {
+              const Lds* m = lds + oY + q * XTile::PART + ks * 32 * XTile::ROW + 8 * (k & 1);
+              const unsigned x = 64 * ((t + k) >> 1);
+              yo[k][q] = take_tr(m + (yt ^ x), m + 4 * XTile::ROW + (yt ^ x ^ 16));
+            }
+          over_parts<3, PARTS, 3>([&](int i, int j) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+              for (int c = 0; c < CT; ++c) S[t + k][c] = mfma(yo[k][i], dw[c][j], S[t + k][c]);
+          });
+        }
       }
     }
     if constexpr (!SUM) {
+      const int tid = (int)thread(), lr = tid & 15, lg = (tid & 63) >> 4;
       // rows of out of this chunk: base (uniform) and offsets of 32 bits
       const long tok0 = it.start + c0;
       const unsigned wide = MODE == kGrad && p.out_f32 ? 4 : sizeof(T);
       unsigned char* ob = (unsigned char*)p.out + (tok0 * ldo + (long)h * p.dw) * wide;
-      const Bytes db = MODE == kGrad
-          ? (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T) : nullptr;
       float* to = MODE == kGrad && p.dot
-          ? p.dot_out + ((size_t)(slice * 4 + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
+          ? p.dot_out + ((size_t)(slice * WAVES + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int i = 16 * r + lr, row = p.rev ? n - 1 - i : i;
@@ -369,7 +526,7 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
           for (int c = 0; c < CT; ++c) {
             const int col = col0 + 16 * c + 4 * lg;
             const v4f o = O[r][c];
-            auto put = [&](int e0, int m) {   // columns e0 .. e0 + m of the four
+            auto write = [&](int e0, int m) {   // columns e0 .. e0 + m of the four
               unsigned char* q = ob + ((unsigned)row * ((unsigned)ldo * wide) + (col + e0) * wide);
               if (MODE == kGrad && p.out_f32) {
                 __builtin_memcpy(q, (const float*)&o + e0, 4 * m);
@@ -379,19 +536,16 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
                 __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if (MODE == kGrad && p.dot) {
-                T t[4];
-                __builtin_memcpy(t, db + ((unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T)) +
-                                          (col + e0) * (unsigned)sizeof(T)), sizeof(T) * m);
-                for (int e = 0; e < m; ++e) sum = fmaf(o[e0 + e], to_f32(t[e]), sum);
-              }
+              if constexpr (MODE == kGrad)
+                if (p.dot)
+                  for (int e = e0; e < e0 + m; ++e) sum = fmaf(o[e], to_f32(dots[r][c][e]), sum);
             };
             if (col + 4 <= p.dw) {
-              put(0, 4);
+              write(0, 4);
             } else if constexpr (!WHOLE) {
-              if (col < p.dw) put(0, 1);
-              if (col + 1 < p.dw) put(1, 1);
-              if (col + 2 < p.dw) put(2, 1);
+              if (col < p.dw) write(0, 1);
+              if (col + 1 < p.dw) write(1, 1);
+              if (col + 2 < p.dw) write(2, 1);
             }
           }
         }
@@ -425,30 +579,38 @@ __global__ __launch_bounds__(256, PARTS == 1 && DX <= 128 ? 2 : 1) void linear_p
           for (int e = 0; e < 4; ++e) sum = fmaf(S[t][c][e], other[t][c][e], sum);
       sum = sum64(sum);
       const size_t item = it.of ? (size_t)p.sequences + it.slot : (size_t)it.s;
-      if (lane == 0) p.edge_out[(item * p.Hv + h) * kDotParts + slice * 4 + w] = sum;
+      if (lane == 0) p.edge_out[(item * p.Hv + h) * kDotParts + slice * WAVES + w] = sum;
     }
   }
 }
 
-// The variant for these sizes: f(DX, CW, C as constants).  The columns of the state that a wave
-// holds: 32, or 16 where the head has no more than 64 or the operands' parts leave no room in
-// LDS; chunks of 32 tokens where 64 do not fit.
+// The variant for these sizes: f(DX, WAVES, CW, C as constants).  A wave holds 16 columns of the
+// state; eight share a block where the head has more than 64, unless the operands' parts leave no
+// room in LDS.  Chunks of 32 tokens where 64 do not fit.
 template <int PARTS, typename F>
 void linear_shape(int dx, int dw, F f) {
   using std::integral_constant;
-#define S4_CASE(DX, CW, C) \
-  f(integral_constant<int, DX>(), integral_constant<int, CW>(), integral_constant<int, C>())
+  constexpr integral_constant<int, 4> four;
+  constexpr integral_constant<int, 8> eight;
+  constexpr integral_constant<int, 16> cw;
+  constexpr integral_constant<int, 64> c64;
+  constexpr integral_constant<int, PARTS == 1 ? 64 : 32> c256;
+  const bool wide = dw > 64;
   if (dx <= 64) {
-    if (dw <= 64 || PARTS == 3) S4_CASE(64, 16, 64);
-    else if constexpr (PARTS < 3) S4_CASE(64, 32, 64);
+    constexpr integral_constant<int, 64> d;
+    if (wide) f(d, eight, cw, c64);
+    else f(d, four, cw, c64);
   } else if (dx <= 128) {
-    if (dw <= 64 || PARTS > 1) S4_CASE(128, 16, 64);
-    else if constexpr (PARTS == 1) S4_CASE(128, 32, 64);
+    constexpr integral_constant<int, 128> d;
+    if constexpr (PARTS < 3) {
+      if (wide) return f(d, eight, cw, c64);
+    }
+    f(d, four, cw, c64);
   } else {
-    if constexpr (PARTS == 1) S4_CASE(256, 16, 64);
-    else S4_CASE(256, 16, 32);
+    constexpr integral_constant<int, 256> d;
+    if (wide) f(d, eight, cw, c256);
+    else f(d, four, cw, c256);
   }
-#undef S4_CASE
 }
 
 template <typename T, int PARTS, int MODE>
@@ -456,14 +618,15 @@ hipError_t linear_launch(const LinPass& a, hipStream_t s) {
   const bool all_long = !a.offsets && a.each > a.segment, all_short = !a.offsets && !all_long;
   const long items = (all_long || MODE == kSum ? 0 : a.sequences) + (all_short ? 0 : a.slots);
   if (items == 0) return hipSuccess;
-  linear_shape<PARTS>(a.dx, a.dw, [&](auto dx, auto cw, auto c) {
-    constexpr int DX = decltype(dx)::value, CW = decltype(cw)::value, C = decltype(c)::value;
+  linear_shape<PARTS>(a.dx, a.dw, [&](auto dx, auto waves, auto cw, auto c) {
+    constexpr int DX = decltype(dx)::value, W = decltype(waves)::value, CW = decltype(cw)::value;
+    constexpr int C = decltype(c)::value;
     const long units = items * a.Hv;
-    const unsigned grid = (unsigned)((units + 7) / 8 * 8 * ((a.dw + 4 * CW - 1) / (4 * CW)));
+    const unsigned grid = (unsigned)((units + 7) / 8 * 8 * ((a.dw + W * CW - 1) / (W * CW)));
     if (a.dx % 8 == 0 && a.dw % 8 == 0)
-      linear_pass_kernel<T, PARTS, DX, CW, C, true, MODE><<<grid, 256, 0, s>>>(a);
+      linear_pass_kernel<T, PARTS, DX, W, CW, C, true, MODE><<<grid, 64 * W, 0, s>>>(a);
     else
-      linear_pass_kernel<T, PARTS, DX, CW, C, false, MODE><<<grid, 256, 0, s>>>(a);
+      linear_pass_kernel<T, PARTS, DX, W, CW, C, false, MODE><<<grid, 64 * W, 0, s>>>(a);
   });
   return hipGetLastError();
 }
