@@ -66,45 +66,73 @@ __global__ __launch_bounds__(256) void linear_groups_kernel(const float* __restr
 
 // dg_t = <S_{t-1}, gradient of S_{t-1} by what comes later>: the edge before the segment, and
 // behind token i  + k_i . dk_i - q_i . dq_i  of the token itself.  The sums are held in 64 bits
-// over a segment of a few hundred tokens.  One wave per segment and head.  Where exp(g) is 0
-// nothing of the state before is left, and dg is 0.
-__global__ __launch_bounds__(64) void linear_gates_kernel(const LinGates a) {
-  const int lane = threadIdx.x, h = blockIdx.y;
+// over a segment of a few hundred tokens.  A block per segment and head, 64 tokens a wave.  Where
+// exp(g) is 0 nothing of the state before is left, and dg is 0.
+__global__ __launch_bounds__(512) void linear_gates_kernel(const LinGates a) {
+  __shared__ double sums[2][8], totals[8];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = blockIdx.y;
   LinItem it;
   const long skip = a.offsets || a.each <= a.segment ? 0 : a.sequences;
   const long item = skip + blockIdx.x;
   if (!lin_item(a, item, &it)) {
-    if (lane == 0 && a.ldg == 0) a.sums[item * a.Hv + h] = 0.f;
+    if (threadIdx.x == 0 && a.ldg == 0) a.sums[item * a.Hv + h] = 0.f;
     return;
   }
   double run = 0.0, total = 0.0;
-  if (it.len > 0)
-    for (int i = 0; i < a.parts_edge; ++i) run += a.edge[(item * a.Hv + h) * kDotParts + i];
-  for (int t0 = 0; t0 < it.len; t0 += 64) {
+  if (it.len > 0) {
+    const float e = lane < a.parts_edge ? a.edge[(item * a.Hv + h) * kDotParts + lane] : 0.f;
+    run = e;
+#pragma unroll
+    for (int off = 8; off >= 1; off >>= 1) run += __shfl_xor(run, off);
+    run = __shfl(run, 0);
+  }
+  int turn = 0;
+  for (int t0 = 64 * w; t0 - 64 * w < it.len; t0 += 512, turn ^= 1) {
     const bool in = t0 + lane < it.len;
-    const long tok = it.start + t0 + lane;
-    double own = 0.0;
-    float g = 0.f;
-    if (in) {
-      for (int i = 0; i < a.parts_k; ++i) own += a.dotk[((size_t)i * a.Hv + h) * a.tokens + tok];
-      for (int i = 0; i < a.parts_q; ++i) own -= a.dots[((size_t)i * a.Hv + h) * a.tokens + tok];
-      g = a.g[tok * a.ldg + h];
+    const long tok = it.start + (in ? t0 + lane : 0);
+    const float *kp = a.dotk + (size_t)h * a.tokens + tok, *qp = a.dots + (size_t)h * a.tokens + tok;
+    const size_t step = (size_t)a.Hv * a.tokens;
+    float dk[kDotParts], dq[kDotParts];
+#pragma unroll
+    for (int i = 0; i < kDotParts; ++i) {
+      dk[i] = kp[(i < a.parts_k ? i : 0) * step];
+      dq[i] = qp[(i < a.parts_q ? i : 0) * step];
     }
+    const float g = a.g[tok * a.ldg + h];
+    double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kDotParts; ++i) {
+      if (i < a.parts_k) own += dk[i];
+      if (i < a.parts_q) own -= dq[i];
+    }
+    own = in ? own : 0.0;
     double x = own;
 #pragma unroll
     for (int off = 1; off < 64; off <<= 1) {
       const double y = __shfl_up(x, off);
       if (lane >= off) x += y;
     }
-    const double dg = expf(g) == 0.f ? 0.0 : run + (x - own);
+    if (lane == 63) sums[turn][w] = x;
+    __syncthreads();
+    double before = run;   // of the waves before this one
+    for (int i = 0; i < 8; ++i) {
+      const double y = sums[turn][i];
+      if (i < w) before += y;
+      run += y;
+    }
+    const double dg = expf(g) == 0.f ? 0.0 : before + (x - own);
     if (in && a.ldg) a.dg[tok * a.Hv + h] = (float)dg;
     total += in ? dg : 0.0;
-    run += __shfl(x, 63);
   }
   if (a.ldg == 0) {
 #pragma unroll
     for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off);
-    if (lane == 0) a.sums[item * a.Hv + h] = (float)total;
+    if (lane == 0) totals[w] = total;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+      for (int i = 1; i < 8; ++i) total += totals[i];
+      a.sums[item * a.Hv + h] = (float)total;
+    }
   }
 }
 
@@ -181,7 +209,7 @@ hipError_t launch_linear_gates(const LinGates& a, hipStream_t s) {
   const bool all_long = !a.offsets && a.each > a.segment, all_short = !a.offsets && !all_long;
   const long first = all_long ? a.sequences : 0, last = all_short ? a.sequences : a.sequences + a.slots;
   if (last > first)
-    linear_gates_kernel<<<dim3((unsigned)(last - first), (unsigned)a.Hv), 64, 0, s>>>(a);
+    linear_gates_kernel<<<dim3((unsigned)(last - first), (unsigned)a.Hv), 512, 0, s>>>(a);
   if (a.ldg == 0)
     linear_gate_sums_kernel<<<dim3((unsigned)a.Hv), 256, 0, s>>>(a.sums, first, last, a.Hv, a.dg);
   return hipGetLastError();

@@ -96,26 +96,38 @@ struct LinTile {
   // 32 bits), in reverse with rev; columns c0 and on
   __device__ __forceinline__ void fetch(const unsigned char* base, unsigned ld, int n, int rev, int c0,
                                         int d) {
-    const int tid = (int)thread(), r0 = tid / (COLS / 8), c = c0 + tid % (COLS / 8) * 8;
+    const unsigned tid = thread(), r0 = tid / (COLS / 8);
+    const int c = c0 + (int)(tid % (COLS / 8) * 8), step = rev ? -STEP : STEP;
+    if (n == C) {
+      const unsigned first = rev ? C - 1 - r0 : r0;
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      int row = r0 + i * STEP;
-      row = row < n ? row : n - 1;   // behind the end: a row that is there, unused
-      row = rev ? n - 1 - row : row;
-      fetch8<T, WHOLE>(base, (unsigned)row * (ld * (unsigned)sizeof(T)), c, d, v[i]);
+      for (int i = 0; i < N; ++i)
+        fetch8<T, WHOLE>(base, first * (ld * (unsigned)sizeof(T)) + i * (step * (int)ld * (int)sizeof(T)), c, d, v[i]);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        int row = (int)r0 + i * STEP;
+        row = row < n ? row : n - 1;   // behind the end: a row that is there, unused
+        row = rev ? n - 1 - row : row;
+        fetch8<T, WHOLE>(base, (unsigned)row * (ld * (unsigned)sizeof(T)), c, d, v[i]);
+      }
     }
   }
   __device__ __forceinline__ void stage(Lds* to, int n, int c0, int d) const {
-    const int tid = (int)thread(), r0 = tid / (COLS / 8), c = tid % (COLS / 8) * 8;
+    const unsigned tid = thread(), r0 = tid / (COLS / 8);
+    const int c = (int)(tid % (COLS / 8) * 8);
+    // rows 16 apart have one turn
+    Lds* const first = to + (r0 * ROW | (2u * c ^ turn<COLS>(r0)));
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-      const int r = r0 + i * STEP;
-      Lds* at = to + ((unsigned)(r * ROW) | (2u * c ^ turn<COLS>(r)));
+      const int r = (int)r0 + i * STEP;
+      Lds* at = STEP % 16 == 0 ? first + i * STEP * ROW : to + ((unsigned)(r * ROW) | (2u * c ^ turn<COLS>(r)));
       if constexpr (WHOLE && sizeof(T) == 2 && PARTS == 1) {
         typedef int v4i __attribute__((ext_vector_type(4)));
         v4i y;
         __builtin_memcpy(&y, v[i], 16);
-        put(at, r < n && c0 + c < d ? y : v4i{0, 0, 0, 0});
+        if (n < C || c0 + COLS > d) y = r < n && c0 + c < d ? y : v4i{0, 0, 0, 0};
+        put(at, y);
       } else {
         float x[8];
 #pragma unroll
@@ -413,32 +425,6 @@ void linear_pass_kernel(const LinPass p) {
 #pragma unroll
         for (int c = 0; c < CT; ++c) S[t][c] *= a;
     }
-    // `dot` in the rows and columns of O, on its way while the rest is computed
-    T dots[MODE == kGrad ? RT : 1][CT][4];
-    if constexpr (MODE == kGrad) {
-      if (p.dot) {
-        const int tid = (int)thread(), lr = tid & 15, lg = (tid & 63) >> 4;
-        const Bytes db = (Bytes)p.dot + ((it.start + c0) * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          int row = 16 * r + lr;
-          row = row < n ? row : n - 1;
-          row = p.rev ? n - 1 - row : row;
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int col = col0 + 16 * c + 4 * lg;
-            const Bytes from = db + (unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T));
-            if constexpr (WHOLE) {
-              __builtin_memcpy(dots[r][c], from + (col < p.dw ? col : 0) * (unsigned)sizeof(T), 4 * sizeof(T));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                __builtin_memcpy(&dots[r][c][e], from + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T), sizeof(T));
-            }
-          }
-        }
-      }
-    }
     if constexpr (!SUM) __syncthreads();   // P is there
     {
       const unsigned tid = thread(), lr = tid & 15, g = (tid & 63) >> 4, row = 8 * g + (lr >> 2);
@@ -509,8 +495,36 @@ void linear_pass_kernel(const LinPass p) {
         }
       }
     }
+    // `dot` in the rows and columns of O (earlier its registers would be spilled)
+    T dots[MODE == kGrad ? RT : 1][CT][4];
+    if constexpr (MODE == kGrad) {
+      if (p.dot) {
+        const unsigned tid = thread();
+        const int lr = tid & 15, lg = (tid & 63) >> 4;
+        const Bytes db = (Bytes)p.dot + ((it.start + c0) * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T);
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          int row = 16 * r + lr;
+          row = row < n ? row : n - 1;
+          row = p.rev ? n - 1 - row : row;
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const int col = col0 + 16 * c + 4 * lg;
+            const Bytes from = db + (unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T));
+            if constexpr (WHOLE) {
+              __builtin_memcpy(dots[r][c], from + (col < p.dw ? col : 0) * (unsigned)sizeof(T), 4 * sizeof(T));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                __builtin_memcpy(&dots[r][c][e], from + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T), sizeof(T));
+            }
+          }
+        }
+      }
+    }
     if constexpr (!SUM) {
-      const int tid = (int)thread(), lr = tid & 15, lg = (tid & 63) >> 4;
+      const unsigned tid = thread();
+        const int lr = tid & 15, lg = (tid & 63) >> 4;
       // rows of out of this chunk: base (uniform) and offsets of 32 bits
       const long tok0 = it.start + c0;
       const unsigned wide = MODE == kGrad && p.out_f32 ? 4 : sizeof(T);
