@@ -126,7 +126,10 @@ struct LinTile {
         typedef int v4i __attribute__((ext_vector_type(4)));
         v4i y;
         __builtin_memcpy(&y, v[i], 16);
-        if (n < C || c0 + COLS > d) y = r < n && c0 + c < d ? y : v4i{0, 0, 0, 0};
+        if (n < C || c0 + COLS > d) {
+          asm volatile("");   // a branch: most tiles are whole
+          y = r < n && c0 + c < d ? y : v4i{0, 0, 0, 0};
+        }
         put(at, y);
       } else {
         float x[8];
@@ -277,7 +280,8 @@ void linear_pass_kernel(const LinPass p) {
   const float* gb = p.g ? p.g + it.start * p.ldg + h : nullptr;
   const long ldo = (long)p.Hv * p.dw;
   // first row and number of rows of chunk i of this pass's order
-  auto first_of = [&](int i) { return (p.rev ? chunks - 1 - i : i) * C; };
+  // (the sums' pass goes the other way, so that a chunk's decay to the segment's end is known)
+  auto first_of = [&](int i) { return ((p.rev != 0) != SUM ? chunks - 1 - i : i) * C; };
   auto rows_of = [&](int c0) { return len - c0 < C ? len - c0 : C; };
   auto fetch = [&](int i) {
     const int c0 = first_of(i), n = rows_of(c0);
@@ -306,12 +310,14 @@ void linear_pass_kernel(const LinPass p) {
     }
     const double last = __shfl(x, 63);
     if (p.rev) x -= own;
+    // the sums' pass: `all` is the decay behind the chunk so far
+    const double far = SUM ? last + all : last;
     if (lane < C) {
       const float hi = (float)x;
       put(lds + oG + ((i & 1) * 8 * C + 8 * lane), v2f{hi, (float)(x - hi)});
-      put(lds + oD + ((i & 1) * 4 * C + 4 * lane), exp_diff(last - x) * p.update);
+      put(lds + oD + ((i & 1) * 4 * C + 4 * lane), exp_diff(far - x) * p.update);
     }
-    if (lane == 0) put(lds + oWhole + (i & 1) * 4, exp_diff(last));
+    if (!SUM && lane == 0) put(lds + oWhole + (i & 1) * 4, exp_diff(last));
     all += last;
   };
   if (chunks > 0) {
@@ -418,7 +424,7 @@ void linear_pass_kernel(const LinPass p) {
         }
       }
     }
-    {
+    if constexpr (!SUM) {
       const float a = get<float>(lds + oWhole + 4 * at);
 #pragma unroll
       for (int t = 0; t < TILES; ++t)
@@ -495,33 +501,6 @@ void linear_pass_kernel(const LinPass p) {
         }
       }
     }
-    // `dot` in the rows and columns of O (earlier its registers would be spilled)
-    T dots[MODE == kGrad ? RT : 1][CT][4];
-    if constexpr (MODE == kGrad) {
-      if (p.dot) {
-        const unsigned tid = thread();
-        const int lr = tid & 15, lg = (tid & 63) >> 4;
-        const Bytes db = (Bytes)p.dot + ((it.start + c0) * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T);
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          int row = 16 * r + lr;
-          row = row < n ? row : n - 1;
-          row = p.rev ? n - 1 - row : row;
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int col = col0 + 16 * c + 4 * lg;
-            const Bytes from = db + (unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T));
-            if constexpr (WHOLE) {
-              __builtin_memcpy(dots[r][c], from + (col < p.dw ? col : 0) * (unsigned)sizeof(T), 4 * sizeof(T));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                __builtin_memcpy(&dots[r][c][e], from + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T), sizeof(T));
-            }
-          }
-        }
-      }
-    }
     if constexpr (!SUM) {
       const unsigned tid = thread();
         const int lr = tid & 15, lg = (tid & 63) >> 4;
@@ -529,6 +508,8 @@ void linear_pass_kernel(const LinPass p) {
       const long tok0 = it.start + c0;
       const unsigned wide = MODE == kGrad && p.out_f32 ? 4 : sizeof(T);
       unsigned char* ob = (unsigned char*)p.out + (tok0 * ldo + (long)h * p.dw) * wide;
+      const Bytes db = MODE == kGrad
+          ? (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T) : nullptr;
       float* to = MODE == kGrad && p.dot
           ? p.dot_out + ((size_t)(slice * WAVES + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
 #pragma unroll
@@ -550,9 +531,14 @@ void linear_pass_kernel(const LinPass p) {
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
                 __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if constexpr (MODE == kGrad)
-                if (p.dot)
-                  for (int e = e0; e < e0 + m; ++e) sum = fmaf(o[e], to_f32(dots[r][c][e]), sum);
+              if (MODE == kGrad && p.dot) {
+                T t[4];
+                __builtin_memcpy(t, db + ((unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T)) +
+                                          (col + e0) * (unsigned)sizeof(T)), sizeof(T) * m);
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  if (e < m) sum = fmaf(o[e0 + e], to_f32(t[e]), sum);
+              }
             };
             if (col + 4 <= p.dw) {
               write(0, 4);
