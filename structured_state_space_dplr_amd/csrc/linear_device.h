@@ -43,6 +43,10 @@ struct LinItem {
   long slot, start;
   int len;
 };
+// The same value, for all that the compiler knows another one: a load of it is not put under the
+// condition under which it is used, where it would be waited for at once.
+__device__ __forceinline__ void touch(float& v) { asm volatile("" : "+v"(v)); }
+
 __device__ __forceinline__ long uniform(long v) {
   return (long)(unsigned)__builtin_amdgcn_readfirstlane((int)v) |
          (long)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;

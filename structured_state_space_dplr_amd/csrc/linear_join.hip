@@ -32,6 +32,11 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinPass p) {
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
+      touch(add[i]);
+      touch(dec[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) {
       const int m = m0 + i;
       if (m >= n) break;
       const size_t slot = (size_t)(base + (p.rev ? n - 1 - m : m)) * p.Hv + h;
@@ -100,6 +105,11 @@ __global__ __launch_bounds__(512) void linear_gates_kernel(const LinGates a) {
     }
     const float g = a.g[tok * a.ldg + h];
     double own = 0.0;
+#pragma unroll
+    for (int i = 0; i < kDotParts; ++i) {
+      touch(dk[i]);
+      touch(dq[i]);
+    }
 #pragma unroll
     for (int i = 0; i < kDotParts; ++i) {
       if (i < a.parts_k) own += dk[i];

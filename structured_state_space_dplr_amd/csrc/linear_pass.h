@@ -173,10 +173,6 @@ __device__ __forceinline__ void store_state(float* __restrict__ to, int col0, in
     }
   }
 }
-// The same value, for all that the compiler knows another one: a load of it is not put under the
-// condition under which it is used, where it would be waited for at once.
-__device__ __forceinline__ void touch(float& v) { asm volatile("" : "+v"(v)); }
-
 template <int TILES, int CT>
 __device__ __forceinline__ void load_state(const float* __restrict__ from, int col0, int dx, int dw,
                                            int rs, int cs, v4f (&S)[TILES][CT]) {
