@@ -13,11 +13,17 @@ using namespace s4;
 
 typedef s4dplr_linear_attention_plan Plan;
 
-// Segments give each of the 256 CUs two blocks, if the sequences are long enough for it.
+// Tokens of a segment: two blocks for each of the 256 CUs where there is enough work, a block per CU
+// where there is less, and shorter segments, down to one chunk, where a call is bound by the
+// dependent steps of a block.  Against that, each segment's state is written, read and written
+// again, and read.  Forward, 16 heads of 128 x 128 in bf16 (us; chunks times heads, then the
+// chunks of a segment with the time): 256: 1 29.2, 2 31.3, 4 42.8; 512: 1 44.1, 2 37.9, 4 46.1;
+// 1024: 2 59.1, 4 52.9, 8 72.6; 2048: 2 104, 4 80.3, 8 80.1; 4096: 4 151, 8 125, 16 135; 16384 in 64
+// sequences: 8 452, 16 (whole sequences) 329.  Training step of 4096: 4 595, 8 509, 16 774.
 int segment_of(const Plan& p) {
-  const long chunks = (p.tokens / kLinChunk + 1) * p.Hv;
-  const long n = (chunks + 511) / 512;
-  return (int)(n < 4 ? 4 : n) * kLinChunk;
+  const long work = (p.tokens + kLinChunk - 1) / kLinChunk * p.Hv * ((p.dv + 127) / 128);
+  const long n = (work + 511) / 512;
+  return (int)(work <= 384 ? 1 : work <= 768 ? 2 : n < 4 ? 4 : n) * kLinChunk;
 }
 
 struct Inputs {

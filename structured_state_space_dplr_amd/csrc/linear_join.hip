@@ -10,29 +10,39 @@ namespace {
 // segment (rev: behind the last), slot m takes the state before segment m (behind it),
 //   run <- decay_m run + added_m.
 // Bound by the states' read and write; the next slots' loads go ahead of the sums.
+// V: elements a lane, 4 where a state is a multiple of them.
+template <int V>
 __global__ __launch_bounds__(256) void linear_scan_kernel(const LinPass p) {
+  typedef float Vf __attribute__((ext_vector_type(V)));
   const int s = blockIdx.x / p.Hv, h = blockIdx.x % p.Hv;
   const LinRows r = lin_rows(p, s);
   if (r.len <= p.segment) return;
-  const long sz = (long)p.dk * p.dv, at = (long)blockIdx.y * 256 + threadIdx.x;
+  const long sz = (long)p.dk * p.dv, at = ((long)blockIdx.y * 256 + threadIdx.x) * V;
   if (at >= sz) return;
   const long base = r.slot(s, p.segment);
   int n = r.segments(p.segment);
   if (base + n > p.slots) n = (int)(p.slots - base);
-  float run = p.first ? p.first[((size_t)s * p.Hv + h) * sz + at] : 0.f;
+  Vf run = {};
+  if (p.first) __builtin_memcpy(&run, p.first + ((size_t)s * p.Hv + h) * sz + at, sizeof(run));
   constexpr int AHEAD = 8;
   for (int m0 = 0; m0 < n; m0 += AHEAD) {
-    float add[AHEAD], dec[AHEAD];
+    Vf add[AHEAD];
+    float dec[AHEAD];
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
       const int m = m0 + i < n ? m0 + i : n - 1;
       const size_t slot = (size_t)(base + (p.rev ? n - 1 - m : m)) * p.Hv + h;
-      add[i] = p.states[slot * sz + at];
+      __builtin_memcpy(&add[i], p.states + slot * sz + at, sizeof(Vf));
       dec[i] = p.decay[slot];
     }
 #pragma unroll
     for (int i = 0; i < AHEAD; ++i) {
-      touch(add[i]);
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        float v = add[i][e];
+        touch(v);
+        add[i][e] = v;
+      }
       touch(dec[i]);
     }
 #pragma unroll
@@ -40,8 +50,9 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinPass p) {
       const int m = m0 + i;
       if (m >= n) break;
       const size_t slot = (size_t)(base + (p.rev ? n - 1 - m : m)) * p.Hv + h;
-      p.states[slot * sz + at] = run;
-      run = fmaf(dec[i], run, add[i]);   // behind the last one: not used
+      __builtin_memcpy(p.states + slot * sz + at, &run, sizeof(Vf));
+#pragma unroll
+      for (int e = 0; e < V; ++e) run[e] = fmaf(dec[i], run[e], add[i][e]);   // behind the last: not used
     }
   }
 }
@@ -193,7 +204,11 @@ hipError_t launch_linear_sums(const LinPass& a, int dtype, hipStream_t s) {
   const hipError_t e = pass(a, true, dtype, s);
   if (e != hipSuccess) return e;
   const long sz = (long)a.dk * a.dv;
-  linear_scan_kernel<<<dim3((unsigned)(a.sequences * a.Hv), (unsigned)((sz + 255) / 256)), 256, 0, s>>>(a);
+  const unsigned heads = (unsigned)(a.sequences * a.Hv);
+  if (sz % 4 == 0)
+    linear_scan_kernel<4><<<dim3(heads, (unsigned)((sz + 1023) / 1024)), 256, 0, s>>>(a);
+  else
+    linear_scan_kernel<1><<<dim3(heads, (unsigned)((sz + 255) / 256)), 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
