@@ -42,12 +42,12 @@ constexpr int kDotParts = 16;    // waves that share the columns of a head, at m
 
 // Longest sequence that is taken token by token.  Token by token against by chunks, 16 heads of 128
 // x 128 (us): bf16, 128 sequences, 4 tokens 64.2 against 66.6, 6 tokens 80.4 against 60.0; 16
-// sequences, 4 tokens 12.8 against 12.9; one, 6 tokens 10.0 against 10.7.  fp16 (two parts an element):
+// sequences, 4 tokens 12.8 against 12.9, 6 tokens 15.3 against 12.7; one, 6 tokens 10.0 against 10.7.  fp16 (two parts an element):
 // 128 sequences, 8 tokens 94 against 108; 16 sequences, 6 tokens 15.9 against 15.3; one, 8 tokens
 // 12.6 against 12.9.  fp32 (three parts): 128 sequences, 24 tokens 215 against 216; 16 sequences, 16
 // tokens 29.1 against 29.8; one, 8 tokens 11.2 against 14.5, 16 tokens 18.6 against 14.4.
 inline int lin_step_limit(const s4dplr_linear_attention_plan* p) {
-  if (p->dtype == S4DPLR_BF16) return 4;
+  if (p->dtype == S4DPLR_BF16) return 5;
   if (p->dtype == S4DPLR_F16) return 6;
   return (long)p->sequences * p->Hv > 128 ? 16 : 10;
 }
