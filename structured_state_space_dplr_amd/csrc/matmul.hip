@@ -19,6 +19,7 @@ namespace s4 {
 namespace {
 
 typedef int v8i __attribute__((ext_vector_type(8)));
+typedef int v4i __attribute__((ext_vector_type(4)));
 typedef float v4f __attribute__((ext_vector_type(4)));
 typedef __bf16 v8bf __attribute__((ext_vector_type(8)));
 typedef __bf16 v2bf __attribute__((ext_vector_type(2)));
@@ -28,19 +29,40 @@ constexpr int kK = 128;   // values along K a step: one group
 // What lies behind a matrix's last column.
 __device__ __attribute__((aligned(16))) const unsigned kZeros[4] = {0, 0, 0, 0};
 
-// The scales of groups kb .. kb + 3 of a row, byte 0 the first (behind the row's end anything).
-__device__ __forceinline__ unsigned scales4(const unsigned char* __restrict__ row, int kb, int n) {
-  if (n >= 4) {   // the same for all lanes
-    const int at = kb < n - 4 ? kb : n - 4;
-    unsigned t;
-    __builtin_memcpy(&t, row + at, 4);
-    return t >> (8 * (kb - at));
-  }
-  unsigned t = 0;
+// The scales of groups kb .. kb + 3 of R rows, byte 0 the first (behind a row's end anything).
+template <int R>
+__device__ __forceinline__ void scales4(const unsigned char* const (&row)[R], int kb, int n,
+                                        unsigned (&out)[R]) {
+  if (n >= 4) {   // the same for all lanes, and no load under another condition
+    const int at = kb < n - 4 ? kb : n - 4, shift = 8 * (kb - at);
 #pragma unroll
-  for (int i = 0; i < 3; ++i)
-    if (kb + i < n) t |= (unsigned)row[kb + i] << (8 * i);
-  return t;
+    for (int i = 0; i < R; ++i) __builtin_memcpy(&out[i], row[i] + at, 4);
+#pragma unroll
+    for (int i = 0; i < R; ++i) out[i] = shift < 32 ? out[i] >> shift : 0;
+  } else {
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      out[i] = 0;
+      for (int j = 0; kb + j < n; ++j) out[i] |= (unsigned)row[i][kb + j] << (8 * j);
+    }
+  }
+}
+
+// Bytes k .. k + 16 of a row of K, zeros behind its end.
+__device__ __forceinline__ v4i piece16(const unsigned char* __restrict__ row, int k, int K) {
+  v4i x = {0, 0, 0, 0};
+  if (k + 16 <= K) {
+    __builtin_memcpy(&x, row + k, 16);
+  } else if (k < K) {
+    unsigned long lo = 0, hi = 0;
+    for (int j = 0; k + j < K; ++j) {
+      const unsigned long v = row[k + j];
+      if (j < 8) lo |= v << (8 * j);
+      else hi |= v << (8 * (j - 8));
+    }
+    x = v4i{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
+  }
+  return x;
 }
 
 __device__ __forceinline__ float scale_value(unsigned byte) {   // 2^(byte - 127), NaN for 255
@@ -95,17 +117,53 @@ __device__ __forceinline__ bool tile_of(int mt, int nt, int* m, int* n) {
 
 }  // namespace
 
+// The operand that a lane holds: 32 bytes of row lane % 16 behind byte 32 (lane / 16) of a group.
+// c += b a for MT x NT tiles of 16 x 16, one group along K; sa, sb: the groups' scales in byte 0.
+template <typename T, int MT, int NT, typename FA, typename FB>
+__device__ __forceinline__ void group_product(FA a_of, FB b_of, const unsigned (&sa)[MT],
+                                              const unsigned (&sb)[NT], v4f (&acc)[MT][NT]) {
+  if constexpr (sizeof(T) == 4) {
+    v8bf a[MT][4];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) widen(a_of(i), scale_value(sa[i] & 255), a[i]);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      v8bf b[4];
+      widen(b_of(j), scale_value(sb[j] & 255), b);
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+          acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[q], a[i][q], acc[i][j], 0, 0, 0);
+    }
+  } else {
+    v8i a[MT];
+#pragma unroll
+    for (int i = 0; i < MT; ++i) a[i] = a_of(i);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const v8i b = b_of(j);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+        acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+            b, a[i], acc[i][j], 0, 0, 0, (int)sb[j], 0, (int)sa[i]);
+    }
+  }
+}
+
 // A block takes BM x BN of out, a wave WM x WN of it.  Both operands' next step is on its way
-// to the other half of LDS while one is computed: 128 rows of 128 bytes, 16-byte piece p of row
-// r at p ^ (r / 2 % 8), so that the 16 rows of an operand's read lie in different banks.
+// to the other half of LDS while one is computed: rows of 128 bytes, 16-byte piece p of row
+// r at p ^ (r / 2 % 8), so that the 16 rows of an operand's read lie in different banks.  The
+// halves are two variables and their steps written out in turn, without which the compiler waits
+// for the loads before it reads the other half.
 // WHOLE: rows start at multiples of 16 bytes and K is one, so that pieces are whole and go to LDS
 // without registers.
 template <typename T, int BM, int BN, int WM, int WN, bool WHOLE>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_kernel(const MatmulArgs p) {
-  constexpr bool kExact = sizeof(T) == 4;
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(const MatmulArgs p) {
   constexpr int WAVES = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
-  constexpr int LOADS = (BM + BN) / 8;   // of 8 rows, 16 bytes a lane
-  __shared__ __attribute__((aligned(16))) unsigned char lds[2][(BM + BN) * kK];
+  constexpr int LOADS = (BM + BN) / 8 / WAVES, LEFT = BM / 8 / WAVES;   // of 8 rows, 16 bytes a lane
+  static_assert(LOADS * 8 * WAVES == BM + BN && LEFT * 8 * WAVES == BM, "");
+  __shared__ __attribute__((aligned(16))) unsigned char lds0[(BM + BN) * kK], lds1[(BM + BN) * kK];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int m0, n0;
   if (!tile_of((p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &m0, &n0)) return;
@@ -114,41 +172,58 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_kernel(cons
   const int wm = w / (BN / WN) * WM, wn = w % (BN / WN) * WN;
   const int steps = (p.K + kK - 1) / kK;
 
-  auto stage = [&](int kb, int buf) {
+  // rows of the block's loads as offsets of 32 bits (256 rows of less than 2^24 bytes)
+  const unsigned char* const base_a = p.a + (long)m0 * p.lda;
+  const unsigned char* const base_b = p.b + (long)n0 * p.ldb;
+  unsigned from[LOADS];
+  const int lrow = lane / 8;
+  // 8 rows a load: those of a wave's loads are 8 WAVES apart, their turn is that of the first
+  static_assert(8 * WAVES % 16 == 0, "");
+  const int piece = (lane % 8) ^ ((8 * w + lrow) / 2 % 8);
 #pragma unroll
-    for (int i = 0; i < (LOADS + WAVES - 1) / WAVES; ++i) {
-      const int at = i * WAVES + w;
-      if (LOADS % WAVES && at >= LOADS) break;
-      const int r = at * 8 + lane / 8, piece = (lane % 8) ^ (r / 2 % 8);
-      const bool left = at < BM / 8;
-      const int most = (left ? p.M : p.N) - 1;
-      int row = left ? m0 + r : n0 + r - BM;
-      row = row < most ? row : most;   // rows behind the end: the last one, not stored
-      const unsigned char* src = left ? p.a + (long)row * p.lda : p.b + (long)row * p.ldb;
-      const int k = kb * kK + piece * 16;
-      if constexpr (WHOLE) {
-        src = k < p.K ? src + k : reinterpret_cast<const unsigned char*>(kZeros);
+  for (int i = 0; i < LOADS; ++i) {
+    const bool left = i < LEFT;
+    const int r = ((left ? i : i - LEFT) * WAVES + w) * 8 + lrow;
+    const int most = (left ? p.M - m0 : p.N - n0) - 1;   // rows behind the end: the last one, not stored
+    from[i] = (unsigned)(r < most ? r : most) * (unsigned)(left ? p.lda : p.ldb) + 16 * piece;
+  }
+  v4i held[WHOLE ? 1 : LOADS];   // without whole pieces: the next step's, on their way to LDS
+  auto stage = [&](int kb, unsigned char* lds) {
+    const bool full = (kb + 1) * kK <= p.K;
+    const int k = kb * kK + 16 * piece;
+    if constexpr (WHOLE) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i) {
+        const unsigned char* at = (i < LEFT ? base_a : base_b) + kb * kK + from[i];
+        if (!full) at = k < p.K ? at : reinterpret_cast<const unsigned char*>(kZeros);
         __builtin_amdgcn_global_load_lds(
-            (const __attribute__((address_space(1))) void*)src,
-            (__attribute__((address_space(3))) void*)&lds[buf][at * 1024], 16, 0, 0);
-      } else {
-        unsigned char t[16];
-        if (k + 16 <= p.K) {
-          __builtin_memcpy(t, src + k, 16);
-        } else {
-#pragma unroll
-          for (int j = 0; j < 16; ++j) t[j] = k + j < p.K ? src[k + j] : 0;
-        }
-        __builtin_memcpy(&lds[buf][at * 1024 + lane * 16], t, 16);
+            (const __attribute__((address_space(1))) void*)at,
+            (__attribute__((address_space(3))) void*)(lds + (i * WAVES + w) * 1024), 16, 0, 0);
       }
+    } else if (full) {   // pieces at any address
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        __builtin_memcpy(&held[i], (i < LEFT ? base_a : base_b) + kb * kK + from[i], 16);
+    } else {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        held[i] = piece16((i < LEFT ? base_a : base_b) + from[i] - 16 * piece, k, p.K);
     }
   };
-  auto operand = [&](int buf, int row) {   // row: a multiple of 16
-    const int r = lane & 15, g = lane >> 4;
-    const unsigned char* at = &lds[buf][(row + r) * kK];
+  auto commit = [&](unsigned char* lds) {
+    if constexpr (!WHOLE) {
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        *reinterpret_cast<v4i*>(lds + (i * WAVES + w) * 1024 + lane * 16) = held[i];
+    }
+  };
+  const int r16 = lane & 15, g = lane >> 4;
+  const int piece0 = ((2 * g) ^ (r16 / 2)) * 16, piece1 = piece0 ^ 16;
+  auto operand = [&](const unsigned char* lds, int row) {   // row: a multiple of 16
+    const unsigned char* at = lds + (row + r16) * kK;
     v8i x;
-    __builtin_memcpy(&x, at + ((2 * g) ^ (r / 2)) * 16, 16);
-    __builtin_memcpy((char*)&x + 16, at + ((2 * g + 1) ^ (r / 2)) * 16, 16);
+    __builtin_memcpy(&x, at + piece0, 16);
+    __builtin_memcpy((char*)&x + 16, at + piece1, 16);
     return x;
   };
 
@@ -157,70 +232,162 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) void matmul_kernel(cons
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j) acc[i][j] = v4f{0.f, 0.f, 0.f, 0.f};
-  // rows of the scales that this lane's rows have
-  const unsigned char *sa[MT], *sb[NT];
+  const unsigned char *sa[MT], *sb[NT];   // the scales of this lane's rows
 #pragma unroll
   for (int i = 0; i < MT; ++i) {
-    const int m = m0 + wm + 16 * i + (lane & 15);
+    const int m = m0 + wm + 16 * i + r16;
     sa[i] = p.sa + (long)(m < p.M ? m : p.M - 1) * steps;
   }
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    int n = n0 + wn + 16 * j + (lane & 15);
+    int n = n0 + wn + 16 * j + r16;
     n = n < p.N ? n : p.N - 1;
     sb[j] = p.sb + (long)(p.square ? n / kGroup : n) * steps;
   }
-  unsigned ea[MT], eb[NT];
-  if (steps > 0) stage(0, 0);
-  for (int kb = 0; kb < steps; ++kb) {
-    if (kb % 4 == 0) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i) ea[i] = scales4(sa[i], kb, steps);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) eb[j] = scales4(sb[j], kb, steps);
-    }
+  unsigned ea[MT], eb[NT], na[MT], nb[NT];   // of four steps, and of the next four
+  auto step = [&](int kb, const unsigned char* here, unsigned char* there) {
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __syncthreads();
-    if (kb + 1 < steps) stage(kb + 1, (kb + 1) & 1);
-    const int buf = kb & 1;
-    if constexpr (kExact) {
-      v8bf a[MT][4];
+    if (kb % 4 == 0) {
 #pragma unroll
-      for (int i = 0; i < MT; ++i) widen(operand(buf, wm + 16 * i), scale_value(ea[i] & 255), a[i]);
+      for (int i = 0; i < MT; ++i) ea[i] = na[i];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        v8bf b[4];
-        widen(operand(buf, BM + wn + 16 * j), scale_value(eb[j] & 255), b);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            acc[i][j] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(b[q], a[i][q], acc[i][j], 0, 0, 0);
-      }
-    } else {
-      v8i a[MT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) a[i] = operand(buf, wm + 16 * i);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const v8i b = operand(buf, BM + wn + 16 * j);
-#pragma unroll
-        for (int i = 0; i < MT; ++i)
-          acc[i][j] = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-              b, a[i], acc[i][j], 0, 0, 0, (int)eb[j], 0, (int)ea[i]);
+      for (int j = 0; j < NT; ++j) eb[j] = nb[j];
+      if (kb + 4 < steps) {
+        scales4<MT>(sa, kb + 4, steps, na);
+        scales4<NT>(sb, kb + 4, steps, nb);
       }
     }
+    if (kb + 1 < steps) stage(kb + 1, there);
+    group_product<T, MT, NT>([&](int i) { return operand(here, wm + 16 * i); },
+                             [&](int j) { return operand(here, BM + wn + 16 * j); }, ea, eb, acc);
+    if (kb + 1 < steps) commit(there);
 #pragma unroll
     for (int i = 0; i < MT; ++i) ea[i] >>= 8;
 #pragma unroll
     for (int j = 0; j < NT; ++j) eb[j] >>= 8;
+  };
+  if (steps > 0) {
+    scales4<MT>(sa, 0, steps, na);
+    scales4<NT>(sb, 0, steps, nb);
+    stage(0, lds0);
+    commit(lds0);
+  }
+  for (int kb = 0; kb < steps; kb += 2) {
+    step(kb, lds0, lds1);
+    if (kb + 1 < steps) step(kb + 1, lds1, lds0);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
 #pragma unroll
     for (int j = 0; j < NT; ++j)
-      store4((T*)p.out, p.ldo, m0 + wm + 16 * i + (lane & 15), n0 + wn + 16 * j + 4 * (lane >> 4),
-             p.M, p.N, acc[i][j]);
+      store4((T*)p.out, p.ldo, m0 + wm + 16 * i + r16, n0 + wn + 16 * j + 4 * g, p.M, p.N, acc[i][j]);
+}
+
+// Few rows of out (M <= 16 MT): bound by B's bytes.  A block takes 16 columns of out; its waves share
+// out the groups along K, each by itself and without barriers, up to three groups on their way to
+// its own part of LDS, and their sums are added up in a fixed order.  (Operands
+// read to registers take a cache access for every 16 bytes, since neighbouring lanes hold different
+// rows: 32 x 6144 x 4096 18.3 us.)
+template <typename T, int MT, int WAVES, bool WHOLE>
+__global__ __launch_bounds__(64 * WAVES) void matmul_few_kernel(const MatmulArgs p) {
+  constexpr int LOADS = 2 * (MT + 1), BYTES = LOADS * 1024;
+  __shared__ __attribute__((aligned(16))) unsigned char lds0[WAVES * BYTES], lds1[WAVES * BYTES],
+      lds2[WAVES * BYTES];
+  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int r16 = lane & 15, g = lane >> 4;
+  const int groups = (p.K + kK - 1) / kK, n0 = blockIdx.x * 16;
+  const int mine = groups > w ? (groups - w + WAVES - 1) / WAVES : 0;   // groups w, w + WAVES, ...
+
+  // rows of a group's loads: A's 16 MT, then B's 16; those behind the end: the last one, not stored
+  const unsigned char* row[LOADS];
+  const int piece = (lane % 8) ^ (lane / 8 / 2 % 8);   // of even loads; of odd ones, whose rows are 8 on, ^ 4
+#pragma unroll
+  for (int i = 0; i < LOADS; ++i) {
+    const bool left = i < 2 * MT;
+    const int r = (left ? i : i - 2 * MT) * 8 + lane / 8, most = (left ? p.M : p.N - n0) - 1;
+    const int at = r < most ? r : most;
+    row[i] = left ? p.a + (long)at * p.lda : p.b + (long)(n0 + at) * p.ldb;
+  }
+  const unsigned char* srow[MT + 1];   // the scales of this lane's rows, B's last
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    const int m = 16 * i + r16 < p.M ? 16 * i + r16 : p.M - 1;
+    srow[i] = p.sa + (long)m * groups;
+  }
+  const int n = n0 + r16 < p.N ? n0 + r16 : p.N - 1;
+  srow[MT] = p.sb + (long)(p.square ? n / kGroup : n) * groups;
+
+  v4f acc[MT][1];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i][0] = v4f{0.f, 0.f, 0.f, 0.f};
+  v4i held[WHOLE ? 1 : LOADS];
+  unsigned e0[MT + 1], e1[MT + 1], e2[MT + 1];
+  auto stage = [&](int j, unsigned char* lds, unsigned (&e)[MT + 1]) {
+    if (j >= mine) return;
+    const int kb = w + j * WAVES;
+    const bool full = (kb + 1) * kK <= p.K;
+#pragma unroll
+    for (int i = 0; i < LOADS; ++i) {
+      const int k = kb * kK + 16 * (i % 2 ? piece ^ 4 : piece);
+      if constexpr (WHOLE) {
+        const unsigned char* at = row[i] + k;
+        if (!full) at = k < p.K ? at : reinterpret_cast<const unsigned char*>(kZeros);
+        __builtin_amdgcn_global_load_lds(
+            (const __attribute__((address_space(1))) void*)at,
+            (__attribute__((address_space(3))) void*)(lds + w * BYTES + i * 1024), 16, 0, 0);
+      } else if (full) {
+        __builtin_memcpy(&held[i], row[i] + k, 16);
+      } else {
+        held[i] = piece16(row[i], k, p.K);
+      }
+    }
+#pragma unroll
+    for (int i = 0; i <= MT; ++i) e[i] = srow[i][kb];
+    if constexpr (!WHOLE)
+#pragma unroll
+      for (int i = 0; i < LOADS; ++i)
+        *reinterpret_cast<v4i*>(lds + w * BYTES + i * 1024 + lane * 16) = held[i];
+  };
+  auto step = [&](int j, const unsigned char* lds, const unsigned (&e)[MT + 1]) {
+    if (j >= mine) return;
+    auto operand = [&](int tile) {
+      const unsigned char* at = lds + w * BYTES + (tile * 16 + r16) * kK;
+      v8i x;
+      __builtin_memcpy(&x, at + ((2 * g) ^ (r16 / 2)) * 16, 16);
+      __builtin_memcpy((char*)&x + 16, at + ((2 * g + 1) ^ (r16 / 2)) * 16, 16);
+      return x;
+    };
+    unsigned ea[MT], eb[1] = {e[MT]};
+#pragma unroll
+    for (int i = 0; i < MT; ++i) ea[i] = e[i];
+    group_product<T, MT, 1>([&](int i) { return operand(i); }, [&](int) { return operand(MT); }, ea, eb, acc);
+  };
+  stage(0, lds0, e0);
+  stage(1, lds1, e1);
+  stage(2, lds2, e2);
+  for (int j = 0; j < mine; j += 3) {
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");   // three groups are there
+    step(j, lds0, e0);
+    stage(j + 3, lds0, e0);
+    step(j + 1, lds1, e1);
+    stage(j + 4, lds1, e1);
+    step(j + 2, lds2, e2);
+    stage(j + 5, lds2, e2);
+  }
+  // the sums: of tile i by wave i
+  v4f(*sums)[MT][64] = reinterpret_cast<v4f(*)[MT][64]>(lds0);
+  static_assert(WAVES * MT * 64 * 16 <= WAVES * BYTES, "");
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < MT; ++i) sums[w][i][lane] = acc[i][0];
+  __syncthreads();
+  for (int i = w; i < MT; i += WAVES) {
+    v4f c = sums[0][i][lane];
+#pragma unroll
+    for (int q = 1; q < WAVES; ++q) c += sums[q][i][lane];
+    store4((T*)p.out, p.ldo, 16 * i + r16, n0 + 4 * g, p.M, p.N, c);
+  }
 }
 
 namespace {
@@ -231,7 +398,15 @@ hipError_t tiles(const MatmulArgs& a, bool whole, hipStream_t s) {
   const unsigned grid = (unsigned)((n + 7) / 8 * 8);
   constexpr int threads = (BM / WM) * (BN / WN) * 64;
   if (whole) matmul_kernel<T, BM, BN, WM, WN, true><<<grid, threads, 0, s>>>(a);
-  else matmul_kernel<T, BM, BN, WM, WN, false><<<grid, threads, 0, s>>>(a);
+  else if constexpr (BM <= 128) matmul_kernel<T, BM, BN, WM, WN, false><<<grid, threads, 0, s>>>(a);
+  return hipGetLastError();
+}
+
+template <typename T, int MT, int WAVES>
+hipError_t few(const MatmulArgs& a, bool whole, hipStream_t s) {
+  const unsigned grid = (unsigned)((a.N + 15) / 16);
+  if (whole) matmul_few_kernel<T, MT, WAVES, true><<<grid, 64 * WAVES, 0, s>>>(a);
+  else matmul_few_kernel<T, MT, WAVES, false><<<grid, 64 * WAVES, 0, s>>>(a);
   return hipGetLastError();
 }
 
@@ -239,7 +414,13 @@ template <typename T>
 hipError_t matmul(const MatmulArgs& a, hipStream_t s) {
   const bool whole = ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) |
                        (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) & 15) == 0;
-  return tiles<T, 128, 128, 64, 64>(a, whole, s);
+  if (a.M <= 64)
+    return a.M <= 16 ? few<T, 1, 8>(a, whole, s) : a.M <= 32 ? few<T, 2, 8>(a, whole, s) : few<T, 4, 4>(a, whole, s);
+  auto blocks = [&](int bm, int bn) { return (long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  if constexpr (sizeof(T) == 2)
+    if (whole && blocks(256, 256) >= 256) return tiles<T, 256, 256, 64, 128>(a, true, s);
+  if (blocks(128, 128) >= 256) return tiles<T, 128, 128, 64, 64>(a, whole, s);
+  return tiles<T, 64, 64, 32, 32>(a, whole, s);
 }
 
 }  // namespace
