@@ -416,10 +416,17 @@ hipError_t matmul(const MatmulArgs& a, hipStream_t s) {
                        (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) & 15) == 0;
   if (a.M <= 64)
     return a.M <= 16 ? few<T, 1, 8>(a, whole, s) : a.M <= 32 ? few<T, 2, 8>(a, whole, s) : few<T, 4, 4>(a, whole, s);
+  // Tiles of 128 where they fill the CUs, of 64 below (bf16, K = 4096, us): 512 x 4096, 128 tiles, 64
+  // 23.9, 128 33.2; 1024 x 4096, 256 tiles, 64 36.6, 128 35.6; 2048 x 4096 66.1 and 47.7.  Tiles of 256,
+  // whose operands are read from LDS half as often, one a CU: a round of them takes what 5 / 3 rounds
+  // of 128, two a CU, do: 8192 x 2048 256 72.4, 128 82.3; 3000 x 4096 71.3 and 81.9; 4096 x 6144 (384
+  // tiles, two rounds) 138 and 124; 2048 x 4096 70.2 and 47.7.  Their float32 form spills.
   auto blocks = [&](int bm, int bn) { return (long)((a.M + bm - 1) / bm) * ((a.N + bn - 1) / bn); };
+  const long half = blocks(128, 128);
   if constexpr (sizeof(T) == 2)
-    if (whole && blocks(256, 256) >= 256) return tiles<T, 256, 256, 64, 128>(a, true, s);
-  if (blocks(128, 128) >= 256) return tiles<T, 128, 128, 64, 64>(a, whole, s);
+    if (whole && (blocks(256, 256) + 255) / 256 * 5 <= (half + 511) / 512 * 3)
+      return tiles<T, 256, 256, 64, 128>(a, true, s);
+  if (half >= 256) return tiles<T, 128, 128, 64, 64>(a, whole, s);
   return tiles<T, 64, 64, 32, 32>(a, whole, s);
 }
 
