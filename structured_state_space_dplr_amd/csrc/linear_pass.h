@@ -97,19 +97,19 @@ struct LinTile {
   __device__ __forceinline__ void fetch(const unsigned char* base, unsigned ld, int n, int rev, int c0,
                                         int d) {
     const unsigned tid = thread(), r0 = tid / (COLS / 8);
-    const int c = c0 + (int)(tid % (COLS / 8) * 8), step = rev ? -STEP : STEP;
+    const int c = c0 + (int)(tid % (COLS / 8) * 8);
+    const unsigned pitch = ld * (unsigned)sizeof(T);
     if (n == C) {
-      const unsigned first = rev ? C - 1 - r0 : r0;
+      const unsigned first = (rev ? C - 1 - r0 : r0) * pitch, step = rev ? 0u - STEP * pitch : STEP * pitch;
 #pragma unroll
-      for (int i = 0; i < N; ++i)
-        fetch8<T, WHOLE>(base, first * (ld * (unsigned)sizeof(T)) + i * (step * (int)ld * (int)sizeof(T)), c, d, v[i]);
+      for (int i = 0; i < N; ++i) fetch8<T, WHOLE>(base, first + i * step, c, d, v[i]);
     } else {
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         int row = (int)r0 + i * STEP;
         row = row < n ? row : n - 1;   // behind the end: a row that is there, unused
         row = rev ? n - 1 - row : row;
-        fetch8<T, WHOLE>(base, (unsigned)row * (ld * (unsigned)sizeof(T)), c, d, v[i]);
+        fetch8<T, WHOLE>(base, (unsigned)row * pitch, c, d, v[i]);
       }
     }
   }
@@ -527,7 +527,7 @@ void linear_pass_kernel(const LinPass p) {
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
                 __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if (MODE == kGrad && p.dot) {
+              if (MODE == kGrad && p.dot) {   // (loaded earlier, its registers would be spilled)
                 T t[4];
                 __builtin_memcpy(t, db + ((unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T)) +
                                           (col + e0) * (unsigned)sizeof(T)), sizeof(T) * m);
@@ -546,8 +546,10 @@ void linear_pass_kernel(const LinPass p) {
           }
         }
         if (MODE == kGrad && p.dot) {   // over the lanes that share the row
-          sum += __shfl_xor(sum, 16);
-          sum += __shfl_xor(sum, 32);
+          const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+          sum = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+          const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+          sum = __uint_as_float(b[0]) + __uint_as_float(b[1]);
           if (lg == 0 && i < n) to[row] = sum;
         }
       }

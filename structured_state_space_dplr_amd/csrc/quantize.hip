@@ -12,14 +12,18 @@
 
 namespace s4 {
 
+namespace {
+constexpr int kThreads = 512;
+}
+
 template <typename T>
-__global__ __launch_bounds__(256) void quantize_kernel(const QuantizeArgs a) {
+__global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a) {
   constexpr int VEC = Vec<T>::N;          // columns a lane
   constexpr int LANES = kGroup / VEC;     // lanes a row
-  constexpr int SETS = 256 / LANES;       // sets of neighbouring rows
+  constexpr int SETS = kThreads / LANES;      // sets of neighbouring rows
   constexpr int R = kGroup / SETS;        // rows a set
   __shared__ unsigned red[SETS][kGroup];
-  __shared__ unsigned all[4];
+  __shared__ unsigned all[kThreads / 64];
   // byte (c, r) of the transposed tile at 128 c + R (set ^ (c / VEC)) + r % R, so that the lanes of a
   // write lie apart
   __shared__ __attribute__((aligned(16))) unsigned char turned[kGroup * kGroup];
@@ -29,18 +33,36 @@ __global__ __launch_bounds__(256) void quantize_kernel(const QuantizeArgs a) {
   const int cg = (a.cols + kGroup - 1) / kGroup, rg = (a.rows + kGroup - 1) / kGroup;
   const T* x = (const T*)a.x;
   float v[R][VEC];
+  if (r0 + kGroup <= a.rows && c0 + kGroup <= a.cols) {
+    Vec<T> t[R];
 #pragma unroll
-  for (int i = 0; i < R; ++i) {
-    const T* p = x + (long)(row + i) * a.ldx + col;
-    if (row + i < a.rows && col + VEC <= a.cols) {
-      const Vec<T> t = load_vec(p);
+    for (int i = 0; i < R; ++i) t[i] = load_vec(x + (long)(row + i) * a.ldx + col);
 #pragma unroll
-      for (int j = 0; j < VEC; ++j) v[i][j] = to_f32(t.v[j]);
-    } else {
+    for (int i = 0; i < R; ++i)
 #pragma unroll
-      for (int j = 0; j < VEC; ++j)
-        v[i][j] = row + i < a.rows && col + j < a.cols ? to_f32(p[j]) : 0.f;
+      for (int j = 0; j < VEC; ++j) v[i][j] = to_f32(t[i].v[j]);
+  } else {
+    // at the edge: every load from inside, all on their way together, and zeros behind the ends
+    T t[R][VEC];
+    const bool whole = a.cols % VEC == 0;
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      const T* p = x + (long)(row + i < a.rows ? row + i : a.rows - 1) * a.ldx;
+      if (whole) {
+        __builtin_memcpy(t[i], p + (col < a.cols ? col : 0), sizeof(t[i]));
+      } else {
+#pragma unroll
+        for (int j = 0; j < VEC; ++j) t[i][j] = p[col + j < a.cols ? col + j : 0];
+      }
     }
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) {
+        float f = to_f32(t[i][j]);
+        asm volatile("" : "+v"(f));   // or the loads are put under the condition, one by one
+        v[i][j] = row + i < a.rows && col + j < a.cols ? f : 0.f;
+      }
   }
   unsigned block = 0;   // scale of the whole tile
   if (a.square) {
@@ -58,7 +80,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const QuantizeArgs a) {
     if (tid % 64 == 0) all[tid / 64] = big;
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) big = all[i] > big ? all[i] : big;
+    for (int i = 0; i < kThreads / 64; ++i) big = all[i] > big ? all[i] : big;
     block = scale_byte(big);
     if (tid == 0) {
       if (a.q) a.scales[(long)blockIdx.y * cg + blockIdx.x] = (unsigned char)block;
@@ -128,7 +150,7 @@ __global__ __launch_bounds__(256) void quantize_kernel(const QuantizeArgs a) {
     __builtin_memcpy(&turned[(lane * VEC + j) * kGroup + R * (set ^ (lane % SETS))], t, R);
   }
   __syncthreads();
-  constexpr int STEP = 256 / SETS;   // columns a pass
+  constexpr int STEP = kThreads / SETS;   // columns a pass
   const int s = tid % SETS;
 #pragma unroll
   for (int i = 0; i < kGroup / STEP; ++i) {
@@ -150,9 +172,9 @@ __global__ __launch_bounds__(256) void quantize_kernel(const QuantizeArgs a) {
 
 hipError_t launch_quantize(const QuantizeArgs& a, int dtype, hipStream_t s) {
   const dim3 grid((unsigned)((a.cols + kGroup - 1) / kGroup), (unsigned)((a.rows + kGroup - 1) / kGroup));
-  if (dtype == S4DPLR_F32) quantize_kernel<float><<<grid, 256, 0, s>>>(a);
-  else if (dtype == S4DPLR_BF16) quantize_kernel<bf16><<<grid, 256, 0, s>>>(a);
-  else quantize_kernel<f16><<<grid, 256, 0, s>>>(a);
+  if (dtype == S4DPLR_F32) quantize_kernel<float><<<grid, kThreads, 0, s>>>(a);
+  else if (dtype == S4DPLR_BF16) quantize_kernel<bf16><<<grid, kThreads, 0, s>>>(a);
+  else quantize_kernel<f16><<<grid, kThreads, 0, s>>>(a);
   return hipGetLastError();
 }
 
