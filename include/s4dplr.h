@@ -609,7 +609,7 @@ s4dplr_status s4dplr_rms_norm_bwd(const void* h, const float* gamma, const float
  * with `square` both have the scales of 128 x 128 blocks, [ceil(rows / 128)][ceil(cols / 128)]
  * and its transpose.  Either pair may be NULL.  Every value is rounded once, to
  * nearest with ties to even.  No rows or columns: a no-op.
- * Limits: rows <= 2^22, cols and ldx < 2^24, ldx >= cols, fewer than 2^23 blocks (ERR_SHAPE).
+ * Limits: rows <= 2^22, cols and ldx < 2^24, ldx >= cols, fewer than 2^22 blocks (ERR_SHAPE).
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (dtype), ERR_HIP.
  */
 s4dplr_status s4dplr_quantize_fp8(const void* x, long ldx, void* q, void* scales, void* qt,
@@ -623,10 +623,11 @@ s4dplr_status s4dplr_quantize_fp8(const void* x, long ldx, void* q, void* scales
  * [N][ceil(K / 128)], with b_square [ceil(N / 128)][ceil(K / 128)].  out: elements of `dtype`,
  * rounded once.  Sums are fp32.  16-bit outputs come from the 8-bit matrix
  * instructions, which add up the products inside an instruction with fewer bits: off by about
- * 2^-16 of the result (7e-5 where a group's values span eight powers of two); a float32 output from
- * the bf16 ones, exact in every product.
+ * 2^-16 of the result's size (7e-5 where a group's values span 16 powers of two); a float32 output
+ * from the bf16 ones, exact in every product.
  * The layer's products: output X W^T (X by rows, W square), dX = dY W (dY by rows, W's
  * transpose, square), dW = dY^T X (the transposes of both, by their rows).
+ * For a float32 output, the values that the matrices stand for lie within float32.
  * M or N = 0 is a no-op, K = 0 writes zeros.  Limits: sizes and pitches below 2^24,
  * ceil(M / 64) ceil(N / 128) < 2^23 (ERR_SHAPE).
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (dtype), ERR_HIP.

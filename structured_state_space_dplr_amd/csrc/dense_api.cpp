@@ -109,8 +109,8 @@ s4dplr_status s4dplr_quantize_fp8(const void* x, long ldx, void* q, void* scales
   if (rows < 0 || cols < 0 || rows > kMostSize / 4 || cols >= kMostSize || ldx < cols ||
       ldx >= kMostSize)
     return S4DPLR_ERR_SHAPE;
-  // the launch's blocks, each of 256 threads, are counted in 32 bits
-  if (groups(rows) * groups(cols) >= (1u << 23)) return S4DPLR_ERR_SHAPE;
+  // a launch counts its threads, 512 a block, in 32 bits
+  if (groups(rows) * groups(cols) >= (1u << 22)) return S4DPLR_ERR_SHAPE;
   if (!q != !scales || !qt != !scales_t) return S4DPLR_ERR_NULL;
   if (rows == 0 || cols == 0 || (!q && !qt)) return S4DPLR_OK;
   if (!x) return S4DPLR_ERR_NULL;

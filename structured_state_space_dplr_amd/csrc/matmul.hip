@@ -3,7 +3,7 @@
 // The matrix instruction 16x16x128 takes 8-bit operands with a scale for each 32 values of a
 // row, so one instruction is a group's product with its scales applied, and nothing is
 // left for the vector units.  Inside, products are summed with fewer bits than fp32 has
-// (measured: off by 1.5e-5 of the result's norm for normal values, 7e-5 where they span eight
+// (measured: off by 1.5e-5 of the result's norm for normal values, 7e-5 where they span 16
 // powers of two), which outputs of 16 bits do not show; a float32 output is taken
 // by the bf16 instruction, whose products are exact and whose sums are fp32, after the 8 bits
 // and their scales are turned into bf16 (exact), at about half the rate.
@@ -325,6 +325,8 @@ __global__ __launch_bounds__(64 * WAVES) void matmul_few_kernel(const MatmulArgs
   unsigned e0[MT + 1], e1[MT + 1], e2[MT + 1];
   auto stage = [&](int j, unsigned char* lds, unsigned (&e)[MT + 1]) {
     if (j >= mine) return;
+    // the reads of what lay there are done before anything else comes there
+    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
     const int kb = w + j * WAVES;
     const bool full = (kb + 1) * kK <= p.K;
 #pragma unroll
