@@ -29,16 +29,18 @@ constexpr int kK = 128;   // values along K a step: one group
 // What lies behind a matrix's last column.
 __device__ __attribute__((aligned(16))) const unsigned kZeros[4] = {0, 0, 0, 0};
 
-// The scales of groups kb .. kb + 3 of R rows, byte 0 the first (behind a row's end anything).
+// The scales of groups kb .. kb + 3 of R rows (behind a row's end anything): byte 0 is the first once
+// they are shifted by scales_shift, which waits for the loads.
+__device__ __forceinline__ int scales_shift(int kb, int n) {
+  return n >= 4 && kb > n - 4 ? 8 * (kb - (n - 4)) : 0;
+}
 template <int R>
 __device__ __forceinline__ void scales4(const unsigned char* const (&row)[R], int kb, int n,
                                         unsigned (&out)[R]) {
   if (n >= 4) {   // the same for all lanes, and no load under another condition
-    const int at = kb < n - 4 ? kb : n - 4, shift = 8 * (kb - at);
+    const int at = kb < n - 4 ? kb : n - 4;
 #pragma unroll
     for (int i = 0; i < R; ++i) __builtin_memcpy(&out[i], row[i] + at, 4);
-#pragma unroll
-    for (int i = 0; i < R; ++i) out[i] = shift < 32 ? out[i] >> shift : 0;
   } else {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
@@ -158,12 +160,15 @@ __device__ __forceinline__ void group_product(FA a_of, FB b_of, const unsigned (
 // for the loads before it reads the other half.
 // WHOLE: rows start at multiples of 16 bytes and K is one, so that pieces are whole and go to LDS
 // without registers.
-template <typename T, int BM, int BN, int WM, int WN, bool WHOLE>
+// DEEP: three steps on their way to four buffers, for small tiles, whose steps are shorter than a load.
+template <typename T, int BM, int BN, int WM, int WN, bool WHOLE, bool DEEP>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(const MatmulArgs p) {
   constexpr int WAVES = (BM / WM) * (BN / WN), MT = WM / 16, NT = WN / 16;
   constexpr int LOADS = (BM + BN) / 8 / WAVES, LEFT = BM / 8 / WAVES;   // of 8 rows, 16 bytes a lane
   static_assert(LOADS * 8 * WAVES == BM + BN && LEFT * 8 * WAVES == BM, "");
-  __shared__ __attribute__((aligned(16))) unsigned char lds0[(BM + BN) * kK], lds1[(BM + BN) * kK];
+  constexpr int BYTES = (BM + BN) * kK;
+  __shared__ __attribute__((aligned(16))) unsigned char lds0[BYTES], lds1[BYTES],
+      lds2[DEEP ? BYTES : 16], lds3[DEEP ? BYTES : 16];
   const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   int m0, n0;
   if (!tile_of((p.M + BM - 1) / BM, (p.N + BN - 1) / BN, &m0, &n0)) return;
@@ -246,19 +251,30 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
   }
   unsigned ea[MT], eb[NT], na[MT], nb[NT];   // of four steps, and of the next four
   auto step = [&](int kb, const unsigned char* here, unsigned char* there) {
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __syncthreads();
+    // this step's loads are done: those of the steps behind it may be on their way, at least LOADS a step
+    if (DEEP && kb + 2 < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * LOADS) : "memory");
+    else if (DEEP && kb + 1 < steps) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(LOADS) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    if constexpr (DEEP) {
+      asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
+      __builtin_amdgcn_s_barrier();   // without a wait for all loads
+      asm volatile("" ::: "memory");
+    } else {
+      __syncthreads();
+    }
     if (kb % 4 == 0) {
+      const int shift = scales_shift(kb, steps);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) ea[i] = na[i];
+      for (int i = 0; i < MT; ++i) ea[i] = na[i] >> shift;
 #pragma unroll
-      for (int j = 0; j < NT; ++j) eb[j] = nb[j];
+      for (int j = 0; j < NT; ++j) eb[j] = nb[j] >> shift;
       if (kb + 4 < steps) {
         scales4<MT>(sa, kb + 4, steps, na);
         scales4<NT>(sb, kb + 4, steps, nb);
       }
     }
-    if (kb + 1 < steps) stage(kb + 1, there);
+    constexpr int ahead = DEEP ? 3 : 1;
+    if (kb + ahead < steps) stage(kb + ahead, there);
     group_product<T, MT, NT>([&](int i) { return operand(here, wm + 16 * i); },
                              [&](int j) { return operand(here, BM + wn + 16 * j); }, ea, eb, acc);
     if (kb + 1 < steps) commit(there);
@@ -273,9 +289,20 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
     stage(0, lds0);
     commit(lds0);
   }
-  for (int kb = 0; kb < steps; kb += 2) {
-    step(kb, lds0, lds1);
-    if (kb + 1 < steps) step(kb + 1, lds1, lds0);
+  if constexpr (DEEP) {
+    if (steps > 1) stage(1, lds1);
+    if (steps > 2) stage(2, lds2);
+    for (int kb = 0; kb < steps; kb += 4) {
+      step(kb, lds0, lds3);
+      if (kb + 1 < steps) step(kb + 1, lds1, lds0);
+      if (kb + 2 < steps) step(kb + 2, lds2, lds1);
+      if (kb + 3 < steps) step(kb + 3, lds3, lds2);
+    }
+  } else {
+    for (int kb = 0; kb < steps; kb += 2) {
+      step(kb, lds0, lds1);
+      if (kb + 1 < steps) step(kb + 1, lds1, lds0);
+    }
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i)
@@ -399,8 +426,8 @@ hipError_t tiles(const MatmulArgs& a, bool whole, hipStream_t s) {
   const long n = (long)((a.N + BN - 1) / BN) * ((a.M + BM - 1) / BM);
   const unsigned grid = (unsigned)((n + 7) / 8 * 8);
   constexpr int threads = (BM / WM) * (BN / WN) * 64;
-  if (whole) matmul_kernel<T, BM, BN, WM, WN, true><<<grid, threads, 0, s>>>(a);
-  else if constexpr (BM <= 128) matmul_kernel<T, BM, BN, WM, WN, false><<<grid, threads, 0, s>>>(a);
+  if (whole) matmul_kernel<T, BM, BN, WM, WN, true, BM == 64><<<grid, threads, 0, s>>>(a);
+  else if constexpr (BM <= 128) matmul_kernel<T, BM, BN, WM, WN, false, false><<<grid, threads, 0, s>>>(a);
   return hipGetLastError();
 }
 
