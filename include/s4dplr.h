@@ -621,13 +621,15 @@ s4dplr_status s4dplr_quantize_fp8(const void* x, long ldx, void* q, void* scales
  *   out_mn = sum over the groups g of sa_mg sb_ng sum_k a_mk b_nk   (k in group g).
  * lda, ldb, ldo: elements from one row to the next.  a_scales [M][ceil(K / 128)], b_scales
  * [N][ceil(K / 128)], with b_square [ceil(N / 128)][ceil(K / 128)].  out: elements of `dtype`,
- * rounded once.  Sums are fp32.  16-bit outputs come from the 8-bit matrix
- * instructions, which add up the products inside an instruction with fewer bits: off by about
- * 2^-16 of the result's size (7e-5 where a group's values span 16 powers of two); a float32 output
- * from the bf16 ones, exact in every product.
+ * rounded once.  Sums are fp32.  16-bit outputs come from the 8-bit matrix instructions, which add
+ * up the products inside an instruction with fewer bits: off by 1.5e-5 of the result's size for
+ * normally distributed values, 7e-5 where those of both operands span eight powers of two, up to
+ * about 2^-13 of a group's sum of magnitudes; a float32 output comes from the bf16 ones, exact in
+ * every product.
  * The layer's products: output X W^T (X by rows, W square), dX = dY W (dY by rows, W's
  * transpose, square), dW = dY^T X (the transposes of both, by their rows).
- * For a float32 output, the values that the matrices stand for lie within float32.
+ * For a float32 output, what the matrices' values stand for is zero or a normal float32 number
+ * (smaller ones may be rounded or lost).
  * M or N = 0 is a no-op, K = 0 writes zeros.  Limits: sizes and pitches below 2^24,
  * ceil(M / 64) ceil(N / 128) < 2^23 (ERR_SHAPE).
  * Errors: ERR_NULL, ERR_SHAPE, ERR_ALIGN, ERR_ALIAS, ERR_UNSUPPORTED (dtype), ERR_HIP.

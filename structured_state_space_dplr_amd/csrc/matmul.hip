@@ -3,10 +3,11 @@
 // The matrix instruction 16x16x128 takes 8-bit operands with a scale for each 32 values of a
 // row, so one instruction is a group's product with its scales applied, and nothing is
 // left for the vector units.  Inside, products are summed with fewer bits than fp32 has
-// (measured: off by 1.5e-5 of the result's norm for normal values, 7e-5 where they span 16
-// powers of two), which outputs of 16 bits do not show; a float32 output is taken
-// by the bf16 instruction, whose products are exact and whose sums are fp32, after the 8 bits
-// and their scales are turned into bf16 (exact), at about half the rate.
+// (measured: off by 1.5e-5 of the result's norm for normal values, 7e-5 where both operands' span
+// eight powers of two, up to about 2^-13 of a group's sum of magnitudes), which outputs of 16 bits
+// rarely show; a float32 output is taken by the bf16 instruction, whose products are exact and
+// whose sums are fp32, after the 8 bits and their scales are turned into bf16 (exact), at about half
+// the rate (4096^3: 1.8 PFLOP/s in bf16, 1.0 in float32).
 //
 // The product is taken transposed (B's rows as the instruction's rows), so that a lane holds
 // four neighbouring columns of a row of out.
