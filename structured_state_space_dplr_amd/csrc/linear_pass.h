@@ -6,11 +6,19 @@
 // From the ends of the sequences (rev) the chunk's rows are taken in reverse, and G_i is the sum of g
 // over the rows behind row i of the chunk's order, without its own: the same formulas.
 //
-// A block of four waves walks over a segment's chunks.  Wave w holds CW columns of the state in
+// A block of eight waves (four where the head has 64 columns or less, or the parts leave no room)
+// walks over a segment's chunks.  Wave w holds CW columns of the state in
 // registers, in the matrix instruction's result layout, which is also its operand layout for X S
 // once the rows of Y^T are permuted (delta_prep.hip).  X, Y, W lie in LDS as bf16 parts; P is shared out
 // by strips of 16 rows and passed through LDS.  The next chunk's rows are on their way in
 // registers.
+//
+// What bounds it is the issue of instructions: in 16-bit 128 x 128 heads the vector units are busy 64 % of
+// the CUs' time (splitting states and weights into parts, the decays, staging) and the matrix units
+// 35 %, one after the other in a wave, with four waves a SIMD; LDS is at 46 %.  Eight waves a
+// block, which share X, Y and P, against four: 160 us instead of 172 for a prompt of 16384 tokens of
+// 16 heads.  Kernel times there (bf16): sums 36 us, states 15, pass 88; training step of 4 x 4096
+// tokens: sums 44, states 14, passes 111 (o, dv) and 132 (dq, dk), with their sums by rows.
 #pragma once
 
 #include "linear_device.h"
@@ -508,6 +516,29 @@ void linear_pass_kernel(const LinPass p) {
           ? (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T) : nullptr;
       float* to = MODE == kGrad && p.dot
           ? p.dot_out + ((size_t)(slice * WAVES + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
+      // all rows' loads on their way together (the zeros: or the registers of an array that is filled
+      // under a condition live through the whole loop, and are spilled)
+      T dot[MODE == kGrad ? RT : 1][CT][4] = {};
+      if (MODE == kGrad && p.dot) {
+#pragma unroll
+        for (int r = 0; r < RT; ++r) {
+          const int i = 16 * r + lr < n ? 16 * r + lr : n - 1;
+          const unsigned at = (unsigned)(p.rev ? n - 1 - i : i) * ((unsigned)p.lddot * (unsigned)sizeof(T));
+#pragma unroll
+          for (int c = 0; c < CT; ++c) {
+            const int col = col0 + 16 * c + 4 * lg;
+            if constexpr (WHOLE) {
+              __builtin_memcpy(dot[r][c], db + (at + (col < p.dw ? col : 0) * (unsigned)sizeof(T)), sizeof(dot[r][c]));
+            } else {
+#pragma unroll
+              for (int e = 0; e < 4; ++e)
+                __builtin_memcpy(&dot[r][c][e], db + (at + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T)),
+                                 sizeof(T));
+            }
+          }
+        }
+        asm volatile("" ::: "memory");   // not put behind the conditions below
+      }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int i = 16 * r + lr, row = p.rev ? n - 1 - i : i;
@@ -527,13 +558,10 @@ void linear_pass_kernel(const LinPass p) {
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
                 __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if (MODE == kGrad && p.dot) {   // (loaded earlier, its registers would be spilled)
-                T t[4];
-                __builtin_memcpy(t, db + ((unsigned)row * ((unsigned)p.lddot * (unsigned)sizeof(T)) +
-                                          (col + e0) * (unsigned)sizeof(T)), sizeof(T) * m);
+              if (MODE == kGrad && p.dot) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                  if (e < m) sum = fmaf(o[e0 + e], to_f32(t[e]), sum);
+                  if (e < m) sum = fmaf(o[e0 + e], to_f32(dot[r][c][e0 + e]), sum);
               }
             };
             if (col + 4 <= p.dw) {

@@ -2,7 +2,8 @@
 //   S <- exp(g) S + k v^T,  o = scale S^T q,
 // one pass over the state a token.  A block of 256 threads holds kCols columns of one head's state
 // in registers (8 lanes x 4 columns, 32 groups of rows), so a head is spread over dv / 32 blocks
-// and a row of 32 columns is a whole line; for one token the state's read and write bound it.
+// and a row of 32 columns is a whole line; for one token the state's read and write bound it (128
+// sequences of 16 heads of 128 x 128: 53 us, 5.1 TB/s; one sequence of 16 heads of 64 x 64: 3.7).
 #include "linear_device.h"
 
 namespace s4 {

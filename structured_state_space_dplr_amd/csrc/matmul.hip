@@ -316,7 +316,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
 // out the groups along K, each by itself and without barriers, up to three groups on their way to
 // its own part of LDS, and their sums are added up in a fixed order.  (Operands
 // read to registers take a cache access for every 16 bytes, since neighbouring lanes hold different
-// rows: 32 x 6144 x 4096 18.3 us.)
+// rows: 32 x 6144 x 4096 18.3 us against 11.7, 2.2 TB/s of B.)
 template <typename T, int MT, int WAVES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES) void matmul_few_kernel(const MatmulArgs p) {
   constexpr int LOADS = 2 * (MT + 1), BYTES = LOADS * 1024;
