@@ -17,8 +17,9 @@ a violation raises ``S4DPLRPreconditionError``.  The check copies the
 inputs to host memory and synchronizes, so it is for debugging, not for the
 timed path.
 
-The token-major operators (``layer_norm_fwd`` / ``layer_norm_bwd`` and, on a
-``DeltaPlan``, ``delta_fwd`` / ``delta_bwd``) take float32, bfloat16 or float16
+The token-major operators (``layer_norm_fwd`` / ``layer_norm_bwd``, on a
+``DeltaPlan`` ``delta_fwd`` / ``delta_bwd`` and on a ``LinearAttentionPlan``
+``linear_attention_fwd`` / ``linear_attention_bwd``) take float32, bfloat16 or float16
 tensors of any size and alignment, launch on the device of their tensors, and
 ``stream=None`` is that device's current stream.  With ``S4DPLR_VALIDATE=1``
 their inputs are checked to be finite, the log decays g to be <= 0 and offsets
