@@ -316,7 +316,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
 // out the groups along K, each by itself and without barriers, up to three groups on their way to
 // its own part of LDS, and their sums are added up in a fixed order.  (Operands
 // read to registers take a cache access for every 16 bytes, since neighbouring lanes hold different
-// rows: 32 x 6144 x 4096 18.3 us against 11.7, 2.2 TB/s of B.)
+// rows: 32 x 6144 x 4096 18.3 us against 11.7.)
 template <typename T, int MT, int WAVES, bool WHOLE>
 __global__ __launch_bounds__(64 * WAVES) void matmul_few_kernel(const MatmulArgs p) {
   constexpr int LOADS = 2 * (MT + 1), BYTES = LOADS * 1024;
@@ -444,8 +444,16 @@ template <typename T>
 hipError_t matmul(const MatmulArgs& a, hipStream_t s) {
   const bool whole = ((reinterpret_cast<uintptr_t>(a.a) | reinterpret_cast<uintptr_t>(a.b) |
                        (uintptr_t)a.lda | (uintptr_t)a.ldb | (uintptr_t)a.K) & 15) == 0;
-  if (a.M <= 64)
-    return a.M <= 16 ? few<T, 1, 8>(a, whole, s) : a.M <= 32 ? few<T, 2, 8>(a, whole, s) : few<T, 4, 4>(a, whole, s);
+  // Few rows: eight waves a block (four for more than 32 rows) while there is a block of 16 columns a CU at
+  // most; half as many above, so that two blocks share a CU's LDS: bf16, K = 4096, us, 32 x 6144 10.1,
+  // as before 11.4, 32 x 16384 20.3 and 23.7, 64 x 6144 14.8 and 16.7; the other way round 32 x 4096
+  // with K = 16384 20.1, with four waves 21.1.  Above two blocks a CU, more than 32 rows are faster by
+  // tiles of 64: 64 x 8192 15.2, tiles 16.8; 64 x 12288 27.3 and 17.5.
+  if (a.M <= (a.N <= 32 * 256 ? 64 : 32)) {
+    if (a.N <= 16 * 256)
+      return a.M <= 16 ? few<T, 1, 8>(a, whole, s) : a.M <= 32 ? few<T, 2, 8>(a, whole, s) : few<T, 4, 4>(a, whole, s);
+    return a.M <= 16 ? few<T, 1, 4>(a, whole, s) : a.M <= 32 ? few<T, 2, 4>(a, whole, s) : few<T, 4, 2>(a, whole, s);
+  }
   // Tiles of 128 where they fill the CUs, of 64 below (bf16, K = 4096, us): 512 x 4096, 128 tiles, 64
   // 23.9, 128 33.2; 1024 x 4096, 256 tiles, 64 36.6, 128 35.6; 2048 x 4096 66.1 and 47.7.  Tiles of 256,
   // whose operands are read from LDS half as often, one a CU: a round of them takes what 5 / 3 rounds

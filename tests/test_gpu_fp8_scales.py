@@ -1,4 +1,4 @@
-"""GPU tests of the 8-bit product at the ends of its scales.
+"""GPU tests of the 8-bit product at the ends of its scales, and of few rows by many columns.
 
 Scales of 2^-127 (byte 0), whose float32 is subnormal, and of 2^127 (byte 254) meet in one product,
 so that the result is of ordinary size.  A float32 output widens the values first: they are drawn
@@ -6,6 +6,8 @@ so that each stands for a normal bf16 number.  Tolerances as in test_gpu_fp8: (K
 of magnitudes for float32; 2^-12 of it and the rounding of the output for 16 bits."""
 import pytest
 import torch
+
+from test_gpu_fp8 import check_product, operands
 
 pytestmark = pytest.mark.gpu
 
@@ -47,3 +49,14 @@ def test_ends_of_the_scales(s4, dtype, M, N, K, square):
         tol = 2.0 ** -12 * size + torch.finfo(dtype).eps / 2 * want.abs() + torch.finfo(dtype).tiny
         assert size.max() < torch.finfo(dtype).max
     assert ((out.cpu().double() - want).abs() <= tol).all()
+
+
+@pytest.mark.parametrize("dtype", [F32, BF, F16])
+@pytest.mark.parametrize("M,N,K", [(1, 4100, 300), (16, 5000, 256), (17, 6001, 1000), (32, 4112, 129), (33, 5000, 640),
+                                   (64, 8192, 144), (64, 8200, 256), (40, 9003, 100)])
+def test_few_rows_by_many_columns(s4, dtype, M, N, K):
+    """Whole numbers without a tolerance, as in test_gpu_fp8, and values of many sizes."""
+    check_product(s4, operands(M + N, M, N, K, False, True), dtype, True)
+    check_product(s4, operands(M + K, M, N, K, True, True), dtype, True)
+    if dtype != F16:   # their results pass fp16's range
+        check_product(s4, operands(M, M, N, K, False, False, 8), dtype, False)
