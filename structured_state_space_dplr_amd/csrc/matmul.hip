@@ -51,21 +51,38 @@ __device__ __forceinline__ void scales4(const unsigned char* const (&row)[R], in
   }
 }
 
-// Bytes k .. k + 16 of a row of K, zeros behind its end.
+// Bytes k .. k + 16 of a row of K, as they lie 16 bytes before its end where it ends sooner: one load,
+// not one a byte.  piece_end moves them to their place, with zeros behind the end.
 __device__ __forceinline__ v4i piece16(const unsigned char* __restrict__ row, int k, int K) {
   v4i x = {0, 0, 0, 0};
-  if (k + 16 <= K) {
-    __builtin_memcpy(&x, row + k, 16);
-  } else if (k < K) {
+  if (K >= 16) {   // the same for all lanes
+    __builtin_memcpy(&x, row + (k < K - 16 ? k : K - 16), 16);
+  } else {
     unsigned long lo = 0, hi = 0;
-    for (int j = 0; k + j < K; ++j) {
-      const unsigned long v = row[k + j];
+    for (int j = 0; j < K; ++j) {
+      const unsigned long v = row[j];
       if (j < 8) lo |= v << (8 * j);
       else hi |= v << (8 * (j - 8));
     }
     x = v4i{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
   }
   return x;
+}
+__device__ __forceinline__ v4i piece_end(v4i x, int k, int K) {
+  const int cut = K >= 16 ? k - (k < K - 16 ? k : K - 16) : k;   // bytes before k
+  unsigned long lo, hi;
+  __builtin_memcpy(&lo, &x, 8);
+  __builtin_memcpy(&hi, (const char*)&x + 8, 8);
+  if (cut >= 16) {
+    lo = hi = 0;
+  } else if (cut >= 8) {
+    lo = hi >> (8 * (cut - 8));
+    hi = 0;
+  } else {
+    lo = lo >> (8 * cut) | (hi << 1) << (63 - 8 * cut);
+    hi >>= 8 * cut;
+  }
+  return v4i{(int)lo, (int)(lo >> 32), (int)hi, (int)(hi >> 32)};
 }
 
 __device__ __forceinline__ float scale_value(unsigned byte) {   // 2^(byte - 127), NaN for 255
@@ -216,8 +233,11 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
         held[i] = piece16((i < LEFT ? base_a : base_b) + from[i] - 16 * piece, k, p.K);
     }
   };
-  auto commit = [&](unsigned char* lds) {
+  auto commit = [&](int kb, unsigned char* lds) {
     if constexpr (!WHOLE) {
+      if ((kb + 1) * kK > p.K)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) held[i] = piece_end(held[i], kb * kK + 16 * piece, p.K);
 #pragma unroll
       for (int i = 0; i < LOADS; ++i)
         *reinterpret_cast<v4i*>(lds + (i * WAVES + w) * 1024 + lane * 16) = held[i];
@@ -278,7 +298,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
     if (kb + ahead < steps) stage(kb + ahead, there);
     group_product<T, MT, NT>([&](int i) { return operand(here, wm + 16 * i); },
                              [&](int j) { return operand(here, BM + wn + 16 * j); }, ea, eb, acc);
-    if (kb + 1 < steps) commit(there);
+    if (kb + 1 < steps) commit(kb + 1, there);
 #pragma unroll
     for (int i = 0; i < MT; ++i) ea[i] >>= 8;
 #pragma unroll
@@ -288,7 +308,7 @@ __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64, 2) void matmul_kernel(c
     scales4<MT>(sa, 0, steps, na);
     scales4<NT>(sb, 0, steps, nb);
     stage(0, lds0);
-    commit(lds0);
+    commit(0, lds0);
   }
   if constexpr (DEEP) {
     if (steps > 1) stage(1, lds1);
@@ -372,6 +392,10 @@ __global__ __launch_bounds__(64 * WAVES) void matmul_few_kernel(const MatmulArgs
         held[i] = piece16(row[i], k, p.K);
       }
     }
+    if constexpr (!WHOLE)
+      if (!full)
+#pragma unroll
+        for (int i = 0; i < LOADS; ++i) held[i] = piece_end(held[i], kb * kK + 16 * (i % 2 ? piece ^ 4 : piece), p.K);
 #pragma unroll
     for (int i = 0; i <= MT; ++i) e[i] = srow[i][kb];
     if constexpr (!WHOLE)
