@@ -7,7 +7,7 @@
 // that a row's group lies in neighbouring lanes, and a column's values that one lane holds
 // are 4 (16-bit) or 8 (fp32) neighbouring bytes of the transposed tile, which goes through LDS.
 // Bound by HBM where there are tiles for every CU (8192 x 4096 of bf16, both forms: 33 us, 4.1 TB/s),
-// by a tile's own loads, barriers and stores below (about 10 us).
+// by a tile's own loads, barriers and stores below (1003 x 1040 of fp16 5.5 us).
 #include "fp8.h"
 #include "fp8_device.h"
 #include "vec.h"
@@ -34,6 +34,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
   const int col = c0 + lane * VEC, row = r0 + set * R;
   const int cg = (a.cols + kGroup - 1) / kGroup, rg = (a.rows + kGroup - 1) / kGroup;
   const T* x = (const T*)a.x;
+  const bool rows = a.q && blockIdx.z == 0, columns = a.qt && blockIdx.z == gridDim.z - 1;
   float v[R][VEC];
   if (r0 + kGroup <= a.rows && c0 + kGroup <= a.cols) {
     Vec<T> t[R];
@@ -43,26 +44,35 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) v[i][j] = to_f32(t[i].v[j]);
-  } else {
+  } else if (a.cols % VEC == 0) {
     // at the edge: every load from inside, all on their way together, and zeros behind the ends
+    typedef int v4i __attribute__((ext_vector_type(4)));
+    v4i t[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i)
+      __builtin_memcpy(&t[i], x + (long)(row + i < a.rows ? row + i : a.rows - 1) * a.ldx + (col < a.cols ? col : 0), 16);
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+      asm volatile("" : "+v"(t[i]));   // or the loads are put under the condition, one by one, or split
+      T u[VEC];
+      __builtin_memcpy(u, &t[i], 16);
+#pragma unroll
+      for (int j = 0; j < VEC; ++j) v[i][j] = row + i < a.rows && col < a.cols ? to_f32(u[j]) : 0.f;
+    }
+  } else {
     T t[R][VEC];
-    const bool whole = a.cols % VEC == 0;
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       const T* p = x + (long)(row + i < a.rows ? row + i : a.rows - 1) * a.ldx;
-      if (whole) {
-        __builtin_memcpy(t[i], p + (col < a.cols ? col : 0), sizeof(t[i]));
-      } else {
 #pragma unroll
-        for (int j = 0; j < VEC; ++j) t[i][j] = p[col + j < a.cols ? col + j : 0];
-      }
+      for (int j = 0; j < VEC; ++j) t[i][j] = p[col + j < a.cols ? col + j : 0];
     }
 #pragma unroll
     for (int i = 0; i < R; ++i)
 #pragma unroll
       for (int j = 0; j < VEC; ++j) {
         float f = to_f32(t[i][j]);
-        asm volatile("" : "+v"(f));   // or the loads are put under the condition, one by one
+        asm volatile("" : "+v"(f));
         v[i][j] = row + i < a.rows && col + j < a.cols ? f : 0.f;
       }
   }
@@ -85,11 +95,11 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
     for (int i = 0; i < kThreads / 64; ++i) big = all[i] > big ? all[i] : big;
     block = scale_byte(big);
     if (tid == 0) {
-      if (a.q) a.scales[(long)blockIdx.y * cg + blockIdx.x] = (unsigned char)block;
-      if (a.qt) a.scales_t[(long)blockIdx.x * rg + blockIdx.y] = (unsigned char)block;
+      if (rows) a.scales[(long)blockIdx.y * cg + blockIdx.x] = (unsigned char)block;
+      if (columns) a.scales_t[(long)blockIdx.x * rg + blockIdx.y] = (unsigned char)block;
     }
   }
-  if (a.q) {
+  if (rows) {
 #pragma unroll
     for (int i = 0; i < R; ++i) {
       unsigned byte = block;
@@ -119,7 +129,7 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
       if (!a.square && lane == 0) a.scales[(long)(row + i) * cg + blockIdx.x] = (unsigned char)byte;
     }
   }
-  if (!a.qt) return;
+  if (!columns) return;
   if (!a.square) {
 #pragma unroll
     for (int j = 0; j < VEC; ++j) {
@@ -173,7 +183,12 @@ __global__ __launch_bounds__(kThreads) void quantize_kernel(const QuantizeArgs a
 }
 
 hipError_t launch_quantize(const QuantizeArgs& a, int dtype, hipStream_t s) {
-  const dim3 grid((unsigned)((a.cols + kGroup - 1) / kGroup), (unsigned)((a.rows + kGroup - 1) / kGroup));
+  const unsigned across = (a.cols + kGroup - 1) / kGroup, down = (a.rows + kGroup - 1) / kGroup;
+  // Both forms of a tile by blocks of their own while there is a tile a CU at most: each is a chain of
+  // steps that the other need not wait for (fp16, us): 1024 x 2048 4.6 against 5.4, 2048 x 2048 6.1 and
+  // 6.2; fp32 7.4 and 8.1; above, the tile's second read costs more: fp32 2048 x 4096 13.1 and 11.8.
+  const unsigned apart = a.q && a.qt && (long)across * down <= 256 ? 2 : 1;
+  const dim3 grid(across, down, apart);
   if (dtype == S4DPLR_F32) quantize_kernel<float><<<grid, kThreads, 0, s>>>(a);
   else if (dtype == S4DPLR_BF16) quantize_kernel<bf16><<<grid, kThreads, 0, s>>>(a);
   else quantize_kernel<f16><<<grid, kThreads, 0, s>>>(a);
