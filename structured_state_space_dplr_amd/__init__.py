@@ -175,7 +175,15 @@ class S4DPLRPreconditionError(ValueError):
         self.where, self.what = where, what
 
 
+# os.environ's own store where it has one (bytes): a look without encoding the name and raising and
+# catching a KeyError, 0.4 us of a call's 9
+_environ = getattr(os.environ, "_data", None)
+_VALIDATE_KEY = os.fsencode(VALIDATE_ENV)
+
+
 def validation_enabled() -> bool:
+    if type(_environ) is dict:
+        return _environ.get(_VALIDATE_KEY) == b"1"
     return os.environ.get(VALIDATE_ENV, "") == "1"
 
 
@@ -509,7 +517,7 @@ def _launch(device, stream, fn, args):
     index = device.index
     # the raw handle of the device's current stream, without a Stream object
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else _stream(stream)
-    if index == torch.cuda.current_device():
+    if index == torch._C._cuda_getDevice():
         return fn(*args, raw)
     with torch.cuda.device(device):
         return fn(*args, raw)
