@@ -116,10 +116,16 @@ hipError_t launch_linear_steps(const LinStep& a, int dtype, hipStream_t s);
 // What the segments add to the states, then (scan) the states before them.
 hipError_t launch_linear_sums(const LinPass& a, int dtype, hipStream_t s);
 hipError_t launch_linear_pass(const LinPass& a, int dtype, hipStream_t s);
-// out [tokens][Hk][d] = the sums over each group of heads of part [tokens][Hv][d], in the
+// Each out [tokens][Hk][d] = the sums over each group of heads of part [tokens][Hv][d], in the
 // sequences' rows.
-hipError_t launch_linear_groups(const float* part, void* out, const int* offsets, int sequences,
-                                long tokens, int Hk, int Hv, int d, int dtype, hipStream_t s);
+struct LinGroups {
+  const float* part[2];
+  void* out[2];                   // may be NULL
+  const int* offsets;
+  int sequences, Hk, Hv, d;
+  long tokens;
+};
+hipError_t launch_linear_groups(const LinGroups& a, int dtype, hipStream_t s);
 // dg from the passes' dots and edges; dg is [tokens][Hv] or (ldg == 0) [Hv].
 struct LinGates {
   const float *dots, *dotk, *edge;

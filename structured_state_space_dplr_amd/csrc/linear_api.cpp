@@ -343,12 +343,11 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
     }
     if ((e = launch_linear_pass(zv, p->dtype, stream)) != hipSuccess) return done(e);
   }
-  for (int i = 0; i < 2 && grouped; ++i)
-    if (void* to = i ? dk : dq)
-      if ((e = launch_linear_groups(at<float>(ws, i ? p->off_dk : p->off_dq), to, offsets,
-                                    p->sequences, p->tokens, p->Hk, p->Hv, p->dk, p->dtype,
-                                    stream)) != hipSuccess)
-        return done(e);
+  if (grouped && (dq || dk)) {
+    const LinGroups l = {{at<float>(ws, p->off_dq), at<float>(ws, p->off_dk)}, {dq, dk}, offsets,
+                         p->sequences, p->Hk, p->Hv, p->dk, p->tokens};
+    if ((e = launch_linear_groups(l, p->dtype, stream)) != hipSuccess) return done(e);
+  }
   if (dg) {
     LinGates l = {};
     l.dots = dots;

@@ -58,16 +58,17 @@ __global__ __launch_bounds__(256) void linear_scan_kernel(const LinPass p) {
   }
 }
 
+// Both gradients of a call in one launch, one of blockIdx.y each.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_groups_kernel(const float* __restrict__ part,
-                                                            T* __restrict__ out,
-                                                            const int* __restrict__ offsets,
-                                                            int sequences, long tokens, int Hk,
-                                                            int group, int d) {
+__global__ __launch_bounds__(256) void linear_groups_kernel(const LinGroups a) {
+  const float* __restrict__ part = a.part[blockIdx.y];
+  T* __restrict__ out = (T*)a.out[blockIdx.y];
+  if (!out) return;
+  const int Hk = a.Hk, group = a.Hv / a.Hk, d = a.d;
   // the rows of the sequences, which lie one behind the other
-  long lo = 0, hi = tokens;
-  if (offsets) {
-    const Rows r = clamp_rows((int)tokens, offsets[0], offsets[sequences]);
+  long lo = 0, hi = a.tokens;
+  if (a.offsets) {
+    const Rows r = clamp_rows((int)a.tokens, a.offsets[0], a.offsets[a.sequences]);
     lo = r.start;
     hi = r.start + r.len;
   }
@@ -214,21 +215,14 @@ hipError_t launch_linear_sums(const LinPass& a, int dtype, hipStream_t s) {
   return hipGetLastError();
 }
 
-hipError_t launch_linear_groups(const float* part, void* out, const int* offsets, int sequences,
-                                long tokens, int Hk, int Hv, int d, int dtype, hipStream_t s) {
-  const long n = tokens * Hk * d;
+hipError_t launch_linear_groups(const LinGroups& a, int dtype, hipStream_t s) {
+  const long n = a.tokens * a.Hk * a.d;
   if (n == 0) return hipSuccess;
   const long blocks = (n + 255) / 256;
-  const unsigned grid = (unsigned)(blocks < (1 << 16) ? blocks : 1 << 16);
-  if (dtype == S4DPLR_F32)
-    linear_groups_kernel<float><<<grid, 256, 0, s>>>(part, (float*)out, offsets, sequences, tokens, Hk,
-                                                   Hv / Hk, d);
-  else if (dtype == S4DPLR_BF16)
-    linear_groups_kernel<bf16><<<grid, 256, 0, s>>>(part, (bf16*)out, offsets, sequences, tokens, Hk,
-                                                   Hv / Hk, d);
-  else
-    linear_groups_kernel<f16><<<grid, 256, 0, s>>>(part, (f16*)out, offsets, sequences, tokens, Hk,
-                                                   Hv / Hk, d);
+  const dim3 grid((unsigned)(blocks < (1 << 16) ? blocks : 1 << 16), 2);
+  if (dtype == S4DPLR_F32) linear_groups_kernel<float><<<grid, 256, 0, s>>>(a);
+  else if (dtype == S4DPLR_BF16) linear_groups_kernel<bf16><<<grid, 256, 0, s>>>(a);
+  else linear_groups_kernel<f16><<<grid, 256, 0, s>>>(a);
   return hipGetLastError();
 }
 
