@@ -23,10 +23,7 @@ hipError_t launch_linear_steps(const LinStep&, int, hipStream_t) { return hipSuc
 hipError_t launch_linear_sums(const LinPass&, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_linear_pass(const LinPass&, int, hipStream_t) { return hipSuccess; }
 hipError_t launch_linear_gates(const LinGates&, hipStream_t) { return hipSuccess; }
-hipError_t launch_linear_groups(const float*, void*, const int*, int, long, int, int, int, int,
-                                hipStream_t) {
-  return hipSuccess;
-}
+hipError_t launch_linear_groups(const LinGroups&, int, hipStream_t) { return hipSuccess; }
 int linear_parts(int, int, int) { return 4; }
 }  // namespace s4
 
