@@ -5,8 +5,8 @@ namespace s4 {
 
 hipError_t linear_pass_f32(const LinPass& a, bool sum, hipStream_t s) {
   if (sum) return linear_launch<float, 3, kSum>(a, s);
-  // out of the pass in the tensors' type, without sums by rows
-  const bool plain = a.out && !a.out_f32 && !a.dot;
+  // out of the pass, if any, in the tensors' type, without sums by rows
+  const bool plain = !a.out_f32 && !a.dot;
   return plain ? linear_launch<float, 3, kOut>(a, s) : linear_launch<float, 3, kGrad>(a, s);
 }
 

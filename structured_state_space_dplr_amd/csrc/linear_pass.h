@@ -552,7 +552,7 @@ void linear_pass_kernel(const LinPass p) {
               unsigned char* q = ob + ((unsigned)row * ((unsigned)ldo * wide) + (col + e0) * wide);
               if (MODE == kGrad && p.out_f32) {
                 __builtin_memcpy(q, (const float*)&o + e0, 4 * m);
-              } else if (MODE == kOut || p.out) {
+              } else if (p.out) {
                 T t[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
