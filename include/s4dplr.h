@@ -537,7 +537,10 @@ s4dplr_status s4dplr_linear_attention_fwd(const s4dplr_linear_attention_plan* pl
  * for zeros) to dq, dk [tokens][Hk][dk], dv [tokens][Hv][dv] (contiguous, elements of the
  * plan's dtype), dg (float32, the shape of g) and dstate [sequences][Hv][dk][dv] (float32; may
  * be dstate_out itself).  Any output may be NULL (not written; dg must be where g is); outputs
- * are overwritten, not accumulated.  dg is taken from q . dq and k . dk by sums in 64 bits.
+ * are overwritten, not accumulated.  dg_t is summed over what passes token t, each term with the
+ * decay at t in it, so that it has the digits of a float32 sum in heads and at tokens that forget
+ * fast too; for that the workspace of a training plan has room for a state for each 64 tokens (32 where dv
+ * is above 128 and elements are not bfloat16).
  * Gradients of shared key heads are summed over their value heads in a fixed order: equal calls
  * give equal bits.  `saved` is only read.  Errors as for s4dplr_linear_attention_fwd.
  */

@@ -20,7 +20,7 @@ SOURCES = ["kernels.hip", "big.hip", "recurrent.hip", "backward.hip", "vandermon
            "noalloc.hip", "rank.hip", "norm.hip", "delta_step.hip", "delta_prep.hip",
            "delta_scan.hip", "delta_grads.hip", "rms.hip", "quantize.hip", "matmul.hip",
            "linear_bf16.hip", "linear_f16.hip", "linear_f32.hip", "linear_step.hip",
-           "linear_join.hip", "api.cpp", "token_api.cpp", "dense_api.cpp", "linear_api.cpp"]
+           "linear_join.hip", "linear_gates.hip", "api.cpp", "token_api.cpp", "dense_api.cpp", "linear_api.cpp"]
 ARCH = "gfx950"
 
 

@@ -24,9 +24,11 @@ struct s4dplr_linear_attention_plan {
   // Workspace, byte offsets.
   size_t off_states;           // [slot][Hv] states: before each segment, backward behind it
   size_t off_decay;            // [slot][Hv] float: the segment's whole decay
-  size_t off_dots, off_dotk;   // backward: [dot_parts][Hv][tokens] parts of q . dq and of k . dk
-  size_t off_edge;             // backward: [sequences + slots][Hv][dot_parts] parts of <S, dS> before
-  size_t off_dgsum;            // backward: [sequences + slots][Hv] sums of dg over a segment
+  size_t off_dots, off_dotk;   // backward: [linear_parts][Hv][tokens] parts of dg by rows (LinPass::dot)
+  size_t off_inner;            // backward: [ceil(tokens / linear_chunk)][Hv][linear_parts] states before
+                               // the chunks inside a segment, by waves
+  size_t off_dgsum;            // backward: [sequences + chunk_slots][Hv] sums of dg over a chunk
+  long chunk_slots;            // slots as above with a chunk as the segment
   size_t off_dq, off_dk;       // backward, Hv > Hk: [tokens][Hv][dk] float
   size_t total;
   // saved (training): [slot][Hv] states before each segment, [sequences][Hv] states before
@@ -39,6 +41,17 @@ namespace s4 {
 
 constexpr int kLinChunk = 64;    // tokens a chunk
 constexpr int kDotParts = 16;    // waves that share the columns of a head, at most
+
+// Tokens a chunk of a pass with dx columns, of tensors whose elements are `parts` bf16 parts: 32 where
+// 64 do not fit into LDS.
+constexpr int linear_chunk(int dx, int parts) { return dx > 128 && parts > 1 ? 32 : kLinChunk; }
+// Rows of a state that a wave of a pass with dx columns holds, 16 columns of each.
+constexpr int linear_rows(int dx) { return dx <= 64 ? 64 : dx <= 128 ? 128 : 256; }
+constexpr int linear_type_parts(int dtype) { return dtype == S4DPLR_BF16 ? 1 : dtype == S4DPLR_F16 ? 2 : 3; }
+constexpr long linear_slots(long tokens, int sequences, int segment) {
+  const long most = tokens / (segment + 1);
+  return most == 0 ? 0 : tokens / segment + (sequences < most ? sequences : most);
+}
 
 // Longest sequence that is taken token by token.  Token by token against by chunks, 16 heads of 128
 // x 128 (us): bf16, 128 sequences, 4 tokens 64.2 against 66.6, 6 tokens 80.4 against 60.0; 16
@@ -83,14 +96,17 @@ struct LinPass {
   long rs, cs;                    // a state's element (row of dx, column of dw) is at rs row + cs column
   float read, pair, update;
   int rev;
-  // sums over the columns of out times `dot`, by waves: [part][Hv][tokens]; may be NULL
+  // The decays' gradient (dot not NULL): sums over the columns of `dot` times what out has from the
+  // state before the chunk, read (decay to t) S^T x_t, by waves: [part][Hv][tokens].  Forwards, the
+  // states before the chunks inside a segment go to `inner`.  In reverse, they are read from there, those
+  // before segments from inner_slots and inner_first, and their inner products with the state behind the
+  // chunk, times the chunk's decay, take the place of the last row's sum, which dg has no use for.
   const void* dot;
   long lddot;
   int gdot;
   float* dot_out;
-  // sums of the state behind a segment times the saved one; may be NULL
-  const float *edge_first, *edge_slots;
-  float* edge_out;                // [sequences + slots][Hv][kDotParts]
+  float* inner;                   // of the chunk that begins in row `token`: token / chunk
+  const float *inner_first, *inner_slots;
   float* states;                  // the sums' pass: [slot] what each segment adds
   float* decay;                   // [slot][Hv]
   int sequences, each, Hv, dk, dv, segment;
@@ -126,15 +142,19 @@ struct LinGroups {
   long tokens;
 };
 hipError_t launch_linear_groups(const LinGroups& a, int dtype, hipStream_t s);
-// dg from the passes' dots and edges; dg is [tokens][Hv] or (ldg == 0) [Hv].
+// dg from the passes' sums by rows and the pairs inside the chunks; dg is [tokens][Hv] or (ldg == 0) [Hv].
 struct LinGates {
-  const float *dots, *dotk, *edge;
-  int parts_q, parts_k, parts_edge;
+  const void *q, *k, *v, *dout;
+  long ldq, ldk, ldv, lddout;
+  int dtype, group, dk, dv;
+  float scale;
+  const float *dots, *dotk;
+  int parts;
   float *dg, *sums;
   const float* g;
   long ldg;
   const int* offsets;
-  int sequences, each, Hv, segment;
+  int sequences, each, Hv, segment;   // segment: the chunk
   long tokens, slots;
 };
 hipError_t launch_linear_gates(const LinGates& a, hipStream_t s);

@@ -123,9 +123,8 @@ s4dplr_status s4dplr_linear_attention_plan_create(s4dplr_linear_attention_plan**
   p->dtype = dtype;
   p->training = (flags & S4DPLR_LINEAR_ATTENTION_TRAINING) != 0;
   p->segment = segment_of(*p);
-  const long most = tokens / (p->segment + 1);
-  p->slots = most == 0 ? 0 : tokens / p->segment + (sequences < most ? sequences : most);
-  const size_t state = sizeof(float) * (size_t)Hv * dk * dv, units = (size_t)sequences + p->slots;
+  p->slots = linear_slots(tokens, sequences, p->segment);
+  const size_t state = sizeof(float) * (size_t)Hv * dk * dv;
   size_t off = 0;
   auto take = [&off](size_t n) {
     const size_t here = off;
@@ -135,11 +134,15 @@ s4dplr_status s4dplr_linear_attention_plan_create(s4dplr_linear_attention_plan**
   p->off_states = take(p->slots * state);
   p->off_decay = take(sizeof(float) * p->slots * Hv);
   if (p->training) {
-    const size_t dots = sizeof(float) * kDotParts * (size_t)Hv * tokens;
+    const int chunk = linear_chunk(dv, linear_type_parts(dtype));
+    const size_t parts = (size_t)Hv * linear_parts(dv, dk, dtype), dots = sizeof(float) * parts * tokens;
     p->off_dots = take(dots);
     p->off_dotk = take(dots);
-    p->off_edge = take(sizeof(float) * units * Hv * kDotParts);
-    p->off_dgsum = take(sizeof(float) * units * Hv);
+    // none where a segment is one chunk
+    const long inside = p->segment > chunk && tokens > chunk ? (tokens + chunk - 1) / chunk : 0;
+    p->off_inner = take(sizeof(float) * parts * inside * linear_rows(dv) * 16);
+    p->chunk_slots = linear_slots(tokens, sequences, chunk);
+    p->off_dgsum = take(sizeof(float) * ((size_t)sequences + p->chunk_slots) * Hv);
     const size_t grads = Hv > Hk ? sizeof(float) * (size_t)tokens * Hv * dk : 0;
     p->off_dq = take(grads);
     p->off_dk = take(grads);
@@ -269,7 +272,7 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
   const float* before = at<float>(const_cast<void*>(saved), 0);
   const float* first = at<float>(const_cast<void*>(saved), p->off_first);
   float *dots = at<float>(ws, p->off_dots), *dotk = at<float>(ws, p->off_dotk);
-  float* edge = at<float>(ws, p->off_edge);
+  float* inner = at<float>(ws, p->off_inner);
   hipError_t e = hipSuccess;
   // from the ends: the gradient of the states, for dk and dv
   LinPass z = base(p, a);
@@ -312,6 +315,7 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
       l.lddot = ldq;
       l.gdot = group;
       l.dot_out = dots;
+      l.inner = inner;
     }
     if ((e = launch_linear_pass(l, p->dtype, stream)) != hipSuccess) return done(e);
   }
@@ -332,17 +336,14 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
       l.lddot = ldk;
       l.gdot = group;
       l.dot_out = dotk;
+      l.inner = inner;
+      l.inner_first = first;
+      l.inner_slots = before;
     }
     if ((e = launch_linear_pass(l, p->dtype, stream)) != hipSuccess) return done(e);
   }
-  if (dv || dg || dstate) {
-    if (dg) {
-      zv.edge_first = first;
-      zv.edge_slots = before;
-      zv.edge_out = edge;
-    }
+  if (dv || dstate)
     if ((e = launch_linear_pass(zv, p->dtype, stream)) != hipSuccess) return done(e);
-  }
   if (grouped && (dq || dk)) {
     const LinGroups l = {{at<float>(ws, p->off_dq), at<float>(ws, p->off_dk)}, {dq, dk}, offsets,
                          p->sequences, p->Hk, p->Hv, p->dk, p->tokens};
@@ -350,11 +351,22 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
   }
   if (dg) {
     LinGates l = {};
+    l.q = q;
+    l.k = k;
+    l.v = v;
+    l.dout = dout;
+    l.ldq = ldq;
+    l.ldk = ldk;
+    l.ldv = ldv;
+    l.lddout = ldo;
+    l.dtype = p->dtype;
+    l.group = group;
+    l.dk = p->dk;
+    l.dv = p->dv;
+    l.scale = scale;
     l.dots = dots;
     l.dotk = dotk;
-    l.edge = edge;
-    l.parts_q = l.parts_k = linear_parts(p->dv, p->dk, p->dtype);
-    l.parts_edge = linear_parts(p->dk, p->dv, p->dtype);
+    l.parts = linear_parts(p->dv, p->dk, p->dtype);
     l.dg = dg;
     l.sums = at<float>(ws, p->off_dgsum);
     l.g = g;
@@ -363,9 +375,9 @@ s4dplr_status s4dplr_linear_attention_bwd(const s4dplr_linear_attention_plan* p,
     l.sequences = p->sequences;
     l.each = p->each;
     l.Hv = p->Hv;
-    l.segment = p->segment;
+    l.segment = linear_chunk(p->dv, linear_type_parts(p->dtype));
     l.tokens = p->tokens;
-    l.slots = p->slots;
+    l.slots = p->chunk_slots;
     e = launch_linear_gates(l, stream);
   }
   return done(e);

@@ -47,6 +47,14 @@ struct LinItem {
 // condition under which it is used, where it would be waited for at once.
 __device__ __forceinline__ void touch(float& v) { asm volatile("" : "+v"(v)); }
 
+// The thread's number, not known to be the one of another call: what is computed from it is
+// computed there, and not kept in registers through a loop (64 of which would be spilled).
+__device__ __forceinline__ unsigned thread() {
+  unsigned t = threadIdx.x;
+  asm volatile("" : "+v"(t));
+  return t;
+}
+
 __device__ __forceinline__ long uniform(long v) {
   return (long)(unsigned)__builtin_amdgcn_readfirstlane((int)v) |
          (long)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32;

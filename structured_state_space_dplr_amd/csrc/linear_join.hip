@@ -1,5 +1,5 @@
 // Linear attention: what joins the blocks of a pass.  The states before the segments from what
-// the segments add, the gradients of shared heads, and the gradient of the decays.
+// the segments add, and the gradients of shared heads.
 #include "linear_device.h"
 
 namespace s4 {
@@ -82,101 +82,6 @@ __global__ __launch_bounds__(256) void linear_groups_kernel(const LinGroups a) {
   }
 }
 
-// dg_t = <S_{t-1}, gradient of S_{t-1} by what comes later>: the edge before the segment, and
-// behind token i  + k_i . dk_i - q_i . dq_i  of the token itself.  The sums are held in 64 bits
-// over a segment of a few hundred tokens.  A block per segment and head, 64 tokens a wave; all parts
-// of a token are loaded together (4 x 4096 tokens of 16 heads, 17 MB: 25 us one by one, 15 so).
-// Where exp(g) is 0 nothing of the state before is left, and dg is 0.
-__global__ __launch_bounds__(512) void linear_gates_kernel(const LinGates a) {
-  __shared__ double sums[2][8], totals[8];
-  const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), h = blockIdx.y;
-  LinItem it;
-  const long skip = a.offsets || a.each <= a.segment ? 0 : a.sequences;
-  const long item = skip + blockIdx.x;
-  if (!lin_item(a, item, &it)) {
-    if (threadIdx.x == 0 && a.ldg == 0) a.sums[item * a.Hv + h] = 0.f;
-    return;
-  }
-  double run = 0.0, total = 0.0;
-  if (it.len > 0) {
-    const float e = lane < a.parts_edge ? a.edge[(item * a.Hv + h) * kDotParts + lane] : 0.f;
-    run = e;
-#pragma unroll
-    for (int off = 8; off >= 1; off >>= 1) run += __shfl_xor(run, off);
-    run = __shfl(run, 0);
-  }
-  int turn = 0;
-  for (int t0 = 64 * w; t0 - 64 * w < it.len; t0 += 512, turn ^= 1) {
-    const bool in = t0 + lane < it.len;
-    const long tok = it.start + (in ? t0 + lane : 0);
-    const float *kp = a.dotk + (size_t)h * a.tokens + tok, *qp = a.dots + (size_t)h * a.tokens + tok;
-    const size_t step = (size_t)a.Hv * a.tokens;
-    float dk[kDotParts], dq[kDotParts];
-#pragma unroll
-    for (int i = 0; i < kDotParts; ++i) {
-      dk[i] = kp[(i < a.parts_k ? i : 0) * step];
-      dq[i] = qp[(i < a.parts_q ? i : 0) * step];
-    }
-    const float g = a.g[tok * a.ldg + h];
-    double own = 0.0;
-#pragma unroll
-    for (int i = 0; i < kDotParts; ++i) {
-      touch(dk[i]);
-      touch(dq[i]);
-    }
-#pragma unroll
-    for (int i = 0; i < kDotParts; ++i) {
-      if (i < a.parts_k) own += dk[i];
-      if (i < a.parts_q) own -= dq[i];
-    }
-    own = in ? own : 0.0;
-    double x = own;
-#pragma unroll
-    for (int off = 1; off < 64; off <<= 1) {
-      const double y = __shfl_up(x, off);
-      if (lane >= off) x += y;
-    }
-    if (lane == 63) sums[turn][w] = x;
-    __syncthreads();
-    double before = run;   // of the waves before this one
-    for (int i = 0; i < 8; ++i) {
-      const double y = sums[turn][i];
-      if (i < w) before += y;
-      run += y;
-    }
-    const double dg = expf(g) == 0.f ? 0.0 : before + (x - own);
-    if (in && a.ldg) a.dg[tok * a.Hv + h] = (float)dg;
-    total += in ? dg : 0.0;
-  }
-  if (a.ldg == 0) {
-#pragma unroll
-    for (int off = 32; off >= 1; off >>= 1) total += __shfl_xor(total, off);
-    if (lane == 0) totals[w] = total;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      for (int i = 1; i < 8; ++i) total += totals[i];
-      a.sums[item * a.Hv + h] = (float)total;
-    }
-  }
-}
-
-// dg of one decay a head: the items' sums, always in the same order.
-__global__ __launch_bounds__(256) void linear_gate_sums_kernel(const float* __restrict__ sums,
-                                                               long first, long last, int Hv,
-                                                               float* __restrict__ dg) {
-  __shared__ double red[256];
-  const int h = blockIdx.x;
-  double s = 0.0;
-  for (long i = first + threadIdx.x; i < last; i += 256) s += sums[i * Hv + h];
-  red[threadIdx.x] = s;
-  __syncthreads();
-  if (threadIdx.x >= 64) return;
-  s = (red[threadIdx.x] + red[threadIdx.x + 64]) + (red[threadIdx.x + 128] + red[threadIdx.x + 192]);
-#pragma unroll
-  for (int off = 32; off >= 1; off >>= 1) s += __shfl_xor(s, off);
-  if (threadIdx.x == 0) dg[h] = (float)s;
-}
-
 }  // namespace
 
 hipError_t linear_pass_bf16(const LinPass& a, bool sum, hipStream_t s);
@@ -223,16 +128,6 @@ hipError_t launch_linear_groups(const LinGroups& a, int dtype, hipStream_t s) {
   if (dtype == S4DPLR_F32) linear_groups_kernel<float><<<grid, 256, 0, s>>>(a);
   else if (dtype == S4DPLR_BF16) linear_groups_kernel<bf16><<<grid, 256, 0, s>>>(a);
   else linear_groups_kernel<f16><<<grid, 256, 0, s>>>(a);
-  return hipGetLastError();
-}
-
-hipError_t launch_linear_gates(const LinGates& a, hipStream_t s) {
-  const bool all_long = !a.offsets && a.each > a.segment, all_short = !a.offsets && !all_long;
-  const long first = all_long ? a.sequences : 0, last = all_short ? a.sequences : a.sequences + a.slots;
-  if (last > first)
-    linear_gates_kernel<<<dim3((unsigned)(last - first), (unsigned)a.Hv), 512, 0, s>>>(a);
-  if (a.ldg == 0)
-    linear_gate_sums_kernel<<<dim3((unsigned)a.Hv), 256, 0, s>>>(a.sums, first, last, a.Hv, a.dg);
   return hipGetLastError();
 }
 

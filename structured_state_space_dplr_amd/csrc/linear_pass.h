@@ -18,7 +18,8 @@
 // 35 %, one after the other in a wave, with four waves a SIMD; LDS is at 46 %.  Eight waves a
 // block, which share X, Y and P, against four: 160 us instead of 172 for a prompt of 16384 tokens of
 // 16 heads.  Kernel times there (bf16): sums 36 us, states 15, pass 88; training step of 4 x 4096
-// tokens: sums 44, states 14, passes 111 (o, dv) and 132 (dq, dk), with their sums by rows.
+// tokens: sums 44, states 14, passes 107 (o, dv) and, with what the decays' gradient needs of them, 159
+// (dq; 235 MB of states written) and 171 (dk; the same read).
 #pragma once
 
 #include "linear_device.h"
@@ -46,14 +47,6 @@ __device__ __forceinline__ void fetch8(const unsigned char* __restrict__ base, u
 template <int COLS>
 __device__ __forceinline__ unsigned turn(unsigned row) {
   return COLS == 64 ? (row >> 1 & 1) << 6 | (row >> 2 & 3) << 4 : (row & 3) << 6 | (row >> 2 & 3) << 4;
-}
-
-// The thread's number, not known to be the one of another call: what is computed from it is
-// computed there, and not kept in registers through the loop (64 of which would be spilled).
-__device__ __forceinline__ unsigned thread() {
-  unsigned t = threadIdx.x;
-  asm volatile("" : "+v"(t));
-  return t;
 }
 
 typedef __attribute__((address_space(3))) unsigned char Lds;
@@ -157,7 +150,8 @@ struct LinTile {
 template <int TILES, int CT>
 __device__ __forceinline__ void store_state(float* __restrict__ to, int col0, int dx, int dw, int rs,
                                             int cs, const v4f (&S)[TILES][CT]) {
-  const int lr = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
+  const unsigned tid = thread();
+  const int lr = tid & 15, lg = (tid & 63) >> 4;
 #pragma unroll
   for (int c = 0; c < CT; ++c) {
     const int col = col0 + 16 * c + lr;
@@ -183,9 +177,10 @@ __device__ __forceinline__ void store_state(float* __restrict__ to, int col0, in
 }
 template <int TILES, int CT>
 __device__ __forceinline__ void load_state(const float* __restrict__ from, int col0, int dx, int dw,
-                                           int rs, int cs, v4f (&S)[TILES][CT]) {
-  const int lr = threadIdx.x & 15, lg = (threadIdx.x & 63) >> 4;
-  auto row_of = [&](int t) { return 32 * (t >> 1) + 8 * lg + 4 * (t & 1); };
+                                           int rs, int cs, v4f (&S)[TILES][CT], int first = 0) {
+  const unsigned tid = thread();
+  const int lr = tid & 15, lg = (tid & 63) >> 4;
+  auto row_of = [&](int t) { return 32 * ((first + t) >> 1) + 8 * lg + 4 * ((first + t) & 1); };
   if (rs == 1 && dx % 4 == 0) {
 #pragma unroll
     for (int t = 0; t < TILES; ++t)
@@ -336,6 +331,53 @@ void linear_pass_kernel(const LinPass p) {
     yr.stage(lds + oY, n, 0, p.dx);
     wr.stage(lds + oW, n, slice * COLS, p.dw);
     __syncthreads();
+    const long tok0 = it.start + c0;
+    // the decays' gradient: row 0 of this wave's part of dot_out's rows of this chunk
+    float* const part = MODE == kGrad && p.dot
+        ? p.dot_out + ((size_t)(slice * WAVES + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
+    if (MODE == kGrad && p.dot) {
+      // a wave's part of a state, as its lanes hold it
+      constexpr size_t PART = TILES * CT * 64 * 4;
+      float* const inner = p.inner + (((size_t)(tok0 / C) * p.Hv + h) * slices * WAVES + slice * WAVES + w) * PART
+          + 4 * (thread() & 63);
+      if (!p.rev) {
+        if (c0 > 0)
+#pragma unroll
+          for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int c = 0; c < CT; ++c) __builtin_memcpy(inner + (t * CT + c) * 256, &S[t][c], 16);
+      } else {
+        // the inner product of the states on either side of the chunk, four tiles at a time; nothing where
+        // the decay over the chunk is 0
+        float across = 0.f;
+        const float whole = get<float>(lds + oWhole + 4 * at);
+        if (__builtin_amdgcn_readfirstlane(__float_as_uint(whole)) != 0) {
+          const float* const from = it.of ? p.inner_slots + ((size_t)it.slot * p.Hv + h) * sz
+                                          : p.inner_first + ((size_t)it.s * p.Hv + h) * sz;
+#pragma unroll
+          for (int t0 = 0; t0 < TILES; t0 += 4) {
+            v4f other[4][CT];
+            if (c0 > 0) {
+#pragma unroll
+              for (int t = 0; t < 4; ++t)
+#pragma unroll
+                for (int c = 0; c < CT; ++c) __builtin_memcpy(&other[t][c], inner + ((t0 + t) * CT + c) * 256, 16);
+            } else {
+              load_state(from, col0, p.dx, p.dw, rs, cs, other, t0);
+            }
+#pragma unroll
+            for (int t = 0; t < 4; ++t)
+#pragma unroll
+              for (int c = 0; c < CT; ++c)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) across = fmaf(S[t0 + t][c][e], other[t][c][e], across);
+            touch(across);
+          }
+          across = sum64(across) * whole;
+        }
+        if (lane == 0) part[n - 1] = across;
+      }
+    }
     if (i + 1 < chunks) fetch(i + 1);
     decays(i + 1);
     fetch_g(i + 2);
@@ -419,12 +461,51 @@ void linear_pass_kernel(const LinPass p) {
               for (int c = 0; c < CT; ++c) O[r][c] = mfma(so[c][i], xo[r][j], O[r][c]);
           });
         }
+        // (the zeros: or the registers of an array that is filled under a condition live through the whole
+        // loop, and are spilled)
+        T dot[MODE == kGrad ? RT : 1][CT][4] = {};
+        if (MODE == kGrad && p.dot) {
+          const unsigned tid = thread();
+          const int lr = tid & 15, lg = (tid & 63) >> 4;
+          const Bytes db = (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T);
+#pragma unroll
+          for (int r = 0; r < RT; ++r) {
+            const int i = 16 * r + lr < n ? 16 * r + lr : n - 1;
+            const unsigned at = (unsigned)(p.rev ? n - 1 - i : i) * ((unsigned)p.lddot * (unsigned)sizeof(T));
+#pragma unroll
+            for (int c = 0; c < CT; ++c) {
+              const int col = col0 + 16 * c + 4 * lg;
+              if constexpr (WHOLE) {
+                __builtin_memcpy(dot[r][c], db + (at + (col < p.dw ? col : 0) * (unsigned)sizeof(T)), sizeof(dot[r][c]));
+              } else {
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                  __builtin_memcpy(&dot[r][c][e], db + (at + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T)),
+                                   sizeof(T));
+              }
+            }
+          }
+        }
 #pragma unroll
         for (int r = 0; r < RT; ++r) {
           const v2f gi = get<v2f>(lds + oG + (at * 8 * C + 8 * lr) + 8 * 16 * r);
           const float e = __builtin_amdgcn_exp2f(gi[0] + gi[1]) * p.read;
 #pragma unroll
           for (int c = 0; c < CT; ++c) O[r][c] *= e;
+          if (MODE == kGrad && p.dot) {   // columns behind dw: O is 0
+            float sum = 0.f;
+#pragma unroll
+            for (int c = 0; c < CT; ++c)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) sum = fmaf(O[r][c][e], to_f32(dot[r][c][e]), sum);
+            // over the lanes that share the row
+            const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+            sum = __uint_as_float(a[0]) + __uint_as_float(a[1]);
+            const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
+            sum = __uint_as_float(b[0]) + __uint_as_float(b[1]);
+            const int i = 16 * r + lr;
+            if (g == 0 && i < n && !(p.rev && i == 0)) part[p.rev ? n - 1 - i : i] = sum;
+          }
         }
       }
     }
@@ -509,40 +590,11 @@ void linear_pass_kernel(const LinPass p) {
       const unsigned tid = thread();
         const int lr = tid & 15, lg = (tid & 63) >> 4;
       // rows of out of this chunk: base (uniform) and offsets of 32 bits
-      const long tok0 = it.start + c0;
       const unsigned wide = MODE == kGrad && p.out_f32 ? 4 : sizeof(T);
       unsigned char* ob = (unsigned char*)p.out + (tok0 * ldo + (long)h * p.dw) * wide;
-      const Bytes db = MODE == kGrad
-          ? (Bytes)p.dot + (tok0 * p.lddot + (long)(h / p.gdot) * p.dw) * (long)sizeof(T) : nullptr;
-      float* to = MODE == kGrad && p.dot
-          ? p.dot_out + ((size_t)(slice * WAVES + w) * p.Hv + h) * p.tokens + tok0 : nullptr;
-      // all rows' loads on their way together (the zeros: or the registers of an array that is filled
-      // under a condition live through the whole loop, and are spilled)
-      T dot[MODE == kGrad ? RT : 1][CT][4] = {};
-      if (MODE == kGrad && p.dot) {
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const int i = 16 * r + lr < n ? 16 * r + lr : n - 1;
-          const unsigned at = (unsigned)(p.rev ? n - 1 - i : i) * ((unsigned)p.lddot * (unsigned)sizeof(T));
-#pragma unroll
-          for (int c = 0; c < CT; ++c) {
-            const int col = col0 + 16 * c + 4 * lg;
-            if constexpr (WHOLE) {
-              __builtin_memcpy(dot[r][c], db + (at + (col < p.dw ? col : 0) * (unsigned)sizeof(T)), sizeof(dot[r][c]));
-            } else {
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                __builtin_memcpy(&dot[r][c][e], db + (at + (col + e < p.dw ? col + e : 0) * (unsigned)sizeof(T)),
-                                 sizeof(T));
-            }
-          }
-        }
-        asm volatile("" ::: "memory");   // not put behind the conditions below
-      }
 #pragma unroll
       for (int r = 0; r < RT; ++r) {
         const int i = 16 * r + lr, row = p.rev ? n - 1 - i : i;
-        float sum = 0.f;
         if (i < n) {
 #pragma unroll
           for (int c = 0; c < CT; ++c) {
@@ -558,11 +610,6 @@ void linear_pass_kernel(const LinPass p) {
                 for (int e = 0; e < 4; ++e) t[e] = from_f32<T>(o[e]);
                 __builtin_memcpy(q, t + e0, sizeof(T) * m);
               }
-              if (MODE == kGrad && p.dot) {
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                  if (e < m) sum = fmaf(o[e0 + e], to_f32(dot[r][c][e0 + e]), sum);
-              }
             };
             if (col + 4 <= p.dw) {
               write(0, 4);
@@ -572,13 +619,6 @@ void linear_pass_kernel(const LinPass p) {
               if (col + 2 < p.dw) write(2, 1);
             }
           }
-        }
-        if (MODE == kGrad && p.dot) {   // over the lanes that share the row
-          const auto a = __builtin_amdgcn_permlane16_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
-          sum = __uint_as_float(a[0]) + __uint_as_float(a[1]);
-          const auto b = __builtin_amdgcn_permlane32_swap(__float_as_uint(sum), __float_as_uint(sum), false, false);
-          sum = __uint_as_float(b[0]) + __uint_as_float(b[1]);
-          if (lg == 0 && i < n) to[row] = sum;
         }
       }
     }
@@ -591,22 +631,6 @@ void linear_pass_kernel(const LinPass p) {
   } else {
     if (p.last && (it.of == 0 || (p.rev ? it.m == 0 : it.m == it.of - 1)))
       store_state(p.last + ((size_t)it.s * p.Hv + h) * sz, col0, p.dx, p.dw, rs, cs, S);
-    if (MODE == kOut && p.edge_out) {
-      const float* with = it.of ? p.edge_slots + ((size_t)it.slot * p.Hv + h) * sz
-                                : p.edge_first + ((size_t)it.s * p.Hv + h) * sz;
-      v4f other[TILES][CT];
-      load_state(with, col0, p.dx, p.dw, rs, cs, other);
-      float sum = 0.f;
-#pragma unroll
-      for (int t = 0; t < TILES; ++t)
-#pragma unroll
-        for (int c = 0; c < CT; ++c)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) sum = fmaf(S[t][c][e], other[t][c][e], sum);
-      sum = sum64(sum);
-      const size_t item = it.of ? (size_t)p.sequences + it.slot : (size_t)it.s;
-      if (lane == 0) p.edge_out[(item * p.Hv + h) * kDotParts + slice * WAVES + w] = sum;
-    }
   }
 }
 
@@ -620,7 +644,7 @@ void linear_shape(int dx, int dw, F f) {
   constexpr integral_constant<int, 8> eight;
   constexpr integral_constant<int, 16> cw;
   constexpr integral_constant<int, 64> c64;
-  constexpr integral_constant<int, PARTS == 1 ? 64 : 32> c256;
+  constexpr integral_constant<int, linear_chunk(256, PARTS)> c256;
   const bool wide = dw > 64;
   if (dx <= 64) {
     constexpr integral_constant<int, 64> d;
