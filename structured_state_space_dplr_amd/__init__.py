@@ -175,16 +175,19 @@ class S4DPLRPreconditionError(ValueError):
         self.where, self.what = where, what
 
 
-# os.environ's own store where it has one (bytes): a look without encoding the name and raising and
-# catching a KeyError, 0.4 us of a call's 9
-_environ = getattr(os.environ, "_data", None)
+# os.environ's own store where it is the interpreter's (names and values in bytes): a look without encoding
+# the name and raising and catching a KeyError, 0.4 us of a call's 9.  A mapping that was put in its place
+# is asked as any other.
+_Environ = type(os.environ)
 _VALIDATE_KEY = os.fsencode(VALIDATE_ENV)
 
 
 def validation_enabled() -> bool:
-    if type(_environ) is dict:
-        return _environ.get(_VALIDATE_KEY) == b"1"
-    return os.environ.get(VALIDATE_ENV, "") == "1"
+    env = os.environ
+    data = getattr(env, "_data", None) if type(env) is _Environ else None
+    if type(data) is dict:
+        return data.get(_VALIDATE_KEY) == b"1"
+    return env.get(VALIDATE_ENV, "") == "1"
 
 
 def _host(t):
