@@ -1026,7 +1026,11 @@ def matmul_fp8(a, a_scales, b, b_scales, out, stream=None) -> None:
 
     a_scales: [M, ceil(K / 128)] float8_e8m0fnu; b_scales: [N, ceil(K / 128)], or
     [ceil(N / 128), ceil(K / 128)] for 128 x 128 blocks.  out: float32, bfloat16 or
-    float16.  a, b and out may be column ranges of wider matrices."""
+    float16.  a, b and out may be column ranges of wider matrices.
+
+    Sums of a float32 output are float32.  For 16-bit outputs the matrix instruction adds up each
+    128 products with fewer bits, off by up to about 2^-13 of the sum of their magnitudes: where sums
+    cancel, take a float32 output and round it."""
     if not isinstance(out, torch.Tensor):
         raise TypeError("out: expected a torch.Tensor")
     if out.dtype not in _DTYPES:

@@ -141,7 +141,8 @@ s4dplr_status s4dplr_matmul_fp8(const void* a, long lda, const void* a_scales, c
     if (n < 0 || n >= kMostSize) return S4DPLR_ERR_SHAPE;
   if (lda < K || ldb < K || ldo < N || lda >= kMostSize || ldb >= kMostSize || ldo >= kMostSize)
     return S4DPLR_ERR_SHAPE;
-  // a launch counts its threads in 32 bits: tiles of 64 x 128 at 256 threads
+  // a launch counts its threads in 32 bits: tiles of 128 x 128 have 256 threads each and are no more than these,
+  // smaller and larger ones are fewer (matmul.hip)
   if (((size_t)M + 63) / 64 * groups(N) >= (1u << 23)) return S4DPLR_ERR_SHAPE;
   if (M == 0 || N == 0) return S4DPLR_OK;
   if (!out || (K > 0 && (!a || !a_scales || !b || !b_scales))) return S4DPLR_ERR_NULL;

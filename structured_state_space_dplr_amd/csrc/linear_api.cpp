@@ -19,7 +19,8 @@ typedef s4dplr_linear_attention_plan Plan;
 // again, and read.  Forward, 16 heads of 128 x 128 in bf16 (us; chunks times heads, then the
 // chunks of a segment with the time): 256: 1 29.2, 2 31.3, 4 42.8; 512: 1 44.1, 2 37.9, 4 46.1;
 // 1024: 2 59.1, 4 52.9, 8 72.6; 2048: 2 104, 4 80.3, 8 80.1; 4096: 4 151, 8 125, 16 135; 16384 in 64
-// sequences: 8 452, 16 (whole sequences) 329.  Training step of 4096: 4 595, 8 509, 16 774.
+// sequences: 8 452, 16 (whole sequences) 329.  Training step of 4096: 4 747, 8 687, 16 938; of 2048: 4
+// 374, 8 389, 16 592.
 int segment_of(const Plan& p) {
   const long work = (p.tokens + kLinChunk - 1) / kLinChunk * p.Hv * ((p.dv + 127) / 128);
   const long n = (work + 511) / 512;
